@@ -11,6 +11,12 @@ With the environment variable Q8_LIBRARY=timeline set before the first
 import, the package loads the timeline build, libq8narrow_timeline.so, instead
 (same entry points and results, plus ``q8_timeline_set`` of
 ``include/q8timeline.h``: per-wave real-time counter records for profiling).
+
+The attention side (``include/q8kv4.h``: rotary positions, the paged 4-bit
+cache, its append, read-back and attention) takes two handles that a program
+makes once: ``Rotary`` (a plan, from ``rotary_plan``) and ``KV4Cache``.  Their
+tensors are checked when they are made, so that a step's calls check only
+what changes from step to step.
 """
 
 from __future__ import annotations
@@ -72,6 +78,32 @@ _SIGNATURES = {
     "q8_device_supported": ([], _i32),
     "q8_status_str": ([_i32], ctypes.c_char_p),
 }
+
+
+class _RotaryPlan(ctypes.Structure):
+    _fields_ = [("inv_freq", _vp), ("amplitude", ctypes.c_double), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
+
+
+class _KV4Cache(ctypes.Structure):
+    _fields_ = [("pages", _vp), ("block_table", _vp), ("n_pages", _i64),
+                ("n_slots", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("page_tokens", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32)]
+
+
+# include/q8kv4.h.
+_f64, _f32, _size = ctypes.c_double, ctypes.c_float, ctypes.c_size_t
+_KV4_SIGNATURES = {
+    "q8_rotary_frequencies": ([_i32, _f64, _i32, _f64, _f64, _f64, _f64, _vp, _vp], _i32),
+    "q8_rotary": ([_vp, _i64, _vp, _i64, _i32, _vp, _i32, _i32, _vp, _vp], _i32),
+    "q8_kv4_page_bytes": ([_i32, _i32, _i32], _size),
+    "q8_kv4_append": ([_vp, _vp, _vp, _vp, _i64, _i32, _vp, _vp, _vp, _i32, _vp, _i64, _vp], _i32),
+    "q8_kv4_read": ([_vp, _vp, _vp, _i32, _vp, _vp, _vp], _i32),
+    "q8_kv4_attend_workspace_bytes": ([_vp, _i32, _i32, _i32], _size),
+    "q8_kv4_attend": ([_vp, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _f32, _i32, _vp, _i64, _vp,
+                       _size, _vp], _i32),
+}
 # The timeline build's own symbol (include/q8timeline.h).
 _TIMELINE_SIGNATURES = {
     "q8_timeline_set": ([_vp, _i64], _i32),
@@ -91,7 +123,7 @@ def _load_library():
             f"{LIB_PATH} is not built; run `python -c 'import __graft_entry__ as g; g.build()'` "
             "or `python quantized_weight_streaming_q8_amd/build.py` (hipcc, gfx950)")
     lib = ctypes.CDLL(LIB_PATH)
-    sigs = dict(_SIGNATURES, **(_TIMELINE_SIGNATURES if TIMELINE else {}))
+    sigs = dict(_SIGNATURES, **_KV4_SIGNATURES, **(_TIMELINE_SIGNATURES if TIMELINE else {}))
     for name, (args, res) in sigs.items():
         fn = getattr(lib, name)
         fn.argtypes = args
@@ -364,6 +396,190 @@ def q8_timeline_set(records, max_waves: int) -> None:
                       "first import to load the timeline build)")
     (r,) = _dev(_arg(records, "records", (torch.int64,), 8 * Q8_STAMP_WORDS * max(max_waves, 0)))
     _check(_lib.q8_timeline_set(r, max_waves), "q8_timeline_set")
+
+
+# ------------------------------------- the attention side (include/q8kv4.h)
+
+Q8_ROTARY_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "bands": 3, "yarn": 4}
+Q8_KV4_MAX_HEAD_DIM = 256
+Q8_KV4_MAX_PAGE = 4096
+Q8_KV4_MAX_TOKENS = 64
+Q8_KV4_MAX_SEQS = 4096
+_F64 = (torch.float64,)
+
+
+class Rotary:
+    """A rotary plan: the frequencies of a model's position rotation on the
+    device (float64, one for each pair), how values pair up, and the amplitude
+    of the rotated values."""
+
+    def __init__(self, inv_freq: torch.Tensor, interleaved: bool = False, amplitude: float = 1.0):
+        (addr,) = _dev(_arg(inv_freq, "inv_freq", _F64, 8))
+        self.inv_freq = inv_freq
+        self.rot_dim = 2 * inv_freq.numel()
+        self.interleaved = bool(interleaved)
+        self.amplitude = float(amplitude)
+        self.device = inv_freq.device
+        self._c = _RotaryPlan(addr, self.amplitude, self.rot_dim, int(self.interleaved))
+        self._ref = ctypes.addressof(self._c)
+
+
+def rotary_frequencies(rot_dim: int, base: float = 1e4, scaling: str = "none",
+                       factor: float = 1.0, original_context: float = 0.0,
+                       low: float = 1.0, high: float | None = None):
+    """(frequencies float64 on the host, amplitude) of q8_rotary_frequencies.
+    ``low`` and ``high`` bound the ramp of "bands" (default 1..4 turns) and
+    "yarn" (1..32)."""
+    if scaling not in Q8_ROTARY_SCALINGS:
+        raise ValueError(f"scaling: expected one of {sorted(Q8_ROTARY_SCALINGS)}, got {scaling!r}")
+    if high is None:
+        high = 32.0 if scaling == "yarn" else 4.0
+    out = torch.empty(max(rot_dim, 2) // 2, dtype=torch.float64)
+    amplitude = ctypes.c_double()
+    _check(_lib.q8_rotary_frequencies(rot_dim, base, Q8_ROTARY_SCALINGS[scaling], factor,
+                                      original_context, low, high, out.data_ptr(),
+                                      ctypes.addressof(amplitude)), "q8_rotary_frequencies")
+    return out, amplitude.value
+
+
+def rotary_plan(rot_dim: int, base: float = 1e4, interleaved: bool = False, scaling: str = "none",
+                factor: float = 1.0, original_context: float = 0.0, low: float = 1.0,
+                high: float | None = None, device="cuda") -> Rotary:
+    """A rotary plan on the device (rotary_frequencies for the scalings)."""
+    f, amplitude = rotary_frequencies(rot_dim, base, scaling, factor, original_context, low, high)
+    return Rotary(f.to(device), interleaved, amplitude)
+
+
+class KV4Cache:
+    """A paged 4-bit cache: ``n_pages`` pages of ``page_tokens`` positions for
+    ``n_kv_heads`` heads of ``head_dim``, and the block table (int32
+    [n_slots][max_pages], kept and read by every call) that names the pages of
+    each slot.  ``pages`` is allocated unless given (uint8, any contents)."""
+
+    def __init__(self, n_pages: int, page_tokens: int, n_kv_heads: int, head_dim: int,
+                 block_table: torch.Tensor, pages: torch.Tensor | None = None):
+        nbytes = q8_kv4_page_bytes(n_kv_heads, head_dim, page_tokens)
+        if nbytes == 0 or n_pages < 1:
+            raise ValueError(f"invalid cache shape: {n_pages} pages of {page_tokens} positions, "
+                             f"{n_kv_heads} heads of {head_dim}")
+        _arg(block_table, "block_table", _I32, 4)
+        if block_table.dim() != 2:
+            raise ValueError(f"block_table: expected [n_slots][max_pages], got {list(block_table.shape)}")
+        if pages is None:
+            pages = torch.empty(n_pages * nbytes, dtype=torch.uint8, device=block_table.device)
+        addr, table = _dev(_arg(pages, "pages", _ANY, n_pages * nbytes), ("block_table", block_table))
+        self.pages, self.block_table = pages, block_table
+        self.n_pages, self.page_tokens = n_pages, page_tokens
+        self.n_kv_heads, self.head_dim = n_kv_heads, head_dim
+        self.n_slots, self.max_pages = block_table.shape
+        self.page_bytes = nbytes
+        self.device = block_table.device
+        self._c = _KV4Cache(addr, table, n_pages, self.n_slots, self.max_pages, page_tokens,
+                            n_kv_heads, head_dim)
+        self._ref = ctypes.addressof(self._c)
+
+
+def _handle(h, kind, name: str):
+    """Address of a handle's C struct, its device checked."""
+    if not isinstance(h, kind):
+        raise TypeError(f"{name}: expected a {kind.__name__}, got {type(h).__name__}")
+    if h.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {h.device}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return h._ref
+
+
+def _span(rows: int, stride: int, width: int) -> int:
+    """Bytes of `rows` fp32 rows of `width` values, `stride` apart."""
+    return _n((rows - 1) * stride + width, 4) if rows > 0 else 0
+
+
+def q8_rotary(X, Y, n_rows: int, x_stride: int, pos, n_heads: int, head_dim: int,
+              rotary: Rotary, y_stride: int | None = None, stream=None) -> None:
+    """Y (default stride n_heads * head_dim) = X rotated at pos; X itself may
+    be Y, with y_stride = x_stride."""
+    w = n_heads * head_dim
+    if y_stride is None:
+        y_stride = w
+    x, y, p = _dev(_arg(X, "X", _F32, _span(n_rows, x_stride, w)),
+                   _arg(Y, "Y", _F32, _span(n_rows, y_stride, w)), _arg(pos, "pos", _I32, _n(n_rows, 4)))
+    _check(_lib.q8_rotary(x, x_stride, y, y_stride, n_rows, p, n_heads, head_dim,
+                          _handle(rotary, Rotary, "rotary"), _stream(stream)), "q8_rotary")
+
+
+def q8_kv4_page_bytes(n_kv_heads: int, head_dim: int, page_tokens: int) -> int:
+    return int(_lib.q8_kv4_page_bytes(n_kv_heads, head_dim, page_tokens))
+
+
+def q8_kv4_append(cache: KV4Cache, QKV, n_rows: int, row_stride: int, batch_index, pos,
+                  rotary: Rotary | None = None, n_q_heads: int = 0, Q=None,
+                  q_stride: int | None = None, stream=None) -> None:
+    """Append the rows of a QKV projection: QKV fp32 [n_rows][row_stride],
+    n_q_heads query heads, then n_kv_heads key heads, then as many value
+    heads.  With a Q, the rotated queries go there (rows q_stride apart,
+    default n_q_heads * head_dim); without one the queries are skipped."""
+    d, kv = cache.head_dim, cache.n_kv_heads
+    wq = n_q_heads * d
+    width = wq + 2 * kv * d
+    if row_stride < width:
+        raise ValueError(f"row_stride: {row_stride} is less than the {width} values of a row")
+    rows, bi, p = _dev(_arg(QKV, "QKV", _F32, _span(n_rows, row_stride, width)),
+                       _arg(batch_index, "batch_index", _I32, _n(n_rows, 4)),
+                       _arg(pos, "pos", _I32, _n(n_rows, 4)))
+    out = None
+    if Q is not None:
+        if q_stride is None:
+            q_stride = wq
+        (out,) = _dev(_arg(Q, "Q", _F32, _span(n_rows, q_stride, wq)))
+    _check(_lib.q8_kv4_append(_handle(cache, KV4Cache, "cache"), rows, rows and rows + 4 * wq,
+                              rows and rows + 4 * (wq + kv * d), row_stride, n_rows, bi, p,
+                              None if rotary is None else _handle(rotary, Rotary, "rotary"),
+                              0 if Q is None else n_q_heads, out, q_stride or 0, _stream(stream)),
+           "q8_kv4_append")
+
+
+def q8_kv4_read(cache: KV4Cache, batch_index, pos, n_rows: int, K, V, stream=None) -> None:
+    need = _n(n_rows * cache.n_kv_heads * cache.head_dim, 4)
+    bi, p, k, v = _dev(_arg(batch_index, "batch_index", _I32, _n(n_rows, 4)),
+                       _arg(pos, "pos", _I32, _n(n_rows, 4)),
+                       _arg(K, "K", _F32, need), _arg(V, "V", _F32, need))
+    _check(_lib.q8_kv4_read(_handle(cache, KV4Cache, "cache"), bi, p, n_rows, k, v, _stream(stream)),
+           "q8_kv4_read")
+
+
+def q8_kv4_attend_workspace_bytes(cache: KV4Cache, n_seq: int, tokens_per_seq: int,
+                                  n_q_heads: int) -> int:
+    return int(_lib.q8_kv4_attend_workspace_bytes(cache._ref, n_seq, tokens_per_seq, n_q_heads))
+
+
+def q8_kv4_attend(cache: KV4Cache, Q, n_seq: int, tokens_per_seq: int, n_q_heads: int,
+                  batch_index, pos, O, workspace, scale: float | None = None, window: int = 0,
+                  q_stride: int | None = None, o_stride: int | None = None,
+                  workspace_bytes: int | None = None, stream=None) -> None:
+    """Attention of n_seq * tokens_per_seq query rows over the cache.  scale
+    defaults to head_dim ** -0.5, the strides to n_q_heads * head_dim."""
+    w, rows = n_q_heads * cache.head_dim, n_seq * tokens_per_seq
+    q_stride = w if q_stride is None else q_stride
+    o_stride = w if o_stride is None else o_stride
+    q, bi, p, o, ws = _dev(_arg(Q, "Q", _F32, _span(rows, q_stride, w)),
+                           _arg(batch_index, "batch_index", _I32, _n(rows, 4)),
+                           _arg(pos, "pos", _I32, _n(rows, 4)),
+                           _arg(O, "O", _F32, _span(rows, o_stride, w)),
+                           _arg(workspace, "workspace"))
+    _check(_lib.q8_kv4_attend(_handle(cache, KV4Cache, "cache"), q, q_stride, n_seq, tokens_per_seq,
+                              n_q_heads, bi, p, cache.head_dim ** -0.5 if scale is None else scale,
+                              window, o, o_stride, ws, _ws_bytes(workspace, workspace_bytes),
+                              _stream(stream)), "q8_kv4_attend")
+
+
+def kv4_attend_workspace(cache: KV4Cache, n_seq: int, tokens_per_seq: int,
+                         n_q_heads: int) -> torch.Tensor:
+    """A zero-filled workspace for q8_kv4_attend."""
+    nbytes = q8_kv4_attend_workspace_bytes(cache, n_seq, tokens_per_seq, n_q_heads)
+    if nbytes == 0:
+        raise ValueError(f"invalid attention shape: {n_seq} sequences of {tokens_per_seq} tokens, "
+                         f"{n_q_heads} query heads over {cache.n_kv_heads}")
+    return torch.zeros(nbytes, dtype=torch.uint8, device=cache.device)
 
 
 # ------------------------------------------------- torch allocation helpers

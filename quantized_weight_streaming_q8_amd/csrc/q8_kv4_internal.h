@@ -1,0 +1,128 @@
+// q8_kv4_internal.h -- the 4-bit cache's page layout and the launchers of
+// the rotary, append, read and attention kernels.
+//
+// Page layout (private).  Per key/value head, one after the other (T
+// positions a page, D = 32 NB values a head):
+//
+//   K codes, T * D/2 bytes, in tiles of 16 positions.  A tile is the A operand
+//     of v_mfma_f32_16x16x32_bf16 for NB blocks: lane (r = position & 15,
+//     g = 0..3) takes values 8g .. 8g+7 of each block, 4 bytes, low nibble
+//     first.  The blocks of a lane lie side by side, four to a 16-byte load:
+//     byte  q*1024 + (16g + r)*W + 4*(b & 3)   of the tile, q = b / 4 and W =
+//     4 * (blocks of this quad, 4 but for the last).
+//   V codes, T * D/2 bytes, in groups of 32 positions.  A group is the A
+//     operand (V transposed) of NB pairs of the same instruction, with the
+//     32 positions along k: lane (c = 0..15, g) takes values 2c and 2c+1 (the
+//     two nibbles of a byte) of each block at 8 positions, byte j = 0..7 for
+//     position 16*(j >> 2) + 4g + (j & 3): the order in which the 16x16 tiles
+//     of scores lie in the lanes, so that they are the B operand as they
+//     stand.  Two blocks to a 16-byte load:
+//     byte  p*1024 + (16g + c)*W + 8*(b & 1) + j,  p = b / 2, W = 8 * (blocks
+//     of this pair, 2 but for the last).
+//   K scales, T * SP bytes, SP = NB rounded up to a power of two: byte b of a
+//     position's SP bytes.
+//   V scales, T * NB bytes, in groups of 32 positions: byte g*8NB + 8b + j,
+//     j as above.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "q8kv4.h"
+
+namespace q8 {
+
+constexpr int kKvTile = 32;       // positions of one step of the attention
+constexpr int kScaleBias = 127;   // E8M0
+constexpr int kNanByte = 255;
+
+__host__ __device__ constexpr int scale_pitch(int nb) {
+    return nb <= 1 ? 1 : nb <= 2 ? 2 : nb <= 4 ? 4 : 8;
+}
+
+// Bytes of one head's part of a page, and the starts of its four regions.
+struct HeadLayout {
+    int64_t v, ks, vs, bytes;
+};
+__host__ __device__ constexpr HeadLayout head_layout(int nb, int page_tokens) {
+    const int64_t codes = (int64_t)page_tokens * nb * 16;
+    const int64_t ks = (int64_t)page_tokens * scale_pitch(nb);
+    // rounded up, so that every head's codes start on 16 bytes
+    const int64_t all = 2 * codes + ks + (int64_t)page_tokens * nb;
+    return {codes, 2 * codes, 2 * codes + ks, (all + 15) / 16 * 16};
+}
+
+// Offset, in a head's K codes, of the 4 bytes of segment g (8 values) of
+// block b at position t of the page.
+__host__ __device__ constexpr int64_t k_code_offset(int nb, int t, int b, int g) {
+    const int q = b >> 2, in_quad = nb - 4 * q < 4 ? nb - 4 * q : 4;
+    return (int64_t)(t >> 4) * (256 * nb) + q * 1024 + (g * 16 + (t & 15)) * (4 * in_quad) + 4 * (b & 3);
+}
+// j (byte of a lane's 8) and g (lane quarter) of a position in its group of 32
+__host__ __device__ constexpr int v_byte(int t) { return ((t >> 4 & 1) << 2) | (t & 3); }
+__host__ __device__ constexpr int v_quarter(int t) { return t >> 2 & 3; }
+// Offset, in a head's V codes, of the byte with values 2c and 2c+1 of block b.
+__host__ __device__ constexpr int64_t v_code_offset(int nb, int t, int b, int c) {
+    const int p = b >> 1, in_pair = nb - 2 * p < 2 ? nb - 2 * p : 2;
+    return (int64_t)(t >> 5) * (512 * nb) + p * 1024 + (v_quarter(t) * 16 + c) * (8 * in_pair) +
+           8 * (b & 1) + v_byte(t);
+}
+__host__ __device__ constexpr int64_t k_scale_offset(int nb, int t, int b) {
+    return (int64_t)t * scale_pitch(nb) + b;
+}
+__host__ __device__ constexpr int64_t v_scale_offset(int nb, int t, int b) {
+    return (int64_t)(t >> 5) * (32 * nb) + v_quarter(t) * (8 * nb) + 8 * b + v_byte(t);
+}
+
+// The cache as the kernels take it.
+struct KvView {
+    uint8_t* pages;
+    const int32_t* table;
+    int64_t n_pages, page_bytes, head_bytes;
+    int32_t n_slots, max_pages, page_tokens, n_kv, nb;
+};
+
+// Page of position p of slot s, or -1 where slot, position or page lies
+// outside the cache.
+__device__ inline int64_t kv_page(const KvView& c, int s, int p) {
+    if (s < 0 || s >= c.n_slots || p < 0 || p >= c.max_pages * c.page_tokens) return -1;
+    const int64_t pg = c.table[(int64_t)s * c.max_pages + p / c.page_tokens];
+    return pg >= 0 && pg < c.n_pages ? pg : -1;
+}
+
+struct RotaryView {
+    const double* inv_freq;  // null: no rotation
+    double amplitude;
+    int half;                // rot_dim / 2
+    int interleaved;
+};
+
+hipError_t launch_rotary(const float* X, int64_t x_stride, float* Y, int64_t y_stride, int n_rows,
+                         const int32_t* pos, int n_heads, int head_dim, const RotaryView& r,
+                         hipStream_t st);
+hipError_t launch_kv4_append(const KvView& c, const float* Q, const float* K, const float* V,
+                             int64_t row_stride, int n_rows, const int32_t* batch_index,
+                             const int32_t* pos, const RotaryView& r, int n_q_heads, float* Q_out,
+                             int64_t q_out_stride, hipStream_t st);
+hipError_t launch_kv4_read(const KvView& c, const int32_t* batch_index, const int32_t* pos,
+                           int n_rows, float* K, float* V, hipStream_t st);
+
+// The attention call as planned on the host.
+struct AttendArgs {
+    KvView c;
+    const float* Q;
+    float* O;
+    int64_t q_stride, o_stride;
+    const int32_t* batch_index;
+    const int32_t* pos;
+    int32_t n_seq, tokens, group, window;
+    float scale_log2;  // softmax scale * log2(e)
+    uint8_t* workspace;
+};
+size_t kv4_attend_workspace(int n_kv, int nb, int64_t capacity, int n_seq, int tokens, int group);
+// Row blocks of all sequences and heads (the workspace has a counter for each).
+int64_t kv4_attend_units(int n_kv, int nb, int n_seq, int tokens, int group);
+constexpr int64_t kMaxUnits = int64_t(1) << 18;
+hipError_t launch_kv4_attend(const AttendArgs& a, hipStream_t st);
+
+}  // namespace q8

@@ -1,0 +1,327 @@
+// q8_kv4_rows.hip -- rotary positions, the append to the 4-bit cache and its
+// read-back: the kernels that pass once over a step's rows.
+//
+// Rotary embedding: pair (a, b) of a head turns by theta = pos * inv_freq[i],
+// y_a = A (a cos - b sin), y_b = A (a sin + b cos).  Sines and cosines depend on
+// (row, i) only, so a workgroup belongs to one row, computes the row's rot/2
+// of them once (double, into LDS) and applies them to its share of the row's
+// heads.  Everything else is one read and one write of each value: the
+// kernels are bound by memory, and for a step's few rows by the latency of
+// one load, one sincos and one store.
+//
+// Rotation alone: a thread takes V pairs at a time and writes both halves, so
+// in place is safe.  Append: a thread takes 4 consecutive values of a key or
+// value head; 8 lanes hold a block of 32 and agree on its scale with three
+// lane exchanges; a thread reads its rotation partners itself.
+
+#include "q8_kv4_internal.h"
+
+#include <math.h>
+
+namespace q8 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxHalf = 512;  // rot_dim <= 1024
+
+// 4-byte aligned vector accesses (rows start at any value)
+typedef float f4u __attribute__((ext_vector_type(4), aligned(4)));
+typedef float f2 __attribute__((ext_vector_type(2)));
+
+// The row's cosines and sines, times the amplitude.
+__device__ inline void fill_angles(double2* cs, const RotaryView& r, int pos) {
+    for (int i = threadIdx.x; i < r.half; i += kThreads) {
+        double s, c;
+        sincos((double)pos * r.inv_freq[i], &s, &c);
+        cs[i] = make_double2(c * r.amplitude, s * r.amplitude);
+    }
+    __syncthreads();
+}
+
+__device__ inline void turn(const double2 cs, float& a, float& b) {
+    const double x = a, y = b;
+    a = (float)(x * cs.x - y * cs.y);
+    b = (float)(x * cs.y + y * cs.x);
+}
+
+template <int V>
+__device__ inline void load_v(const float* p, float (&v)[V]) {
+    if constexpr (V == 4) {
+        const f4u t = *reinterpret_cast<const f4u*>(p);
+        v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
+    } else {
+        for (int i = 0; i < V; ++i) v[i] = p[i];
+    }
+}
+template <int V>
+__device__ inline void store_v(float* p, const float (&v)[V]) {
+    if constexpr (V == 4) {
+        *reinterpret_cast<f4u*>(p) = f4u{v[0], v[1], v[2], v[3]};
+    } else {
+        for (int i = 0; i < V; ++i) p[i] = v[i];
+    }
+}
+
+// Units [u0, u1) of a row's heads: in each head half/V pair units, then
+// (head_dim - 2 half)/V units of the part that passes unchanged.
+template <int V>
+__device__ inline void rotate_units(const float* x, float* y, int head_dim, const RotaryView& r,
+                                    const double2* cs, int u0, int u1) {
+    const int pairs = r.half / V, per_head = (head_dim - r.half) / V;
+    for (int u = u0 + (int)threadIdx.x; u < u1; u += kThreads) {
+        const int h = u / per_head, k = u - h * per_head;
+        const int64_t base = (int64_t)h * head_dim;
+        if (k >= pairs) {
+            const int64_t o = base + 2 * r.half + (int64_t)(k - pairs) * V;
+            float t[V];
+            load_v<V>(x + o, t);
+            store_v<V>(y + o, t);
+            continue;
+        }
+        const int i = k * V;
+        float a[V], b[V];
+        if (r.interleaved) {
+            load_v<V>(x + base + 2 * i, a);
+            load_v<V>(x + base + 2 * i + V, b);
+            if constexpr (V == 4) {  // a, b: four adjacent pairs as they stand
+                turn(cs[i], a[0], a[1]);
+                turn(cs[i + 1], a[2], a[3]);
+                turn(cs[i + 2], b[0], b[1]);
+                turn(cs[i + 3], b[2], b[3]);
+            } else {
+                turn(cs[i], a[0], b[0]);
+            }
+            store_v<V>(y + base + 2 * i, a);
+            store_v<V>(y + base + 2 * i + V, b);
+        } else {
+            load_v<V>(x + base + i, a);
+            load_v<V>(x + base + r.half + i, b);
+#pragma unroll
+            for (int j = 0; j < V; ++j) turn(cs[i + j], a[j], b[j]);
+            store_v<V>(y + base + i, a);
+            store_v<V>(y + base + r.half + i, b);
+        }
+    }
+}
+
+template <int V>
+__global__ void __launch_bounds__(kThreads)
+rotary_kernel(const float* x, int64_t x_stride, float* y, int64_t y_stride,
+              const int32_t* __restrict__ pos, int head_dim, RotaryView r, int units, int per_wg) {
+    __shared__ double2 cs[kMaxHalf];
+    const int64_t t = blockIdx.x;
+    fill_angles(cs, r, pos[t]);
+    const int u0 = (int)blockIdx.y * per_wg;
+    rotate_units<V>(x + t * x_stride, y + t * y_stride, head_dim, r, cs, u0, min(units, u0 + per_wg));
+}
+
+// ------------------------------------------------------------------ append
+
+// Scale byte of a block with largest magnitude a (finite): the exponent
+// floor(log2 a) - 2, one more for a mantissa above 1.75, held to -125..125.
+__device__ inline int scale_byte(float a) {
+    const uint32_t u = __float_as_uint(a);
+    const int e = (int)(u >> 23) - 127 - 2 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return min(max(e, -125), 125) + kScaleBias;
+}
+
+// A block's 4 values per lane over 8 consecutive lanes -> this lane's two
+// code bytes (low 16 bits) and the block's scale byte.
+__device__ inline uint32_t encode4(const float (&v)[4], int& scale) {
+    float a = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float m = fabsf(v[i]);
+        a = fmaxf(a, m <= __FLT_MAX__ ? m : __builtin_inff());
+    }
+#pragma unroll
+    for (int m = 1; m < 8; m <<= 1) a = fmaxf(a, __shfl_xor(a, m, 8));
+    if (!(a <= __FLT_MAX__)) {
+        scale = kNanByte;
+        return 0u;
+    }
+    scale = scale_byte(a);
+    // value / 2^(scale - 127), to the nearest code, ties to even, saturating
+    const float unit = __uint_as_float((uint32_t)scale << 23);
+    uint32_t q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, v[0], v[1], unit, 0);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[2], v[3], unit, 1);
+    return q & 0xffffu;
+}
+
+// One workgroup: one row and either a share of its query heads (blockIdx.y <
+// q_wgs) or a share of its keys and values.
+template <int V>
+__global__ void __launch_bounds__(kThreads)
+kv4_append_kernel(KvView c, const float* q, const float* __restrict__ k, const float* __restrict__ v,
+                  int64_t row_stride, const int32_t* __restrict__ batch_index,
+                  const int32_t* __restrict__ pos, RotaryView r, int q_units, int q_per_wg, int q_wgs,
+                  float* q_out, int64_t q_out_stride, int kv_per_wg) {
+    __shared__ double2 cs[Q8_KV4_MAX_HEAD_DIM / 2];
+    const int64_t t = blockIdx.x;
+    const int p = pos[t];
+    const int D = c.nb * 32;
+    if ((int)blockIdx.y < q_wgs) {
+        fill_angles(cs, r, p);
+        const int u0 = (int)blockIdx.y * q_per_wg;
+        rotate_units<V>(q + t * row_stride, q_out + t * q_out_stride, D, r, cs, u0,
+                        min(q_units, u0 + q_per_wg));
+        return;
+    }
+    const int64_t pg = kv_page(c, batch_index[t], p);
+    if (pg < 0) return;  // the whole workgroup
+    fill_angles(cs, r, p);
+    const int tok = p % c.page_tokens;
+    const HeadLayout hl = head_layout(c.nb, c.page_tokens);
+    const int per_head = D / 4, heads_units = c.n_kv * per_head;  // units: 4 values
+    const int u0 = ((int)blockIdx.y - q_wgs) * kv_per_wg, u1 = min(2 * heads_units, u0 + kv_per_wg);
+    // u1 - u0 is a multiple of 8: the 8 lanes of a block leave the loop together
+    for (int u = u0 + (int)threadIdx.x; u < u1; u += kThreads) {
+        const bool is_v = u >= heads_units;
+        const int uu = is_v ? u - heads_units : u;
+        const int h = uu / per_head, d = (uu - h * per_head) * 4;
+        const float* src = (is_v ? v : k) + t * row_stride + (int64_t)h * D;
+        float x[4];
+        load_v<4>(src + d, x);
+        if (!is_v && d < 2 * r.half) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int e = d + j;
+                if (e >= 2 * r.half) continue;
+                int i, mate;
+                bool first;
+                if (r.interleaved) {
+                    i = e >> 1;
+                    mate = e ^ 1;
+                    first = (e & 1) == 0;
+                } else {
+                    first = e < r.half;
+                    i = first ? e : e - r.half;
+                    mate = first ? e + r.half : i;
+                }
+                const double2 w = cs[i];
+                const double a = x[j], b = src[mate];
+                x[j] = first ? (float)(a * w.x - b * w.y) : (float)(b * w.y + a * w.x);
+            }
+        }
+        int s;
+        uint32_t code = encode4(x, s);
+        const int b = d >> 5, l = (d & 31) >> 2;  // block of the head, lane of the block
+        uint8_t* head = c.pages + pg * c.page_bytes + h * c.head_bytes;
+        if (is_v) {
+            uint8_t* o = head + hl.v + v_code_offset(c.nb, tok, b, 2 * l);
+            const int w = 8 * min(2, c.nb - (b & ~1));  // bytes from c to c + 1
+            o[0] = (uint8_t)code;
+            o[w] = (uint8_t)(code >> 8);
+            if (l == 0) head[hl.vs + v_scale_offset(c.nb, tok, b)] = (uint8_t)s;
+        } else {
+            code |= __shfl_down(code, 1, 8) << 16;
+            if ((l & 1) == 0)
+                *reinterpret_cast<uint32_t*>(head + k_code_offset(c.nb, tok, b, l >> 1)) = code;
+            if (l == 0) head[hl.ks + k_scale_offset(c.nb, tok, b)] = (uint8_t)s;
+        }
+    }
+}
+
+// -------------------------------------------------------------------- read
+
+// One thread per 4 values; blockIdx.y 0: keys, 1: values (either may be null).
+__global__ void __launch_bounds__(kThreads)
+kv4_read_kernel(KvView c, const int32_t* __restrict__ batch_index, const int32_t* __restrict__ pos,
+                int64_t units, float* k, float* v) {
+    const bool is_v = blockIdx.y == 1;
+    float* out = is_v ? v : k;
+    const int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (out == nullptr || u >= units) return;
+    const int D = c.nb * 32, per_row = c.n_kv * D / 4;
+    const int64_t t = u / per_row;
+    const int w = (int)(u - t * per_row), h = w / (D / 4), d = (w - h * (D / 4)) * 4;
+    const int p = pos[t];
+    const int64_t pg = kv_page(c, batch_index[t], p);
+    const float nan = __builtin_nanf("");
+    f4u y = {nan, nan, nan, nan};
+    if (pg >= 0) {
+        const HeadLayout hl = head_layout(c.nb, c.page_tokens);
+        const uint8_t* head = c.pages + pg * c.page_bytes + h * c.head_bytes;
+        const int tok = p % c.page_tokens, b = d >> 5, l = (d & 31) >> 2;
+        uint32_t code;
+        int s;
+        if (is_v) {
+            const uint8_t* o = head + hl.v + v_code_offset(c.nb, tok, b, 2 * l);
+            code = o[0] | (uint32_t)o[8 * min(2, c.nb - (b & ~1))] << 8;
+            s = head[hl.vs + v_scale_offset(c.nb, tok, b)];
+        } else {
+            code = *reinterpret_cast<const uint16_t*>(head + k_code_offset(c.nb, tok, b, l >> 1) +
+                                                      2 * (l & 1));
+            s = head[hl.ks + k_scale_offset(c.nb, tok, b)];
+        }
+        if (s != kNanByte) {
+            const float unit = __uint_as_float((uint32_t)s << 23);
+            const f2 lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, unit, 0);
+            const f2 hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, unit, 1);
+            y = f4u{lo.x, lo.y, hi.x, hi.y};
+        }
+    }
+    *reinterpret_cast<f4u*>(out + u * 4) = y;
+}
+
+// Share of a row's units that one workgroup takes: a pass of its threads for
+// few rows (spread over the most CUs), the whole row for many (the row's
+// angles are computed once).
+int units_per_wg(int units, int n_rows) {
+    const int passes = (units + kThreads - 1) / kThreads;
+    const int64_t wgs = (int64_t)n_rows * passes;
+    const int per = wgs <= 2048 ? 1 : passes;
+    return per * kThreads;
+}
+
+// Four pairs at a time when heads and the rotated part allow it.
+bool wide(int head_dim, const RotaryView& r) { return r.half % 4 == 0 && head_dim % 4 == 0; }
+
+}  // namespace
+
+hipError_t launch_rotary(const float* X, int64_t x_stride, float* Y, int64_t y_stride, int n_rows,
+                         const int32_t* pos, int n_heads, int head_dim, const RotaryView& r,
+                         hipStream_t st) {
+    const bool w = wide(head_dim, r);
+    const int units = n_heads * ((head_dim - r.half) / (w ? 4 : 1));
+    const int per = units_per_wg(units, n_rows);
+    const dim3 grid((unsigned)n_rows, (unsigned)((units + per - 1) / per));
+    if (w)
+        hipLaunchKernelGGL(rotary_kernel<4>, grid, dim3(kThreads), 0, st, X, x_stride, Y, y_stride,
+                           pos, head_dim, r, units, per);
+    else
+        hipLaunchKernelGGL(rotary_kernel<1>, grid, dim3(kThreads), 0, st, X, x_stride, Y, y_stride,
+                           pos, head_dim, r, units, per);
+    return hipGetLastError();
+}
+
+hipError_t launch_kv4_append(const KvView& c, const float* Q, const float* K, const float* V,
+                             int64_t row_stride, int n_rows, const int32_t* batch_index,
+                             const int32_t* pos, const RotaryView& r, int n_q_heads, float* Q_out,
+                             int64_t q_out_stride, hipStream_t st) {
+    const int D = c.nb * 32;
+    const bool w = wide(D, r);
+    const int q_units = n_q_heads * ((D - r.half) / (w ? 4 : 1));
+    const int q_per = units_per_wg(q_units, n_rows);
+    const int q_wgs = (q_units + q_per - 1) / q_per;
+    const int kv_units = 2 * c.n_kv * (D / 4);
+    const int kv_per = units_per_wg(kv_units, n_rows);
+    const dim3 grid((unsigned)n_rows, (unsigned)(q_wgs + (kv_units + kv_per - 1) / kv_per));
+    if (w)
+        hipLaunchKernelGGL(kv4_append_kernel<4>, grid, dim3(kThreads), 0, st, c, Q, K, V, row_stride,
+                           batch_index, pos, r, q_units, q_per, q_wgs, Q_out, q_out_stride, kv_per);
+    else
+        hipLaunchKernelGGL(kv4_append_kernel<1>, grid, dim3(kThreads), 0, st, c, Q, K, V, row_stride,
+                           batch_index, pos, r, q_units, q_per, q_wgs, Q_out, q_out_stride, kv_per);
+    return hipGetLastError();
+}
+
+hipError_t launch_kv4_read(const KvView& c, const int32_t* batch_index, const int32_t* pos,
+                           int n_rows, float* K, float* V, hipStream_t st) {
+    const int64_t units = (int64_t)n_rows * c.n_kv * c.nb * 8;
+    const dim3 grid((unsigned)((units + kThreads - 1) / kThreads), 2);
+    hipLaunchKernelGGL(kv4_read_kernel, grid, dim3(kThreads), 0, st, c, batch_index, pos, units, K, V);
+    return hipGetLastError();
+}
+
+}  // namespace q8
