@@ -574,12 +574,12 @@ def q8_kv4_attend(cache: KV4Cache, Q, n_seq: int, tokens_per_seq: int, n_q_heads
 
 def kv4_attend_workspace(cache: KV4Cache, n_seq: int, tokens_per_seq: int,
                          n_q_heads: int) -> torch.Tensor:
-    """A zero-filled workspace for q8_kv4_attend."""
+    """A workspace for q8_kv4_attend."""
     nbytes = q8_kv4_attend_workspace_bytes(cache, n_seq, tokens_per_seq, n_q_heads)
     if nbytes == 0:
         raise ValueError(f"invalid attention shape: {n_seq} sequences of {tokens_per_seq} tokens, "
                          f"{n_q_heads} query heads over {cache.n_kv_heads}")
-    return torch.zeros(nbytes, dtype=torch.uint8, device=cache.device)
+    return torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
 
 
 # ------------------------------------------------- torch allocation helpers

@@ -42,7 +42,7 @@ q8::KvView view(const q8_kv4_cache* c) {
     v.table = c->block_table;
     v.n_pages = c->n_pages;
     v.page_bytes = (int64_t)q8_kv4_page_bytes(c->n_kv_heads, c->head_dim, c->page_tokens);
-    v.head_bytes = q8::head_layout(nb, c->page_tokens).bytes;
+    v.head_bytes = q8::head_bytes(nb, c->page_tokens);
     v.n_slots = c->n_slots;
     v.max_pages = c->max_pages;
     v.page_tokens = c->page_tokens;
@@ -70,8 +70,8 @@ bool valid_attend_shape(const q8_kv4_cache* c, int n_seq, int tokens, int n_q_he
     return valid_cache_shape(c) && n_seq >= 1 && n_seq <= Q8_KV4_MAX_SEQS && tokens >= 1 &&
            tokens <= Q8_KV4_MAX_TOKENS && n_q_heads >= 1 && n_q_heads <= 8192 &&
            n_q_heads % c->n_kv_heads == 0 &&
-           q8::kv4_attend_units(c->n_kv_heads, c->head_dim / 32, n_seq, tokens,
-                                n_q_heads / c->n_kv_heads) <= q8::kMaxUnits;
+           (int64_t)n_seq * c->n_kv_heads * ((tokens * (n_q_heads / c->n_kv_heads) + 7) / 8) <=
+               q8::kMaxRowBlocks;
 }
 
 }  // namespace
@@ -124,7 +124,7 @@ size_t q8_kv4_page_bytes(int n_kv_heads, int head_dim, int page_tokens) {
     if (!valid_head_dim(head_dim) || n_kv_heads < 1 || n_kv_heads > 1024 || page_tokens < 32 ||
         page_tokens > Q8_KV4_MAX_PAGE || page_tokens % 32 != 0)
         return 0;
-    return (size_t)(n_kv_heads * q8::head_layout(head_dim / 32, page_tokens).bytes);
+    return (size_t)(n_kv_heads * q8::head_bytes(head_dim / 32, page_tokens));
 }
 
 q8_status q8_kv4_append(const q8_kv4_cache* cache, const float* Q, const float* K, const float* V,

@@ -1,14 +1,14 @@
 // q8_kv4_attend.hip -- attention over the 4-bit paged cache for gfx950.
 //
 // For a query row q of one sequence and head, with c = scale * log2(e):
-//     x_t = c q.k_t,  m = max x_t,  l = sum 2^(x_t - m),
-//     O = (1/l) sum 2^(x_t - m) v_t
+//     s_t = q.k_t,  m = max s_t,  l = sum 2^(c (s_t - m)),
+//     O = (1/l) sum 2^(c (s_t - m)) v_t
 // in one pass over the positions t, with m, l and O carried and rescaled when
 // the maximum grows.
 //
 // Exact products.  A code times its power-of-two scale has two significant
 // bits, so v_cvt_scalef32_pk_bf16_fp4 gives keys and values exactly in bf16.
-// q and the weights 2^(x - m) are fp32 numbers of 24 bits: three bf16 pieces
+// q and the weights 2^(c (s - m)) are fp32 numbers of 24 bits: three bf16 pieces
 // of 8 bits by truncation, exactly.  Three matrix instructions instead of one
 // then give fp32 products without error, added in fp32.  The matrix cores have
 // the room: at head_dim 128 a wave's 32 positions cost 48 of them, 768 cycles
@@ -27,10 +27,9 @@
 // Query rows are the tokens x grouped heads of one key/value head, 16 to a
 // column tile, RT tiles to a workgroup.  4 waves of a workgroup take its 32-position
 // steps in turn, each with its own m, l and O, joined in LDS at the end.
-// Sequences longer than kSplit positions are cut into splits (at most
-// kMaxSplits) that different workgroups take; the last to finish joins them
-// in order, through the workspace.  The cut depends on the sequence's own
-// positions only.
+// Longer sequences are cut into splits (splits_of: by the sequence's own
+// positions only) that different workgroups take; they leave their parts in
+// the workspace and a second, short launch joins them in order.
 //
 // Work items, (sequence, head, row block, split), are counted on the GPU, from
 // pos: the host need not know the lengths, a launch captured in a graph
@@ -41,22 +40,28 @@
 namespace q8 {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWaves = 4;
-constexpr int kSplit = 512;     // positions of a split, at least (but for the only one)
+// Waves of a workgroup (2 for the heads whose slots of 4 would pass 64 KB).
+__host__ __device__ constexpr int waves_of(int nb) { return nb <= 4 ? 4 : 2; }
 constexpr int kMaxSplits = 64;
-constexpr int kSplitTiles = kSplit / kKvTile;
-constexpr size_t kCounterBytes = kMaxUnits * sizeof(uint32_t);
+constexpr int kNoVmem = 0x0f70;  // s_waitcnt vmcnt(0), no other count
 
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef float f4u __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
-typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 
+// Splits of a sequence of `tiles` steps of 32 positions: of 512 positions up
+// to 16 of them, then of 1024 up to 64.
 __host__ __device__ inline int splits_of(int tiles) {
-    const int n = (tiles + kSplitTiles - 1) / kSplitTiles;
+    const int fine = (tiles + 15) / 16, coarse = (tiles + 31) / 32;
+    const int n = fine <= 16 ? fine : coarse <= 16 ? 16 : coarse;
     return n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n;
+}
+
+// First step of split i of n over `tiles` steps (evenly, in order).
+__device__ inline int split_start(int tiles, int n, int i) {
+    const int q = tiles / n, r = tiles - q * n;
+    return q * i + min(i, r);
 }
 
 __device__ inline v4f mfma(u4 a, u4 b, v4f c) {
@@ -64,11 +69,11 @@ __device__ inline v4f mfma(u4 a, u4 b, v4f c) {
                                                    __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
 }
 
-// Byte B of w as the exponent of a float (the conversions read no other bits
-// of their scale).
+// Byte B of w as the exponent bits of a float.  The conversions read only
+// those of their scale, so what else the shift leaves does not matter.
 template <int B>
 __device__ inline float scale_exp(uint32_t w) {
-    return __uint_as_float(((w >> (8 * B)) & 0xffu) << 23);
+    return __uint_as_float(B == 3 ? w >> 1 : w << (23 - 8 * B));
 }
 
 // Codes of byte B of w, low nibble first, as two exact bf16.
@@ -100,58 +105,109 @@ __device__ inline void split3(const float (&x)[8], u4 (&p)[3]) {
     for (int i = 0; i < 4; ++i) p[2][i] = pack_hi(r[2 * i], r[2 * i + 1]);
 }
 
+// ---- memory to LDS.  A wave has kSlots slots of its own in LDS, one group of
+// 32 positions each, filled by loads that go past the registers and are
+// waited for by count (loads complete in order).  No other wave touches them.
+constexpr int kSlots = 2;
+
+// A group in LDS: its bytes, the scales' part rounded up to whole loads.
+__host__ __device__ constexpr int scale_loads(int nb) {
+    return (group_bytes(nb) - group_ks(nb) + 255) / 256;
+}
+__host__ __device__ constexpr int slot_bytes(int nb) { return group_ks(nb) + 256 * scale_loads(nb); }
+
+__device__ inline uint32_t lds_address(const void* p) {
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+
+// 64 lanes x 16 (4) bytes from base + voff to the LDS bytes from `lds` on.
+__device__ inline void lds_load16(uint32_t lds, const uint8_t* base, uint32_t voff) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 ::"s"(lds), "v"(voff), "s"(base) : "memory");
+}
+__device__ inline void lds_load4(uint32_t lds, const uint8_t* base, uint32_t voff) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
+                 ::"s"(lds), "v"(voff), "s"(base) : "memory");
+}
+// At most N loads (and stores) still on their way.
+template <int N>
+__device__ inline void wait_loads() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+// LDS reads into registers are done: what they read may be overwritten.
+__device__ inline void wait_lds_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+template <int NB>
+constexpr int kGroupLoads = NB + scale_loads(NB);
+
+template <int NB>
+__device__ inline void load_group(uint32_t lds, const uint8_t* group, int lane) {
+#pragma unroll
+    for (int i = 0; i < NB; ++i) lds_load16(lds + i * 1024, group + i * 1024, lane * 16);
+    // lanes past the end repeat the last word
+#pragma unroll
+    for (int i = 0; i < scale_loads(NB); ++i)
+        lds_load4(lds + group_ks(NB) + i * 256, group + group_ks(NB),
+                  min(i * 256 + lane * 4, group_bytes(NB) - group_ks(NB) - 4));
+}
+
+// N (1..4) words from LDS.
+template <int N>
+__device__ inline void read_words(const uint8_t* p, uint32_t* o) {
+    if constexpr (N == 4) {
+        const u4 t = *reinterpret_cast<const u4*>(p);
+        o[0] = t[0]; o[1] = t[1]; o[2] = t[2]; o[3] = t[3];
+    } else if constexpr (N == 2) {
+        typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+        const u2 t = *reinterpret_cast<const u2*>(p);
+        o[0] = t[0]; o[1] = t[1];
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) o[i] = reinterpret_cast<const uint32_t*>(p)[i];
+    }
+}
+
 // One step's operands of one wave: 32 positions of a head.
 template <int NB>
-struct Step {
-    uint32_t k[2][NB];   // K codes of the two 16-position tiles
-    uint32_t ks[2][(NB + 3) / 4];
-    uint32_t v[2 * NB];  // V codes: block b at v[2b], v[2b + 1]
-    uint32_t vs[2 * NB];
+struct Keys {
+    uint32_t c[2][NB];             // codes of the two 16-position tiles
+    uint32_t s[2][(NB + 3) / 4];   // scales
+};
+template <int NB>
+struct Values {
+    uint32_t c[2 * NB];  // block b at [2b], [2b + 1]
+    uint32_t s[2 * NB];
 };
 
-// n (1..4) dwords from p, aligned to the dword.
-template <int N>
-__device__ inline void load_dwords(const uint8_t* p, uint32_t* o) {
-    typedef uint32_t w __attribute__((ext_vector_type(N), aligned(4)));
-    if constexpr (N == 1) {
-        o[0] = *reinterpret_cast<const uint32_t*>(p);
-    } else {
-        const w t = *reinterpret_cast<const w*>(p);
+template <int NB>
+__device__ inline void read_keys(const uint8_t* slot, int lane, Keys<NB>& k) {
+    constexpr int SP = scale_pitch(NB);
 #pragma unroll
-        for (int i = 0; i < N; ++i) o[i] = t[i];
+    for (int h = 0; h < 2; ++h) {
+        const uint8_t* c = slot + h * 256 * NB;
+#pragma unroll
+        for (int q = 0; q < NB / 4; ++q) read_words<4>(c + q * 1024 + lane * 16, &k.c[h][4 * q]);
+        if constexpr (NB % 4 != 0)
+            read_words<NB % 4>(c + (NB / 4) * 1024 + lane * (4 * (NB % 4)), &k.c[h][NB / 4 * 4]);
+        const uint8_t* s = slot + group_ks(NB) + (16 * h + (lane & 15)) * SP;
+        if constexpr (SP == 1) k.s[h][0] = *s;
+        else if constexpr (SP == 2) k.s[h][0] = *reinterpret_cast<const uint16_t*>(s);
+        else read_words<SP / 4>(s, k.s[h]);
     }
 }
 
 template <int NB>
-__device__ inline void load_step(const uint8_t* head, const HeadLayout& hl, int tok, int lane,
-                                 Step<NB>& s) {
-    constexpr int SP = scale_pitch(NB);
-    const uint8_t* kc = head + (int64_t)(tok >> 4) * (256 * NB);
+__device__ inline void read_values(const uint8_t* slot, int lane, Values<NB>& v) {
+    const uint8_t* c = slot + group_v(NB);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int p = 0; p < NB / 2; ++p) read_words<4>(c + p * 1024 + lane * 16, &v.c[4 * p]);
+    if constexpr (NB % 2 != 0) read_words<2>(c + (NB / 2) * 1024 + lane * 8, &v.c[2 * NB - 2]);
+    const uint8_t* s = slot + group_vs(NB) + (lane >> 4) * (8 * NB);
 #pragma unroll
-        for (int q = 0; q < NB / 4; ++q)
-            load_dwords<4>(kc + h * 256 * NB + q * 1024 + lane * 16, &s.k[h][4 * q]);
-        if constexpr (NB % 4 != 0)
-            load_dwords<NB % 4>(kc + h * 256 * NB + (NB / 4) * 1024 + lane * (4 * (NB % 4)),
-                                &s.k[h][NB / 4 * 4]);
-        const uint8_t* ks = head + hl.ks + (int64_t)(tok + 16 * h + (lane & 15)) * SP;
-        if constexpr (SP == 1) s.ks[h][0] = *ks;
-        else if constexpr (SP == 2) s.ks[h][0] = *reinterpret_cast<const uint16_t*>(ks);
-        else load_dwords<SP / 4>(ks, s.ks[h]);
-    }
-    const uint8_t* vc = head + hl.v + (int64_t)(tok >> 5) * (512 * NB);
-#pragma unroll
-    for (int p = 0; p < NB / 2; ++p) load_dwords<4>(vc + p * 1024 + lane * 16, &s.v[4 * p]);
-    if constexpr (NB % 2 != 0) load_dwords<2>(vc + (NB / 2) * 1024 + lane * 8, &s.v[2 * NB - 2]);
-    const uint8_t* vs = head + hl.vs + (int64_t)(tok >> 5) * (32 * NB) + (lane >> 4) * (8 * NB);
-#pragma unroll
-    for (int p = 0; p < NB / 2; ++p) load_dwords<4>(vs + p * 16, &s.vs[4 * p]);
-    if constexpr (NB % 2 != 0) load_dwords<2>(vs + (NB / 2) * 16, &s.vs[2 * NB - 2]);
+    for (int b = 0; b < NB; ++b) read_words<2>(s + 8 * b, &v.s[2 * b]);
 }
 
-// Bytes of w whose position is not in [0, n): cleared by the returned mask;
-// first: position of byte 0.
+// Mask of the bytes of a word of 4 positions, from `first` on, in [lo, hi).
 __device__ inline uint32_t byte_mask(int first, int lo, int hi) {
     uint32_t m = 0;
 #pragma unroll
@@ -160,110 +216,160 @@ __device__ inline uint32_t byte_mask(int first, int lo, int hi) {
     return m;
 }
 
-__device__ inline uint32_t any_ff(uint32_t w) {  // nonzero where a byte of w is 0xff
+__device__ inline uint32_t any_ff(uint32_t w) {  // 0x80 where a byte of w is 0xff
     return (((w & 0x7f7f7f7fu) + 0x01010101u) & w) & 0x80808080u;
 }
 
+// v plus v of the lane 8 away within each 16.
+__device__ inline float add_ror8(float v) {
+    return v + __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), 0x128, 0xf,
+                                                                 0xf, true));
+}
+// Maximum over lanes 16 and 32 apart.
+__device__ inline float max_over_quarters(float v) {
+    const uint32_t u = __float_as_uint(v);
+    const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const uint32_t m = __float_as_uint(fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1])));
+    const auto b = __builtin_amdgcn_permlane16_swap(m, m, false, false);
+    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+
+// How a column tile holds its rows.  kWide: 16 rows, an operand for each of the
+// three pieces.  kFolded, for at most 8 rows: columns c and c + 8 belong to one
+// row, the first operand has its upper piece in c and its middle one in
+// c + 8, the second its lower piece in c; two instructions instead of three.
+// Scores add up over the two columns; outputs do at the end.
+enum Fold { kWide, kFolded };
+
+// x as operands: N = 3 (wide) or 2 (folded) of 8 bf16, exactly.  Folded, every
+// lane is given its row's x, keep = 0xffff0000 in columns 8..15 and 0 in 0..7.
+template <Fold F>
+__device__ inline void split(const float (&x)[8], uint32_t keep, u4 (&p)[F == kWide ? 3 : 2]) {
+    if constexpr (F == kWide) {
+        split3(x, p);
+    } else {
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = x[i] - __uint_as_float(__float_as_uint(x[i]) & keep);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[0][i] = pack_hi(y[2 * i], y[2 * i + 1]);
+        // columns 8..15: y is the part below the upper piece, and what is below
+        // its own upper half is the lower piece
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = y[i] - trunc_bf16(y[i]);
+        const uint32_t low = keep | keep >> 16;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[1][i] = pack_hi(y[2 * i], y[2 * i + 1]) & low;
+    }
+}
+
 // Carried state of one column tile.
-template <int NB>
+template <int NB, Fold F>
 struct Rows {
-    u4 q[NB][3];         // query operand, three pieces
+    static constexpr int P = F == kWide ? 3 : 2;
+    u4 q[NB][P];         // query operands
     v4f o[NB][2];        // O^T: dim 32b + 2(4g + i) + e in o[b][e][i]
-    float m, l;          // running maximum (of c q.k) and this lane's share of the sum
+    float m, l;          // running maximum (of q.k) and this lane's share of the sum
     int lo, hi;          // positions this column sees
 };
 
-template <int NB, int RT>
-__device__ inline void attend_step(Step<NB>& s, Rows<NB> (&rows)[RT], int tok, int lane, float c,
-                                   bool partial, bool bad, int lo, int hi) {
-    const int g = lane >> 4;
-    v4f S[RT][2];
+template <int NB, int RT, Fold F>
+__device__ inline void scores(const Keys<NB>& k, const Rows<NB, F> (&rows)[RT], v4f (&S)[RT][2]) {
+    constexpr int P = Rows<NB, F>::P;
     const v4f zero = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int r = 0; r < RT; ++r) S[r][0] = S[r][1] = zero;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int b = 0; b < NB; ++b) {
+        u4 a[2];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            const uint32_t sw = s.ks[h][b / 4];
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t sw = k.s[h][b / 4], w = k.c[h][b];
             const float sc = (b & 3) == 0 ? scale_exp<0>(sw) : (b & 3) == 1 ? scale_exp<1>(sw)
                              : (b & 3) == 2 ? scale_exp<2>(sw) : scale_exp<3>(sw);
-            const uint32_t w = s.k[h][b];
-            const u4 a = {dequant2<0>(w, sc), dequant2<1>(w, sc), dequant2<2>(w, sc), dequant2<3>(w, sc)};
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                S[r][h] = mfma(a, rows[r].q[b][2], S[r][h]);
-                S[r][h] = mfma(a, rows[r].q[b][1], S[r][h]);
-                S[r][h] = mfma(a, rows[r].q[b][0], S[r][h]);
-            }
+            a[h] = u4{dequant2<0>(w, sc), dequant2<1>(w, sc), dequant2<2>(w, sc), dequant2<3>(w, sc)};
         }
+#pragma unroll
+        for (int i = P - 1; i >= 0; --i)
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) S[r][h] = mfma(a[h], rows[r].q[b][i], S[r][h]);
     }
-    if (partial) {
-        // Positions outside [lo, hi), which no row sees, may hold anything:
-        // their values and scales become zeros, so that 0 * NaN cannot arise.
-        const uint32_t m0 = bad ? 0u : byte_mask(tok + 4 * g, lo, hi);
-        const uint32_t m1 = bad ? 0u : byte_mask(tok + 16 + 4 * g, lo, hi);
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            s.v[2 * b] &= m0;
-            s.vs[2 * b] &= m0;
-            s.v[2 * b + 1] &= m1;
-            s.vs[2 * b + 1] &= m1;
-        }
-        const float ninf = -__builtin_inff();
+    if constexpr (F == kFolded) {
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int t = tok + 16 * h + 4 * g + i;
-                    const bool seen = t >= rows[r].lo && t < rows[r].hi;
-                    S[r][h][i] = seen ? (bad ? __builtin_nanf("") : S[r][h][i]) : ninf;
-                }
-        // A NaN value block at a position that some rows see and others do
-        // not: 0 * NaN would reach the others.  The block becomes zeros, and
-        // the rows that see it get their NaN here.
-        uint32_t nan_here = 0;
-#pragma unroll
-        for (int b = 0; b < 2 * NB; ++b) nan_here |= any_ff(s.vs[b]);
-        if (__any(nan_here != 0)) {
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    for (int gg = 0; gg < 4; ++gg) {
-                        const uint32_t w = __builtin_amdgcn_readlane(s.vs[2 * b + k], 16 * gg);
-                        for (int j = 0; j < 4; ++j) {
-                            if ((w >> (8 * j) & 0xffu) != 0xffu) continue;
-                            const int t = tok + 16 * k + 4 * gg + j;
-#pragma unroll
-                            for (int r = 0; r < RT; ++r)
-                                if (t >= rows[r].lo && t < rows[r].hi)
-                                    rows[r].o[b][0] = rows[r].o[b][1] = zero + __builtin_nanf("");
-                        }
-                    }
-                    const uint32_t ff = any_ff(s.vs[2 * b + k]) >> 7;  // 1 in each NaN byte
-                    s.vs[2 * b + k] &= ~(ff * 0xffu);
-                }
-        }
+            for (int i = 0; i < 8; ++i) S[r][i >> 2][i & 3] = add_ror8(S[r][i >> 2][i & 3]);
     }
-    u4 p[RT][3];
+}
+
+// A step that some row does not see whole, or whose page is not there (bad).
+template <int NB, int RT, Fold F>
+__device__ inline void mask_step(Values<NB>& v, Rows<NB, F> (&rows)[RT], v4f (&S)[RT][2], int tok, int g,
+                                 bool bad, int lo, int hi) {
+    // Positions outside [lo, hi), which no row sees, may hold anything:
+    // their values and scales become zeros, so that 0 * NaN cannot arise.
+    const uint32_t m0 = bad ? 0u : byte_mask(tok + 4 * g, lo, hi);
+    const uint32_t m1 = bad ? 0u : byte_mask(tok + 16 + 4 * g, lo, hi);
+    uint32_t nan_here = 0;
+#pragma unroll
+    for (int b = 0; b < 2 * NB; ++b) {
+        const uint32_t m = b & 1 ? m1 : m0;
+        v.c[b] &= m;
+        v.s[b] &= m;
+        nan_here |= any_ff(v.s[b]);
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = tok + 16 * h + 4 * g + i;
+                const bool seen = t >= rows[r].lo && t < rows[r].hi;
+                S[r][h][i] = seen ? (bad ? __builtin_nanf("") : S[r][h][i]) : -__builtin_inff();
+            }
+    // A NaN value block at a position that some rows see and others do not:
+    // 0 * NaN would reach the others.  The block becomes zeros, and the rows
+    // that see it get their NaN here.
+    if (!__any(nan_here != 0)) return;
+#pragma unroll
+    for (int b = 0; b < 2 * NB; ++b) {
+        if (!__any(any_ff(v.s[b]) != 0)) continue;
+#pragma unroll 1
+        for (int n = 0; n < 16; ++n) {  // n = 4 * quarter + byte
+            const uint32_t w = __builtin_amdgcn_readlane(v.s[b], 16 * (n >> 2));
+            if ((w >> (8 * (n & 3)) & 0xffu) != 0xffu) continue;
+            const int t = tok + 16 * (b & 1) + n;
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                const float add = t >= rows[r].lo && t < rows[r].hi ? __builtin_nanf("") : 0.0f;
+                rows[r].o[b >> 1][0] += add;
+                rows[r].o[b >> 1][1] += add;
+            }
+        }
+        v.s[b] &= ~((any_ff(v.s[b]) >> 7) * 0xffu);
+    }
+}
+
+template <int NB, int RT, Fold F>
+__device__ inline void softmax_and_values(const Values<NB>& v, Rows<NB, F> (&rows)[RT], v4f (&S)[RT][2],
+                                          float c, float lag, uint32_t keep) {
+    constexpr int P = Rows<NB, F>::P;
+    u4 p[RT][P];
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-        float x[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = S[r][i >> 2][i & 3] * c;
-        float t = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
-                        fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-        t = fmaxf(t, __shfl_xor(t, 16));
-        t = fmaxf(t, __shfl_xor(t, 32));
+        const v4f x0 = S[r][0], x1 = S[r][1];
+        float t = fmaxf(fmaxf(fmaxf(x0[0], x0[1]), fmaxf(x0[2], x0[3])),
+                        fmaxf(fmaxf(x1[0], x1[1]), fmaxf(x1[2], x1[3])));
+        t = max_over_quarters(t);
         // The maximum is raised only when it grew by more than 2^8: weights
         // up to 256 lose nothing in floating point, and most steps skip the rescaling.
-        const bool grow = t > rows[r].m + 8.0f;
+        const bool grow = t > rows[r].m + lag;
         if (__any(grow)) {
             const float m = grow ? t : rows[r].m;
-            const float f = grow ? __builtin_amdgcn_exp2f(rows[r].m - m) : 1.0f;
+            const float f = grow ? __builtin_amdgcn_exp2f((rows[r].m - m) * c) : 1.0f;
             rows[r].m = m;
             rows[r].l *= f;
 #pragma unroll
@@ -275,13 +381,14 @@ __device__ inline void attend_step(Step<NB>& s, Rows<NB> (&rows)[RT], int tok, i
         const float m = rows[r].m == -__builtin_inff() ? 0.0f : rows[r].m;
         float e[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] = __builtin_amdgcn_exp2f(x[i] - m);
+        for (int i = 0; i < 8; ++i)
+            e[i] = __builtin_amdgcn_exp2f((S[r][i >> 2][i & 3] - m) * c);
         rows[r].l += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-        split3(e, p[r]);
+        split<F>(e, keep, p[r]);
     }
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-        const uint32_t w0 = s.v[2 * b], w1 = s.v[2 * b + 1], s0 = s.vs[2 * b], s1 = s.vs[2 * b + 1];
+        const uint32_t w0 = v.c[2 * b], w1 = v.c[2 * b + 1], s0 = v.s[2 * b], s1 = v.s[2 * b + 1];
         const uint32_t d[8] = {dequant2<0>(w0, scale_exp<0>(s0)), dequant2<1>(w0, scale_exp<1>(s0)),
                                dequant2<2>(w0, scale_exp<2>(s0)), dequant2<3>(w0, scale_exp<3>(s0)),
                                dequant2<0>(w1, scale_exp<0>(s1)), dequant2<1>(w1, scale_exp<1>(s1)),
@@ -293,9 +400,9 @@ __device__ inline void attend_step(Step<NB>& s, Rows<NB> (&rows)[RT], int tok, i
             odd[i] = __builtin_amdgcn_perm(d[2 * i + 1], d[2 * i], 0x07060302u);
         }
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
+        for (int k = P - 1; k >= 0; --k)
 #pragma unroll
-            for (int k = 2; k >= 0; --k) {
+            for (int r = 0; r < RT; ++r) {
                 rows[r].o[b][0] = mfma(even, p[r][k], rows[r].o[b][0]);
                 rows[r].o[b][1] = mfma(odd, p[r][k], rows[r].o[b][1]);
             }
@@ -328,62 +435,75 @@ __device__ inline Extent extent_of(const AttendArgs& a, int s) {
     return {lo, hi, tiles, splits_of(tiles), slot};
 }
 
-__device__ inline float agent_load(const float* p) {
-    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+// 0: a row to compute, 1: idle (zeros), 2: outside the cache (NaN).
+__device__ inline int row_flag(int pos, int row_slot, int slot, int n_slots, int cap) {
+    if (pos < 0) return 1;
+    return slot < 0 || slot >= n_slots || row_slot != slot || pos >= cap ? 2 : 0;
 }
-__device__ inline void agent_store(float* p, float v) {
-    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ inline void wait_for_own_stores() {
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    __builtin_amdgcn_s_waitcnt(0);
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+
+// A row's output as its flag has it.
+__device__ inline v4f flagged(v4f x, int flag) {
+    const v4f zero = {0.f, 0.f, 0.f, 0.f};
+    return flag == 0 ? x : flag == 1 ? zero : zero + __builtin_nanf("");
 }
 
 // Weight of a part with maximum m_part in a whole with maximum m.
-__device__ inline float part_weight(float m_part, float m) {
-    return m_part == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m_part - m);
+__device__ inline float part_weight(float m_part, float m, float c) {
+    return m_part == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f((m_part - m) * c);
 }
 
-// Rows of a unit that one workgroup takes, and its partial record: the
-// accumulators component-major (component k of float4 v at k*E/4 + v, so
-// that a device-coherent dword store covers whole lines), then maxima and sums.
-__host__ __device__ constexpr int64_t record_floats(int rows, int nb) {
-    return (int64_t)rows * (nb * 32 + 2);
-}
+// The partial record of a workgroup's rows: accumulators [rows][D], then
+// their maxima and sums.
+__host__ __device__ constexpr int record_floats(int rows, int nb) { return rows * (nb * 32 + 2); }
 
-template <int NB, int RT>
-__global__ void __launch_bounds__(kThreads, RT == 1 && NB <= 4 ? 2 : 1)
+// Extents of 64 sequences and the items counted up to and in each.
+struct Items {
+    int upto[64], mine[64], lo[64], hi[64], tiles[64], splits[64], slot[64];
+};
+
+// LDS of a workgroup: the waves' slots, and over them, once the steps are
+// done, what the join of the waves needs.
+template <int NB, int RT, Fold F>
+struct Shared {
+    static constexpr int kWaves = waves_of(NB);
+    static constexpr int kCols = F == kFolded ? 8 : 16;  // rows of a column tile
+    static constexpr int kRows = kCols * RT;
+    static constexpr int kPitch = NB * 32 + 4;           // floats of a row's accumulator
+    union {
+        uint8_t slots[kWaves][kSlots][slot_bytes(NB)];
+        float o[kWaves][kCols][kPitch];
+    };
+    float m[kWaves][kRows], l[kWaves][kRows];  // of the waves
+    float inv[kRows];
+    int flag[kRows];
+    Items items;                               // of the first 64 sequences
+};
+
+template <int NB, int RT, Fold F>
+__global__ void __launch_bounds__(64 * waves_of(NB), RT == 1 && NB <= 4 ? (F == kFolded ? 3 : 2) : 1)
 kv4_attend_kernel(AttendArgs a, int n_rb, int rec_rows, int max_splits) {
+    using Sh = Shared<NB, RT, F>;
     constexpr int D = NB * 32;
-    constexpr int kPitch = D + 4;  // LDS floats of a row's accumulator
-    constexpr int kRows = 16 * RT;
-    __shared__ float lds_o[kWaves * 16 * kPitch];
-    __shared__ float lds_m[kWaves][kRows], lds_l[kWaves][kRows];
-    __shared__ float lds_w[kMaxSplits][kRows];  // weights of the splits
-    __shared__ float lds_inv[kRows];
-    __shared__ int lds_flag[kRows];             // 0: as computed, 1: zeros, 2: NaN
-    __shared__ uint32_t lds_last;
+    constexpr int kWaves = Sh::kWaves, kThreads = 64 * kWaves;
+    constexpr int kCols = Sh::kCols, kRows = Sh::kRows;
+    __shared__ __align__(16) Sh sh;
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int col = lane & 15, g = lane >> 4;
+    const int col = F == kFolded ? lane & 7 : lane & 15, g = lane >> 4;
+    const bool owner = F == kFolded ? (lane & 15) < 8 && g == 0 : g == 0;  // one lane of a row
+    const uint32_t keep = lane & 8 ? 0xffff0000u : 0u;
+    const float c = a.scale_log2, lag = 8.0f / c;
     const int n_rows = a.tokens * a.group;
-    const HeadLayout hl = head_layout(NB, a.c.page_tokens);
-    const int tiles_per_page = a.c.page_tokens / kKvTile;
+    const int groups_per_page = a.c.page_tokens / kKvTile;
     const int cap = a.c.max_pages * a.c.page_tokens;
-    uint32_t* counters = reinterpret_cast<uint32_t*>(a.workspace);
-    float* records = reinterpret_cast<float*>(a.workspace + kCounterBytes);
+    float* records = reinterpret_cast<float*>(a.workspace);
 
-    for (int64_t item = blockIdx.x;; item += gridDim.x) {
-        // ---- which item: items are counted sequence by sequence, 64 lanes at a time
-        int seq = -1;
-        int64_t rest = item;
-        Extent ex = {0, 0, 0, 1, -1};
-        for (int s0 = 0; s0 < a.n_seq; s0 += 64) {
-            const int s = s0 + lane;
+    // Each lane of the first wave counts the items of one sequence.
+    const auto count_items = [&](int s0) {
+        if (wave == 0) {
             Extent e = {0, 0, 0, 0, -1};
-            if (s < a.n_seq) e = extent_of(a, s);
+            if (s0 + lane < a.n_seq) e = extent_of(a, s0 + lane);
             const int mine = e.splits * a.c.n_kv * n_rb;  // 0 past the last sequence
             int upto = mine;
 #pragma unroll
@@ -391,64 +511,119 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int rec_rows, int max_splits) {
                 const int o = __shfl_up(upto, d);
                 if (lane >= d) upto += o;
             }
-            const uint64_t past = __ballot((int64_t)upto > rest);
-            if (past != 0) {
-                const int f = __builtin_ctzll(past);
-                seq = s0 + f;
-                rest -= __builtin_amdgcn_readlane(upto, f) - __builtin_amdgcn_readlane(mine, f);
-                ex.lo = __builtin_amdgcn_readlane(e.lo, f);
-                ex.hi = __builtin_amdgcn_readlane(e.hi, f);
-                ex.tiles = __builtin_amdgcn_readlane(e.tiles, f);
-                ex.splits = __builtin_amdgcn_readlane(e.splits, f);
-                ex.slot = __builtin_amdgcn_readlane(e.slot, f);
-                break;
-            }
-            rest -= __builtin_amdgcn_readlane(upto, 63);
+            sh.items.upto[lane] = upto;
+            sh.items.mine[lane] = mine;
+            sh.items.lo[lane] = e.lo;
+            sh.items.hi[lane] = e.hi;
+            sh.items.tiles[lane] = e.tiles;
+            sh.items.splits[lane] = e.splits;
+            sh.items.slot[lane] = e.slot;
         }
-        if (seq < 0) return;  // past the last item: every wave of the workgroup
-        const int unit_of_seq = (int)rest / ex.splits;
-        const int split = (int)rest - unit_of_seq * ex.splits;
+        __syncthreads();
+    };
+    int seq0 = 0;             // sequences seq0 .. seq0 + 63 are counted in LDS,
+    int64_t before = 0;       // and this many items lie before them
+    count_items(0);
+
+    for (int64_t item = blockIdx.x;; item += gridDim.x) {
+        // ---- which item: items are counted sequence by sequence
+        uint64_t past;
+        while ((past = __ballot(sh.items.upto[lane] > item - before)) == 0) {
+            before += sh.items.upto[63];
+            seq0 += 64;
+            if (seq0 >= a.n_seq) return;  // past the last item: the whole workgroup
+            __syncthreads();              // everyone is done with the counts
+            count_items(seq0);
+        }
+        const int f = __builtin_ctzll(past);
+        const auto of = [&](const int (&v)[64]) { return __builtin_amdgcn_readfirstlane(v[f]); };
+        const int seq = seq0 + f;
+        const int64_t left = item - before - (of(sh.items.upto) - of(sh.items.mine));
+        const Extent ex = {of(sh.items.lo), of(sh.items.hi), of(sh.items.tiles), of(sh.items.splits),
+                           of(sh.items.slot)};
+        const int rest = (int)left;  // below the sequence's items, < 2^24
+        const int unit_of_seq = rest / ex.splits;
+        const int split_no = rest - unit_of_seq * ex.splits;
         const int head = unit_of_seq / n_rb, rb = unit_of_seq - head * n_rb;
         const int tile_lo = ex.lo / kKvTile;
-        const int t0 = tile_lo + (int)((int64_t)ex.tiles * split / ex.splits);
-        const int t1 = tile_lo + (int)((int64_t)ex.tiles * (split + 1) / ex.splits);
+        const int t0 = tile_lo + split_start(ex.tiles, ex.splits, split_no);
+        const int t1 = tile_lo + split_start(ex.tiles, ex.splits, split_no + 1);
         const int slot = ex.slot;
-        const int64_t table = (int64_t)slot * a.c.max_pages;
 
-        // ---- the query rows
-        Rows<NB> rows[RT];
+        // ---- the first page ids and the query rows, loaded together
+        const int first = t0 + wave;
+        int page = first / groups_per_page, in_page = first - page * groups_per_page;
+        int page0 = page;  // lane i holds the page id of page page0 + i
+        const auto load_ids = [&](int p0) {
+            const int p = p0 + lane;
+            return p < a.c.max_pages ? a.c.table[(int64_t)slot * a.c.max_pages + p] : -1;
+        };
+        int ids = 0;
+        if (first < t1) ids = load_ids(page0);
+        Rows<NB, F> rows[RT];
+        int row_pos[RT], row_slot[RT];
+        f4u q_in[RT][NB][2];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            const int row = min(rb * kRows + r * kCols + col, n_rows - 1);  // past the last: that again
+            const int j = row / a.group, qh = head * a.group + row - j * a.group;
+            const int64_t t = (int64_t)seq * a.tokens + j;
+            row_pos[r] = a.pos[t];
+            row_slot[r] = a.batch_index[t];
+            const float* q = a.Q + t * a.q_stride + (int64_t)qh * D + 8 * g;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                q_in[r][b][0] = *reinterpret_cast<const f4u*>(q + 32 * b);
+                q_in[r][b][1] = *reinterpret_cast<const f4u*>(q + 32 * b + 4);
+            }
+        }
+        // They are here before the groups set out, which come in behind them.
+        __builtin_amdgcn_s_waitcnt(kNoVmem);
+        __builtin_amdgcn_sched_barrier(0);
+
+        // ---- this wave's steps: t0 + wave, + kWaves, ...; the first on their way
+        int ahead = first;  // next step to load
+        bool bad[kSlots];   // its page is not there
+        const auto load_next = [&](int i) {
+            if (page - page0 >= 64) {
+                page0 = page;
+                ids = load_ids(page0);
+            }
+            const int id = __builtin_amdgcn_readlane(ids, page - page0);
+            bad[i] = id < 0 || id >= a.c.n_pages;
+            const uint8_t* p = a.c.pages + (bad[i] ? 0 : id) * a.c.page_bytes + head * a.c.head_bytes +
+                               in_page * group_bytes(NB);
+            load_group<NB>(lds_address(sh.slots[wave][i]), p, lane);
+            ahead += kWaves;
+            in_page += kWaves;
+            while (in_page >= groups_per_page) {
+                in_page -= groups_per_page;
+                ++page;
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i)
+            if (ahead < t1) load_next(i);
+
         int all_lo = 0, all_hi = INT32_MAX;  // seen by every row of the workgroup
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-            const int row = rb * kRows + r * 16 + col;
-            const bool there = row < n_rows;
-            const int j = there ? row / a.group : 0;
-            const int qh = head * a.group + (there ? row - j * a.group : 0);
-            const int64_t t = (int64_t)seq * a.tokens + j;
-            const int p = there ? a.pos[t] : -1;
-            int flag = 0;
-            if (p < 0) flag = 1;
-            else if (slot < 0 || slot >= a.c.n_slots || a.batch_index[t] != slot || p >= cap) flag = 2;
+            const int flag = row_flag(row_pos[r], row_slot[r], slot, a.c.n_slots, cap);
             // rows that are not computed see what their neighbours see, of a
             // query of zeros
-            rows[r].lo = flag == 0 && a.window > 0 ? max(0, p + 1 - a.window) : 0;
-            rows[r].hi = flag == 0 ? p + 1 : INT32_MAX;
+            rows[r].lo = flag == 0 && a.window > 0 ? max(0, row_pos[r] + 1 - a.window) : 0;
+            rows[r].hi = flag == 0 ? row_pos[r] + 1 : INT32_MAX;
             rows[r].m = -__builtin_inff();
             rows[r].l = 0.0f;
             all_lo = max(all_lo, rows[r].lo);
             all_hi = min(all_hi, rows[r].hi);
-            if (wave == 0 && g == 0) lds_flag[r * 16 + col] = flag;
-            const float* q = a.Q + t * a.q_stride + (int64_t)qh * D + 8 * g;
+            if (wave == 0 && owner) sh.flag[r * kCols + col] = flag;
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                if (flag == 0) {
-                    const f4u u = *reinterpret_cast<const f4u*>(q + 32 * b);
-                    const f4u v = *reinterpret_cast<const f4u*>(q + 32 * b + 4);
-                    x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
-                    x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
-                }
-                split3(x, rows[r].q[b]);
+                float x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = flag == 0 ? q_in[r][b][i >> 2][i & 3] : 0.0f;
+                split<F>(x, keep, rows[r].q[b]);
                 rows[r].o[b][0] = rows[r].o[b][1] = v4f{0.f, 0.f, 0.f, 0.f};
             }
         }
@@ -457,46 +632,35 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int rec_rows, int max_splits) {
             all_lo = max(all_lo, __shfl_xor(all_lo, d));
             all_hi = min(all_hi, __shfl_xor(all_hi, d));
         }
-        all_lo = __builtin_amdgcn_readfirstlane(all_lo);
-        all_hi = __builtin_amdgcn_readfirstlane(all_hi);
+        // steps that every row sees whole: [whole_lo, whole_hi)
+        all_lo = max(__builtin_amdgcn_readfirstlane(all_lo), ex.lo);
+        all_hi = min(__builtin_amdgcn_readfirstlane(all_hi), ex.hi);
+        const int whole_lo = (all_lo + kKvTile - 1) / kKvTile, whole_hi = all_hi / kKvTile;
 
-        // ---- this wave's steps: t0 + wave, + 4, ...
-        const int first = t0 + wave;
-        if (first < t1) {
-            int page = first / tiles_per_page, in_page = first - page * tiles_per_page;
-            int window0 = page;  // lane i holds the page id of page window0 + i
-            const auto load_ids = [&](int p0) {
-                const int p = p0 + lane;
-                return p < a.c.max_pages ? a.c.table[table + p] : -1;
-            };
-            int ids = load_ids(window0);
-            const auto fetch = [&](Step<NB>& s, bool& bad) {
-                if (page - window0 >= 64) {
-                    window0 = page;
-                    ids = load_ids(window0);
-                }
-                const int id = __builtin_amdgcn_readlane(ids, page - window0);
-                bad = id < 0 || id >= a.c.n_pages;
-                const uint8_t* h = a.c.pages + (bad ? 0 : id) * a.c.page_bytes + head * a.c.head_bytes;
-                load_step<NB>(h, hl, in_page * kKvTile, lane, s);
-                in_page += kWaves;
-                while (in_page >= tiles_per_page) {
-                    in_page -= tiles_per_page;
-                    ++page;
-                }
-            };
-            Step<NB> now, next;
-            bool bad_now, bad_next = false;
-            fetch(now, bad_now);
-            for (int t = first; t < t1; t += kWaves) {
-                if (t + kWaves < t1) fetch(next, bad_next);
-                const int tok = t * kKvTile;
-                const bool partial = bad_now || tok < all_lo || tok + kKvTile > all_hi || tok < ex.lo ||
-                                     tok + kKvTile > ex.hi;
-                attend_step<NB, RT>(now, rows, tok, lane, a.scale_log2, partial, bad_now, ex.lo, ex.hi);
-                now = next;
-                bad_now = bad_next;
-            }
+        // One step.  Its slot is free for the step after next as soon as the
+        // values are in registers.
+        const auto step = [&](int i, int t) {
+            const uint8_t* slot = sh.slots[wave][i];
+            if (t + kWaves < t1) wait_loads<kGroupLoads<NB>>();  // all but the next step's
+            else wait_loads<0>();
+            Keys<NB> keys;
+            Values<NB> vals;
+            v4f S[RT][2];
+            read_keys<NB>(slot, lane, keys);
+            scores<NB, RT, F>(keys, rows, S);
+            read_values<NB>(slot, lane, vals);
+            wait_lds_reads();
+            const bool bad_now = bad[i];
+            if (ahead < t1) load_next(i);
+            if (bad_now || t < whole_lo || t >= whole_hi)
+                mask_step<NB, RT, F>(vals, rows, S, t * kKvTile, g, bad_now, ex.lo, ex.hi);
+            softmax_and_values<NB, RT, F>(vals, rows, S, c, lag, keep);
+        };
+        static_assert(kSlots == 2, "the loop below alternates between two slots");
+        for (int t = first; t < t1; t += 2 * kWaves) {
+            step(0, t);
+            if (t + kWaves >= t1) break;
+            step(1, t + kWaves);
         }
 
         // ---- join the waves
@@ -505,135 +669,152 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int rec_rows, int max_splits) {
             float l = rows[r].l;
             l += __shfl_xor(l, 16);
             l += __shfl_xor(l, 32);
-            if (g == 0) {
-                lds_m[wave][r * 16 + col] = rows[r].m;
-                lds_l[wave][r * 16 + col] = l;
+            if (owner) {
+                sh.m[wave][r * kCols + col] = rows[r].m;
+                sh.l[wave][r * kCols + col] = l;
             }
         }
         __syncthreads();
         const bool whole = ex.splits == 1;
         const int64_t unit = ((int64_t)seq * a.c.n_kv + head) * n_rb + rb;
-        const int64_t rec_size = record_floats(rec_rows, NB);
-        float* rec = records + (unit * max_splits + split) * rec_size;
-        const int64_t E = (int64_t)rec_rows * D;  // floats of a record's accumulators
-        if (threadIdx.x < kRows) {
-            const int r = threadIdx.x;
-            float m = lds_m[0][r];
-            for (int w = 1; w < kWaves; ++w) m = fmaxf(m, lds_m[w][r]);
-            float l = 0.0f;
-            for (int w = 0; w < kWaves; ++w) {
-                const float f = part_weight(lds_m[w][r], m);
-                lds_w[w][r] = f;
-                l += lds_l[w][r] * f;
-            }
-            lds_inv[r] = 1.0f / l;
-            if (!whole && r < rec_rows) {
-                agent_store(rec + E + r, m);
-                agent_store(rec + E + rec_rows + r, l);
-            }
-        }
-        __syncthreads();
-        const auto store_out = [&](int row, int d, v4f x) {  // 4 values of a row of the block
-            const int flag = lds_flag[row];
-            if (flag == 1) x = v4f{0.f, 0.f, 0.f, 0.f};
-            if (flag == 2) x = v4f{0.f, 0.f, 0.f, 0.f} + __builtin_nanf("");
-            const int abs_row = rb * kRows + row;
-            const int j = abs_row / a.group, qh = head * a.group + abs_row - j * a.group;
-            float* o = a.O + ((int64_t)seq * a.tokens + j) * a.o_stride + (int64_t)qh * D + d;
-            *reinterpret_cast<f4u*>(o) = f4u{x[0], x[1], x[2], x[3]};
-        };
+        float* const rec = records + (unit * max_splits + split_no) * record_floats(rec_rows, NB);
+        float wave_max[RT];
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-            const float f = lds_w[wave][r * 16 + col];
-            float* o = lds_o + (wave * 16 + col) * kPitch + 8 * g;
+            const int i = r * kCols + col;
+            float m = sh.m[0][i];
+            for (int w = 1; w < kWaves; ++w) m = fmaxf(m, sh.m[w][i]);
+            wave_max[r] = m;
+        }
+        if (threadIdx.x < kRows) {
+            const int r = threadIdx.x;
+            float m = sh.m[0][r], l = 0.0f;
+            for (int w = 1; w < kWaves; ++w) m = fmaxf(m, sh.m[w][r]);
+            for (int w = 0; w < kWaves; ++w) l += sh.l[w][r] * part_weight(sh.m[w][r], m, c);
+            sh.inv[r] = 1.0f / l;
+            if (!whole && r < rec_rows) {
+                rec[rec_rows * D + r] = m;
+                rec[rec_rows * D + rec_rows + r] = l;
+            }
+        }
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
+        for (int r = 0; r < RT; ++r) {
+            const float f = part_weight(rows[r].m, wave_max[r], c);
+            float* o = &sh.o[wave][col][8 * g];
 #pragma unroll
-                for (int i = 0; i < 4; i += 2) {
-                    const v4f x = {rows[r].o[b][0][i], rows[r].o[b][1][i], rows[r].o[b][0][i + 1],
-                                   rows[r].o[b][1][i + 1]};
-                    *reinterpret_cast<v4f*>(o + 32 * b + 2 * i) = x * f;
+            for (int b = 0; b < NB; ++b) {
+                v4f x = rows[r].o[b][0] * f, y = rows[r].o[b][1] * f;
+                if constexpr (F == kFolded) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        x[i] = add_ror8(x[i]);
+                        y[i] = add_ror8(y[i]);
+                    }
                 }
+                // folded: columns c and c + 8 hold the same; each writes half
+                if (F == kWide || (lane & 8) == 0)
+                    *reinterpret_cast<v4f*>(o + 32 * b) = v4f{x[0], y[0], x[1], y[1]};
+                if (F == kWide || (lane & 8) != 0)
+                    *reinterpret_cast<v4f*>(o + 32 * b + 4) = v4f{x[2], y[2], x[3], y[3]};
+            }
             __syncthreads();
-            const int here = min(16, min(kRows, n_rows - rb * kRows) - r * 16);  // rows of this tile
+            const int here = min(kCols, n_rows - rb * kRows - r * kCols);  // rows of this tile
             for (int u = threadIdx.x; u < here * (D / 4); u += kThreads) {
                 const int row = u / (D / 4), d = (u - row * (D / 4)) * 4;
-                v4f x = *reinterpret_cast<const v4f*>(lds_o + row * kPitch + d);
+                v4f x = *reinterpret_cast<const v4f*>(&sh.o[0][row][d]);
 #pragma unroll
                 for (int w = 1; w < kWaves; ++w)
-                    x += *reinterpret_cast<const v4f*>(lds_o + (w * 16 + row) * kPitch + d);
+                    x += *reinterpret_cast<const v4f*>(&sh.o[w][row][d]);
+                const int i = r * kCols + row;
                 if (whole) {
-                    store_out(r * 16 + row, d, x * lds_inv[r * 16 + row]);
+                    const int abs_row = rb * kRows + i;
+                    const int j = abs_row / a.group, qh = head * a.group + abs_row - j * a.group;
+                    const v4f y = flagged(x * sh.inv[i], sh.flag[i]);
+                    *reinterpret_cast<f4u*>(a.O + ((int64_t)seq * a.tokens + j) * a.o_stride +
+                                            (int64_t)qh * D + d) = f4u{y[0], y[1], y[2], y[3]};
                 } else {
-                    const int64_t v = (int64_t)(r * 16 + row) * (D / 4) + d / 4;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) agent_store(rec + k * (E / 4) + v, x[k]);
+                    *reinterpret_cast<f4u*>(rec + i * D + d) = f4u{x[0], x[1], x[2], x[3]};
                 }
             }
             __syncthreads();
         }
-        if (whole) continue;
-
-        // ---- join the splits: the last workgroup to finish, in their order
-        wait_for_own_stores();
-        __syncthreads();
-        if (threadIdx.x == 0)
-            lds_last = __hip_atomic_fetch_add(counters + unit, 1u, __ATOMIC_RELAXED,
-                                              __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)ex.splits - 1;
-        __syncthreads();
-        if (!lds_last) continue;
-        const float* base = records + unit * max_splits * rec_size;
-        if (threadIdx.x < rec_rows) {
-            const int r = threadIdx.x;
-            float m = -__builtin_inff();
-            for (int i = 0; i < ex.splits; ++i) {
-                const float mi = agent_load(base + i * rec_size + E + r);
-                lds_w[i][r] = mi;
-                m = fmaxf(m, mi);
-            }
-            float l = 0.0f;
-            for (int i = 0; i < ex.splits; ++i) {
-                const float f = part_weight(lds_w[i][r], m);
-                lds_w[i][r] = f;
-                l += agent_load(base + i * rec_size + E + rec_rows + r) * f;
-            }
-            lds_inv[r] = 1.0f / l;
-        }
-        __syncthreads();
-        const int live = min(kRows, n_rows - rb * kRows);
-        for (int u = threadIdx.x; u < live * (D / 4); u += kThreads) {
-            const int row = u / (D / 4), d = (u - row * (D / 4)) * 4;
-            const float* p = base + u;
-            v4f x = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-            for (int i = 0; i < ex.splits; ++i) {
-                const v4f y = {agent_load(p + i * rec_size), agent_load(p + i * rec_size + E / 4),
-                               agent_load(p + i * rec_size + E / 2), agent_load(p + i * rec_size + 3 * (E / 4))};
-                x += y * lds_w[i][row];
-            }
-            store_out(row, d, x * lds_inv[row]);
-        }
-        if (threadIdx.x == 0)
-            __hip_atomic_store(counters + unit, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __syncthreads();
     }
 }
 
-// Column tiles of a workgroup: two for more than 16 query rows where the
-// registers hold them (head_dim <= 128).
-int row_tiles(int nb, int rows) { return rows > 16 && nb <= 4 ? 2 : 1; }
+// Join the splits of the units that have several, in their order: a
+// workgroup a unit and row.  Its threads are D/4 lanes of 4 values by
+// 256 / (D/4) parts of the splits; the parts are added in order in LDS.
+constexpr int kJoinThreads = 256;
+
+__global__ void __launch_bounds__(kJoinThreads)
+kv4_join_kernel(AttendArgs a, int n_rb, int per_wg, int rec_rows, int max_splits) {
+    __shared__ float weight[kMaxSplits];
+    __shared__ float total;
+    __shared__ __align__(16) float part[kJoinThreads * 4];
+    const int D = a.c.nb * 32, lanes = D / 4, parts = kJoinThreads / lanes;
+    const int64_t unit = blockIdx.x;
+    const int row = blockIdx.y, lane = threadIdx.x & 63;
+    const int rb = (int)(unit % n_rb);
+    const int head = (int)(unit / n_rb % a.c.n_kv), seq = (int)(unit / n_rb / a.c.n_kv);
+    const int abs_row = rb * per_wg + row;
+    if (abs_row >= a.tokens * a.group) return;
+    const Extent ex = extent_of(a, seq);
+    if (ex.splits == 1) return;
+    const int64_t size = record_floats(rec_rows, a.c.nb);
+    const float* rec = reinterpret_cast<const float*>(a.workspace) + unit * max_splits * size;
+    const int d = (int)threadIdx.x % lanes, p = (int)threadIdx.x / lanes;
+    if (threadIdx.x < 64) {
+        float m = -__builtin_inff(), l = 0.0f;
+        if (lane < ex.splits) {
+            m = rec[lane * size + rec_rows * D + row];
+            l = rec[lane * size + rec_rows * D + rec_rows + row];
+        }
+        float top = m;
+#pragma unroll
+        for (int k = 1; k < 64; k <<= 1) top = fmaxf(top, __shfl_xor(top, k));
+        const float w = part_weight(m, top, a.scale_log2);
+        l *= w;
+#pragma unroll
+        for (int k = 1; k < 64; k <<= 1) l += __shfl_xor(l, k);
+        weight[lane] = w;
+        if (lane == 0) total = l;
+    }
+    __syncthreads();
+    v4f x = {0.f, 0.f, 0.f, 0.f};
+    if (p < parts) {
+        const int i0 = ex.splits * p / parts, i1 = ex.splits * (p + 1) / parts;
+#pragma unroll 4
+        for (int i = i0; i < i1; ++i)
+            x += *reinterpret_cast<const f4u*>(rec + i * size + row * D + 4 * d) * weight[i];
+    }
+    *reinterpret_cast<v4f*>(part + 4 * threadIdx.x) = x;
+    __syncthreads();
+    if (p != 0) return;
+    for (int k = 1; k < parts; ++k) x += *reinterpret_cast<const v4f*>(part + 4 * (k * lanes + d));
+    const int j = abs_row / a.group, qh = head * a.group + abs_row - j * a.group;
+    const int64_t t = (int64_t)seq * a.tokens + j;
+    const int flag = row_flag(a.pos[t], a.batch_index[t], ex.slot, a.c.n_slots,
+                              a.c.max_pages * a.c.page_tokens);
+    const v4f y = flagged(x * (1.0f / total), flag);
+    *reinterpret_cast<f4u*>(a.O + t * a.o_stride + (int64_t)qh * D + 4 * d) = f4u{y[0], y[1], y[2], y[3]};
+}
 
 struct Plan {
-    int rt, n_rb, rec_rows, max_splits;
+    int rt, per_wg, n_rb, rec_rows, max_splits;
+    bool folded;
     int64_t units;
 };
 
+// Up to 8 rows: folded.  More than 16: two column tiles a workgroup where the
+// registers hold them (head_dim <= 128).
 Plan plan_attend(int n_kv, int nb, int64_t capacity, int n_seq, int tokens, int group) {
     Plan p;
     const int rows = tokens * group;
-    p.rt = row_tiles(nb, rows);
-    p.n_rb = (rows + 16 * p.rt - 1) / (16 * p.rt);
-    p.rec_rows = rows < 16 * p.rt ? rows : 16 * p.rt;
+    p.folded = rows <= 8;
+    p.rt = rows > 16 && nb <= 4 ? 2 : 1;
+    p.per_wg = (p.folded ? 8 : 16) * p.rt;
+    p.n_rb = (rows + p.per_wg - 1) / p.per_wg;
+    p.rec_rows = rows < p.per_wg ? rows : p.per_wg;
     p.max_splits = splits_of((int)((capacity + kKvTile - 1) / kKvTile));
     p.units = (int64_t)n_seq * n_kv * p.n_rb;
     return p;
@@ -643,25 +824,26 @@ template <int NB>
 void launch(const Plan& p, const AttendArgs& a, unsigned grid, hipStream_t st) {
     if constexpr (NB <= 4) {
         if (p.rt == 2) {
-            hipLaunchKernelGGL((kv4_attend_kernel<NB, 2>), dim3(grid), dim3(kThreads), 0, st, a, p.n_rb,
-                               p.rec_rows, p.max_splits);
+            hipLaunchKernelGGL((kv4_attend_kernel<NB, 2, kWide>), dim3(grid), dim3(64 * waves_of(NB)), 0, st, a,
+                               p.n_rb, p.rec_rows, p.max_splits);
             return;
         }
     }
-    hipLaunchKernelGGL((kv4_attend_kernel<NB, 1>), dim3(grid), dim3(kThreads), 0, st, a, p.n_rb,
-                       p.rec_rows, p.max_splits);
+    if (p.folded)
+        hipLaunchKernelGGL((kv4_attend_kernel<NB, 1, kFolded>), dim3(grid), dim3(64 * waves_of(NB)), 0, st, a,
+                           p.n_rb, p.rec_rows, p.max_splits);
+    else
+        hipLaunchKernelGGL((kv4_attend_kernel<NB, 1, kWide>), dim3(grid), dim3(64 * waves_of(NB)), 0, st, a,
+                           p.n_rb, p.rec_rows, p.max_splits);
 }
 
 }  // namespace
 
-int64_t kv4_attend_units(int n_kv, int nb, int n_seq, int tokens, int group) {
-    return plan_attend(n_kv, nb, 1, n_seq, tokens, group).units;
-}
-
 size_t kv4_attend_workspace(int n_kv, int nb, int64_t capacity, int n_seq, int tokens, int group) {
     const Plan p = plan_attend(n_kv, nb, capacity, n_seq, tokens, group);
     const size_t recs = p.max_splits > 1 ? (size_t)(p.units * p.max_splits) : 0;
-    return kCounterBytes + recs * record_floats(p.rec_rows, nb) * sizeof(float);
+    const size_t bytes = recs * (size_t)record_floats(p.rec_rows, nb) * sizeof(float);
+    return bytes > 0 ? bytes : 16;  // 0 stands for invalid arguments
 }
 
 hipError_t launch_kv4_attend(const AttendArgs& a, hipStream_t st) {
@@ -680,6 +862,10 @@ hipError_t launch_kv4_attend(const AttendArgs& a, hipStream_t st) {
         case 8: launch<8>(p, a, grid, st); break;
         default: return hipErrorInvalidValue;
     }
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.max_splits == 1) return e;
+    hipLaunchKernelGGL(kv4_join_kernel, dim3((unsigned)p.units, (unsigned)p.rec_rows), dim3(kJoinThreads),
+                       0, st, a, p.n_rb, p.per_wg, p.rec_rows, p.max_splits);
     return hipGetLastError();
 }
 

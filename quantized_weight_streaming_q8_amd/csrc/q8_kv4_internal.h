@@ -1,28 +1,27 @@
 // q8_kv4_internal.h -- the 4-bit cache's page layout and the launchers of
 // the rotary, append, read and attention kernels.
 //
-// Page layout (private).  Per key/value head, one after the other (T
-// positions a page, D = 32 NB values a head):
+// Page layout (private).  Per key/value head, one after the other, groups of
+// 32 positions (D = 32 NB values a head), each group one contiguous piece that
+// a wave brings to LDS as it stands:
 //
-//   K codes, T * D/2 bytes, in tiles of 16 positions.  A tile is the A operand
+//   K codes, 512 NB bytes, in two tiles of 16 positions.  A tile is the A operand
 //     of v_mfma_f32_16x16x32_bf16 for NB blocks: lane (r = position & 15,
 //     g = 0..3) takes values 8g .. 8g+7 of each block, 4 bytes, low nibble
-//     first.  The blocks of a lane lie side by side, four to a 16-byte load:
+//     first.  The blocks of a lane lie side by side, four to a 16-byte read:
 //     byte  q*1024 + (16g + r)*W + 4*(b & 3)   of the tile, q = b / 4 and W =
 //     4 * (blocks of this quad, 4 but for the last).
-//   V codes, T * D/2 bytes, in groups of 32 positions.  A group is the A
-//     operand (V transposed) of NB pairs of the same instruction, with the
-//     32 positions along k: lane (c = 0..15, g) takes values 2c and 2c+1 (the
-//     two nibbles of a byte) of each block at 8 positions, byte j = 0..7 for
-//     position 16*(j >> 2) + 4g + (j & 3): the order in which the 16x16 tiles
-//     of scores lie in the lanes, so that they are the B operand as they
-//     stand.  Two blocks to a 16-byte load:
+//   V codes, 512 NB bytes: the A operand (V transposed) of NB pairs of the
+//     same instruction, with the 32 positions along k: lane (c = 0..15, g)
+//     takes values 2c and 2c+1 (the two nibbles of a byte) of each block at 8
+//     positions, byte j = 0..7 for position 16*(j >> 2) + 4g + (j & 3): the
+//     order in which the 16x16 tiles of scores lie in the lanes, so that they
+//     are the B operand as they stand.  Two blocks to a 16-byte read:
 //     byte  p*1024 + (16g + c)*W + 8*(b & 1) + j,  p = b / 2, W = 8 * (blocks
 //     of this pair, 2 but for the last).
-//   K scales, T * SP bytes, SP = NB rounded up to a power of two: byte b of a
+//   K scales, 32 SP bytes, SP = NB rounded up to a power of two: byte b of a
 //     position's SP bytes.
-//   V scales, T * NB bytes, in groups of 32 positions: byte g*8NB + 8b + j,
-//     j as above.
+//   V scales, 32 NB bytes: byte g*8NB + 8b + j, j as above.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -40,38 +39,37 @@ __host__ __device__ constexpr int scale_pitch(int nb) {
     return nb <= 1 ? 1 : nb <= 2 ? 2 : nb <= 4 ? 4 : 8;
 }
 
-// Bytes of one head's part of a page, and the starts of its four regions.
-struct HeadLayout {
-    int64_t v, ks, vs, bytes;
-};
-__host__ __device__ constexpr HeadLayout head_layout(int nb, int page_tokens) {
-    const int64_t codes = (int64_t)page_tokens * nb * 16;
-    const int64_t ks = (int64_t)page_tokens * scale_pitch(nb);
-    // rounded up, so that every head's codes start on 16 bytes
-    const int64_t all = 2 * codes + ks + (int64_t)page_tokens * nb;
-    return {codes, 2 * codes, 2 * codes + ks, (all + 15) / 16 * 16};
+// Starts of a group's parts, and its bytes (a multiple of 32).
+__host__ __device__ constexpr int group_v(int nb) { return 512 * nb; }
+__host__ __device__ constexpr int group_ks(int nb) { return 1024 * nb; }
+__host__ __device__ constexpr int group_vs(int nb) { return 1024 * nb + 32 * scale_pitch(nb); }
+__host__ __device__ constexpr int group_bytes(int nb) { return group_vs(nb) + 32 * nb; }
+__host__ __device__ constexpr int64_t head_bytes(int nb, int page_tokens) {
+    return (int64_t)(page_tokens / kKvTile) * group_bytes(nb);
 }
 
-// Offset, in a head's K codes, of the 4 bytes of segment g (8 values) of
-// block b at position t of the page.
+// Offsets in a head's part of a page, t = position of the page.
+// The 4 bytes of K codes of segment g (8 values) of block b:
 __host__ __device__ constexpr int64_t k_code_offset(int nb, int t, int b, int g) {
     const int q = b >> 2, in_quad = nb - 4 * q < 4 ? nb - 4 * q : 4;
-    return (int64_t)(t >> 4) * (256 * nb) + q * 1024 + (g * 16 + (t & 15)) * (4 * in_quad) + 4 * (b & 3);
+    return (int64_t)(t >> 5) * group_bytes(nb) + (t >> 4 & 1) * (256 * nb) + q * 1024 +
+           (g * 16 + (t & 15)) * (4 * in_quad) + 4 * (b & 3);
 }
-// j (byte of a lane's 8) and g (lane quarter) of a position in its group of 32
+// j (byte of a lane's 8) and g (lane quarter) of a position in its group
 __host__ __device__ constexpr int v_byte(int t) { return ((t >> 4 & 1) << 2) | (t & 3); }
 __host__ __device__ constexpr int v_quarter(int t) { return t >> 2 & 3; }
-// Offset, in a head's V codes, of the byte with values 2c and 2c+1 of block b.
+// The byte of V codes with values 2c and 2c+1 of block b:
 __host__ __device__ constexpr int64_t v_code_offset(int nb, int t, int b, int c) {
     const int p = b >> 1, in_pair = nb - 2 * p < 2 ? nb - 2 * p : 2;
-    return (int64_t)(t >> 5) * (512 * nb) + p * 1024 + (v_quarter(t) * 16 + c) * (8 * in_pair) +
-           8 * (b & 1) + v_byte(t);
+    return (int64_t)(t >> 5) * group_bytes(nb) + group_v(nb) + p * 1024 +
+           (v_quarter(t) * 16 + c) * (8 * in_pair) + 8 * (b & 1) + v_byte(t);
 }
 __host__ __device__ constexpr int64_t k_scale_offset(int nb, int t, int b) {
-    return (int64_t)t * scale_pitch(nb) + b;
+    return (int64_t)(t >> 5) * group_bytes(nb) + group_ks(nb) + (t & 31) * scale_pitch(nb) + b;
 }
 __host__ __device__ constexpr int64_t v_scale_offset(int nb, int t, int b) {
-    return (int64_t)(t >> 5) * (32 * nb) + v_quarter(t) * (8 * nb) + 8 * b + v_byte(t);
+    return (int64_t)(t >> 5) * group_bytes(nb) + group_vs(nb) + v_quarter(t) * (8 * nb) + 8 * b +
+           v_byte(t);
 }
 
 // The cache as the kernels take it.
@@ -120,9 +118,7 @@ struct AttendArgs {
     uint8_t* workspace;
 };
 size_t kv4_attend_workspace(int n_kv, int nb, int64_t capacity, int n_seq, int tokens, int group);
-// Row blocks of all sequences and heads (the workspace has a counter for each).
-int64_t kv4_attend_units(int n_kv, int nb, int n_seq, int tokens, int group);
-constexpr int64_t kMaxUnits = int64_t(1) << 18;
+constexpr int64_t kMaxRowBlocks = int64_t(1) << 18;  // of 8 rows, all sequences and heads
 hipError_t launch_kv4_attend(const AttendArgs& a, hipStream_t st);
 
 }  // namespace q8

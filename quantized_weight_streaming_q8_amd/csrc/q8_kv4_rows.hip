@@ -171,7 +171,6 @@ kv4_append_kernel(KvView c, const float* q, const float* __restrict__ k, const f
     if (pg < 0) return;  // the whole workgroup
     fill_angles(cs, r, p);
     const int tok = p % c.page_tokens;
-    const HeadLayout hl = head_layout(c.nb, c.page_tokens);
     const int per_head = D / 4, heads_units = c.n_kv * per_head;  // units: 4 values
     const int u0 = ((int)blockIdx.y - q_wgs) * kv_per_wg, u1 = min(2 * heads_units, u0 + kv_per_wg);
     // u1 - u0 is a multiple of 8: the 8 lanes of a block leave the loop together
@@ -208,16 +207,16 @@ kv4_append_kernel(KvView c, const float* q, const float* __restrict__ k, const f
         const int b = d >> 5, l = (d & 31) >> 2;  // block of the head, lane of the block
         uint8_t* head = c.pages + pg * c.page_bytes + h * c.head_bytes;
         if (is_v) {
-            uint8_t* o = head + hl.v + v_code_offset(c.nb, tok, b, 2 * l);
+            uint8_t* o = head + v_code_offset(c.nb, tok, b, 2 * l);
             const int w = 8 * min(2, c.nb - (b & ~1));  // bytes from c to c + 1
             o[0] = (uint8_t)code;
             o[w] = (uint8_t)(code >> 8);
-            if (l == 0) head[hl.vs + v_scale_offset(c.nb, tok, b)] = (uint8_t)s;
+            if (l == 0) head[v_scale_offset(c.nb, tok, b)] = (uint8_t)s;
         } else {
             code |= __shfl_down(code, 1, 8) << 16;
             if ((l & 1) == 0)
                 *reinterpret_cast<uint32_t*>(head + k_code_offset(c.nb, tok, b, l >> 1)) = code;
-            if (l == 0) head[hl.ks + k_scale_offset(c.nb, tok, b)] = (uint8_t)s;
+            if (l == 0) head[k_scale_offset(c.nb, tok, b)] = (uint8_t)s;
         }
     }
 }
@@ -240,19 +239,18 @@ kv4_read_kernel(KvView c, const int32_t* __restrict__ batch_index, const int32_t
     const float nan = __builtin_nanf("");
     f4u y = {nan, nan, nan, nan};
     if (pg >= 0) {
-        const HeadLayout hl = head_layout(c.nb, c.page_tokens);
-        const uint8_t* head = c.pages + pg * c.page_bytes + h * c.head_bytes;
+            const uint8_t* head = c.pages + pg * c.page_bytes + h * c.head_bytes;
         const int tok = p % c.page_tokens, b = d >> 5, l = (d & 31) >> 2;
         uint32_t code;
         int s;
         if (is_v) {
-            const uint8_t* o = head + hl.v + v_code_offset(c.nb, tok, b, 2 * l);
+            const uint8_t* o = head + v_code_offset(c.nb, tok, b, 2 * l);
             code = o[0] | (uint32_t)o[8 * min(2, c.nb - (b & ~1))] << 8;
-            s = head[hl.vs + v_scale_offset(c.nb, tok, b)];
+            s = head[v_scale_offset(c.nb, tok, b)];
         } else {
             code = *reinterpret_cast<const uint16_t*>(head + k_code_offset(c.nb, tok, b, l >> 1) +
                                                       2 * (l & 1));
-            s = head[hl.ks + k_scale_offset(c.nb, tok, b)];
+            s = head[k_scale_offset(c.nb, tok, b)];
         }
         if (s != kNanByte) {
             const float unit = __uint_as_float((uint32_t)s << 23);

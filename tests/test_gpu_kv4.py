@@ -399,9 +399,9 @@ def test_attend_idle_and_bad_rows(q8, tokens, group):
         assert (got[4 * t] == 0).all() and np.isnan(got[4 * t + 2]).all()
         for j in (1, 3):
             assert (np.abs(got[4 * t + j] - want[4 * t + j]) <= tol[4 * t + j]).all()
-    # every workspace counter is back at zero and the call repeats
+    # the call repeats, whatever the workspace holds
+    s.ws.fill_(255)
     assert np.array_equal(s.run(), got, equal_nan=True)
-    assert not s.ws[:1 << 20].any()
 
 
 def test_attend_nan_in_sight_and_out_of_sight(q8):

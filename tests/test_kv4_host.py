@@ -189,7 +189,7 @@ def test_attend_refuses(q8):
     assert ws(None, 16, 1, 40) == 0
     for n, t, h in ((0, 1, 40), (16, 0, 40), (16, 65, 40), (16, 1, 39), (16, 1, 0), (4097, 1, 40)):
         assert ws(A(c), n, t, h) == 0, (n, t, h)
-    # more row blocks than the workspace has counters for
+    # more than 2^18 row blocks
     many = _cache(q8, n_kv_heads=1024, n_pages=1)
     assert ws(A(many), 4096, 64, 8192) == 0
 
@@ -198,8 +198,9 @@ def test_attend_workspace_grows_with_the_context(q8):
     ws = q8.library().q8_kv4_attend_workspace_bytes
     A = ctypes.addressof
     sizes = [ws(A(_cache(q8, max_pages=n)), 16, 1, 40) for n in (1, 8, 9, 100, 1000, 100000)]
-    assert sizes[0] == sizes[1] < sizes[2] <= sizes[3] < sizes[4] == sizes[5]
-    assert sizes[0] == 1 << 20   # one split: counters alone
+    assert sizes[0] == sizes[1] == 16   # one split: nothing to leave there
+    assert sizes[1] < sizes[2] <= sizes[3] < sizes[4] <= sizes[5]
+    assert ws(A(_cache(q8, max_pages=1 << 20)), 16, 1, 40) == sizes[5]
 
 
 # --------------------------------------------------------- binding checks
