@@ -185,10 +185,12 @@ size_t q8_kv4_attend_workspace_bytes(const q8_kv4_cache* cache, int n_seq, int t
  * in its 32 outputs.  NaN at positions that a row does not see does not reach
  * it.
  *
- * Arithmetic: the codes, Q and the softmax weights enter the matrix
- * instructions as exact sums of bf16 pieces, so every product is exact, and
- * all sums, maxima and weights are fp32.  The context of a sequence is cut
- * into splits by its own positions only, and the partial results are added
+ * Arithmetic: the cache's values, Q (to 2^-29 of the largest of each 32
+ * values of a head, and no finer than 2^-78) and the softmax weights enter the
+ * matrix instructions as sums of short pieces, so that products have no
+ * error; all sums, maxima and weights are fp32.  A NaN or an infinity in Q
+ * gives a NaN row.  The
+ * context of a sequence is cut into splits by its own positions only, and the partial results are added
  * in the order of the splits: a sequence's rows come out bit for bit the same
  * whatever else is in the batch, and in every call.
  *
@@ -198,8 +200,8 @@ size_t q8_kv4_attend_workspace_bytes(const q8_kv4_cache* cache, int n_seq, int t
  * run at the same time.
  *
  * 1 <= n_seq <= Q8_KV4_MAX_SEQS, 1 <= tokens_per_seq <= Q8_KV4_MAX_TOKENS,
- * n_q_heads a multiple of n_kv_heads, at most 8192; window >= 0; scale finite
- * and > 0; q_stride and o_stride at least n_q_heads * head_dim, rows times
+ * n_q_heads a multiple of n_kv_heads, at most 8192; window >= 0; 0 < scale <=
+ * 2^40; q_stride and o_stride at least n_q_heads * head_dim, rows times
  * stride <= 2^40; Q, O, batch_index and pos 4-byte aligned; O must not
  * overlap Q. */
 q8_status q8_kv4_attend(const q8_kv4_cache* cache, const float* Q, int64_t q_stride, int n_seq,

@@ -173,7 +173,7 @@ q8_status q8_kv4_attend(const q8_kv4_cache* cache, const float* Q, int64_t q_str
                         void* workspace, size_t workspace_bytes, hipStream_t stream) {
     if (!valid_attend_shape(cache, n_seq, tokens_per_seq, n_q_heads) || !valid_cache(cache) ||
         !aligned(Q, 4) || !aligned(O, 4) || !aligned(batch_index, 4) || !aligned(pos, 4) ||
-        !(scale > 0.0f) || !std::isfinite(scale) || window < 0)
+        !(scale > 0.0f) || !(scale <= 1099511627776.0f) || window < 0)
         return Q8_ERR_INVALID_ARG;
     const int64_t rows = (int64_t)n_seq * tokens_per_seq;
     const int64_t width = (int64_t)n_q_heads * cache->head_dim;

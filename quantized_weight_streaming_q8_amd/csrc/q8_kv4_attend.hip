@@ -6,13 +6,16 @@
 // in one pass over the positions t, with m, l and O carried and rescaled when
 // the maximum grows.
 //
-// Exact products.  A code times its power-of-two scale has two significant
-// bits, so v_cvt_scalef32_pk_bf16_fp4 gives keys and values exactly in bf16.
-// q and the weights 2^(c (s - m)) are fp32 numbers of 24 bits: three bf16 pieces
-// of 8 bits by truncation, exactly.  Three matrix instructions instead of one
-// then give fp32 products without error, added in fp32.  The matrix cores have
-// the room: at head_dim 128 a wave's 32 positions cost 48 of them, 768 cycles
-// of a SIMD whose share of HBM brings those 4352 bytes in about 1650.
+// Products without error.  Keys go into the matrix cores as they are: the
+// scaled instructions take 4-bit codes with a power-of-two scale for each 32.
+// Their other operand is q as six 6-bit pieces (4 significant bits, a scale
+// of their own for each 32), which hold q to 2^-29 of its block's largest
+// value.  Values become exact bf16 (a code times its scale has two significant
+// bits; one instruction converts a pair); the weights 2^(c (s - m)) are fp32
+// numbers of 24 bits, three bf16 pieces of 8 bits exactly.  All sums are fp32.
+// The matrix cores have the room: at head_dim 128 and up to 8 query rows a
+// wave's 32 positions cost them 352 cycles of a SIMD whose share of HBM brings
+// those 4352 bytes in about 1650.
 //
 // Layout of the work.  S^T = K q^T puts positions in the rows of a 16x16 tile
 // and query rows in its columns: a lane holds one query row's scores at 4
@@ -48,6 +51,10 @@ constexpr int kNoVmem = 0x0f70;  // s_waitcnt vmcnt(0), no other count
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef float f4u __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+typedef uint32_t v6u __attribute__((ext_vector_type(6)));
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef float v32f __attribute__((ext_vector_type(32)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
 // Splits of a sequence of `tiles` steps of 32 positions: of 512 positions up
@@ -170,8 +177,9 @@ __device__ inline void read_words(const uint8_t* p, uint32_t* o) {
 // One step's operands of one wave: 32 positions of a head.
 template <int NB>
 struct Keys {
-    uint32_t c[2][NB];             // codes of the two 16-position tiles
-    uint32_t s[2][(NB + 3) / 4];   // scales
+    static constexpr int kQuads = (NB + 3) / 4;
+    u4 c[2][kQuads];        // codes of the two 16-position tiles, four blocks each
+    uint32_t s[kQuads];     // scales, the tiles' in bytes 0 and 1
 };
 template <int NB>
 struct Values {
@@ -181,18 +189,16 @@ struct Values {
 
 template <int NB>
 __device__ inline void read_keys(const uint8_t* slot, int lane, Keys<NB>& k) {
-    constexpr int SP = scale_pitch(NB);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const uint8_t* c = slot + h * 256 * NB;
+    for (int q = 0; q < Keys<NB>::kQuads; ++q) {
+        // lanes of blocks that are not there take any codes, at scale 1: the
+        // queries have zeros for them
+        const int b = 4 * q + (lane >> 4), here = min(b, NB - 1) * 16 + (lane & 15);
 #pragma unroll
-        for (int q = 0; q < NB / 4; ++q) read_words<4>(c + q * 1024 + lane * 16, &k.c[h][4 * q]);
-        if constexpr (NB % 4 != 0)
-            read_words<NB % 4>(c + (NB / 4) * 1024 + lane * (4 * (NB % 4)), &k.c[h][NB / 4 * 4]);
-        const uint8_t* s = slot + group_ks(NB) + (16 * h + (lane & 15)) * SP;
-        if constexpr (SP == 1) k.s[h][0] = *s;
-        else if constexpr (SP == 2) k.s[h][0] = *reinterpret_cast<const uint16_t*>(s);
-        else read_words<SP / 4>(s, k.s[h]);
+        for (int h = 0; h < 2; ++h)
+            k.c[h][q] = *reinterpret_cast<const u4*>(slot + h * 256 * NB + here * 16);
+        k.s[q] = *reinterpret_cast<const uint16_t*>(slot + group_ks(NB) + here * 2);
+        if (NB % 4 != 0 && b >= NB) k.s[q] = 0x7f7fu;
     }
 }
 
@@ -235,14 +241,14 @@ __device__ inline float max_over_quarters(float v) {
 }
 
 // How a column tile holds its rows.  kWide: 16 rows, an operand for each of the
-// three pieces.  kFolded, for at most 8 rows: columns c and c + 8 belong to one
-// row, the first operand has its upper piece in c and its middle one in
-// c + 8, the second its lower piece in c; two instructions instead of three.
-// Scores add up over the two columns; outputs do at the end.
+// pieces of a number.  kFolded, for at most 8 rows: columns c and c + 8 belong
+// to one row and hold two pieces, so that half the instructions do.  Scores
+// add up over the two columns; outputs do at the end.
 enum Fold { kWide, kFolded };
 
-// x as operands: N = 3 (wide) or 2 (folded) of 8 bf16, exactly.  Folded, every
-// lane is given its row's x, keep = 0xffff0000 in columns 8..15 and 0 in 0..7.
+// Weights as operands: N = 3 (wide) or 2 (folded: upper and middle piece, then
+// lower piece and nothing) of 8 bf16, exactly.  Folded, every lane is given
+// its row's x, keep = 0xffff0000 in columns 8..15 and 0 in 0..7.
 template <Fold F>
 __device__ inline void split(const float (&x)[8], uint32_t keep, u4 (&p)[F == kWide ? 3 : 2]) {
     if constexpr (F == kWide) {
@@ -263,38 +269,114 @@ __device__ inline void split(const float (&x)[8], uint32_t keep, u4 (&p)[F == kW
     }
 }
 
+// A lane's 32 query values of one block as pieces of 6 bits (E2M3: 4
+// significant bits, up to 7.5, in steps of at least 1/8).  Piece i is
+// what is left by the ones before it over 2^(e - kPieceDown[i]), rounded; e
+// puts the largest value at 3.75 .. 7.5.  A piece leaves at most half a step:
+// 1/4 of the first scale, which over the next is 4, and from there 1/8, again
+// 4 over the next.  Six leave less than 2^-29 of the largest value.
+//
+// The scores come out times 2^-kScoreShift, so that single pieces do not
+// overflow where their sum may not; pieces too small for the scale's range
+// then (below 2^-78) are dropped.  A NaN or infinity among the values makes
+// its block NaN.
+constexpr int kPieces = 6;
+constexpr int kPieceDown[kPieces] = {0, 4, 9, 14, 19, 24};
+constexpr int kScoreShift = 48;
+constexpr float kScoreUnit = 281474976710656.0f;  // 2^kScoreShift
+
+template <Fold F>
+struct Query {
+    static constexpr int P = F == kWide ? kPieces : kPieces / 2;  // operands
+    v6u p[P];               // folded: pieces 2i in columns 0..7 and 2i + 1 in 8..15
+    uint32_t s[(P + 3) / 4];  // their scale bytes, four to a word
+};
+
+template <Fold F>
+__device__ inline void make_query(float (&x)[32], uint32_t keep, Query<F>& q) {
+    uint32_t top = 0;  // of the magnitudes' bits: NaN and infinity are the largest
+#pragma unroll
+    for (int i = 0; i < 32; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+    const bool bad = top > 0x7f7fffffu;
+    // largest value / 2^e in 3.75 .. 7.5
+    const int e = max((int)(top >> 23) - 127 - 2 + ((top & 0x7fffffu) > 0x700000u ? 1 : 0), -100);
+#pragma unroll
+    for (int w = 0; w < (Query<F>::P + 3) / 4; ++w) q.s[w] = 0;
+#pragma unroll
+    for (int n = 0; n < kPieces; ++n) {
+        const int en = e - kPieceDown[n];
+        const float scale = __uint_as_float((uint32_t)(en + 127) << 23);
+        v16f even, odd;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            even[i] = x[2 * i];
+            odd[i] = x[2 * i + 1];
+        }
+        v6u f = __builtin_amdgcn_cvt_scalef32_2xpk16_fp6_f32(even, odd, scale);
+        const v32f back = __builtin_amdgcn_cvt_scalef32_pk32_f32_fp6(f, scale);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] -= back[i];
+        const int byte = en + 127 - kScoreShift;
+        const bool drop = byte < 1 && !bad;
+        const uint32_t sb = bad ? 255u : drop ? 1u : (uint32_t)byte;
+#pragma unroll
+        for (int i = 0; i < 6; ++i) f[i] = drop ? 0u : f[i];
+        const int o = F == kFolded ? n >> 1 : n;  // its operand
+        if (F == kWide || (n & 1) == 0) {
+            q.p[o] = f;
+            q.s[o >> 2] |= sb << (8 * (o & 3));
+        } else {  // columns 8..15 take this piece instead of the one before
+#pragma unroll
+            for (int i = 0; i < 6; ++i) q.p[o][i] = keep != 0 ? f[i] : q.p[o][i];
+            const uint32_t m = keep != 0 ? 0xffu << (8 * (o & 3)) : 0u;
+            q.s[o >> 2] = (q.s[o >> 2] & ~m) | (sb << (8 * (o & 3)) & m);
+        }
+    }
+}
+
 // Carried state of one column tile.
 template <int NB, Fold F>
 struct Rows {
-    static constexpr int P = F == kWide ? 3 : 2;
-    u4 q[NB][P];         // query operands
+    static constexpr int kQuads = (NB + 3) / 4;
+    Query<F> q[kQuads];
     v4f o[NB][2];        // O^T: dim 32b + 2(4g + i) + e in o[b][e][i]
-    float m, l;          // running maximum (of q.k) and this lane's share of the sum
+    float m, l;          // running maximum (of the scores) and this lane's share of the sum
     int lo, hi;          // positions this column sees
 };
 
+// 4-bit codes (tile H of a step) times 6-bit pieces (operand I of the queries).
+template <int H, int I>
+__device__ inline v4f mfma_scaled(u4 k, uint32_t ks, v6u q, uint32_t qs, v4f c) {
+    const v8i a = {(int)k[0], (int)k[1], (int)k[2], (int)k[3], 0, 0, 0, 0};
+    const v8i b = {(int)q[0], (int)q[1], (int)q[2], (int)q[3], (int)q[4], (int)q[5], 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 2, H, (int)ks, I, (int)qs);
+}
+
+template <int NB, int RT, Fold F, int I>
+__device__ inline void score_piece(const Keys<NB>& k, const Rows<NB, F> (&rows)[RT], int q, v4f (&S)[RT][2]) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        const Query<F>& y = rows[r].q[q];
+        S[r][0] = mfma_scaled<0, (I & 3)>(k.c[0][q], k.s[q], y.p[I], y.s[I >> 2], S[r][0]);
+        S[r][1] = mfma_scaled<1, (I & 3)>(k.c[1][q], k.s[q], y.p[I], y.s[I >> 2], S[r][1]);
+    }
+}
+
 template <int NB, int RT, Fold F>
 __device__ inline void scores(const Keys<NB>& k, const Rows<NB, F> (&rows)[RT], v4f (&S)[RT][2]) {
-    constexpr int P = Rows<NB, F>::P;
     const v4f zero = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int r = 0; r < RT; ++r) S[r][0] = S[r][1] = zero;
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        u4 a[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t sw = k.s[h][b / 4], w = k.c[h][b];
-            const float sc = (b & 3) == 0 ? scale_exp<0>(sw) : (b & 3) == 1 ? scale_exp<1>(sw)
-                             : (b & 3) == 2 ? scale_exp<2>(sw) : scale_exp<3>(sw);
-            a[h] = u4{dequant2<0>(w, sc), dequant2<1>(w, sc), dequant2<2>(w, sc), dequant2<3>(w, sc)};
+    for (int q = 0; q < Keys<NB>::kQuads; ++q) {  // small pieces first
+        if constexpr (F == kWide) {
+            score_piece<NB, RT, F, 5>(k, rows, q, S);
+            score_piece<NB, RT, F, 4>(k, rows, q, S);
+            score_piece<NB, RT, F, 3>(k, rows, q, S);
         }
-#pragma unroll
-        for (int i = P - 1; i >= 0; --i)
-#pragma unroll
-            for (int r = 0; r < RT; ++r)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) S[r][h] = mfma(a[h], rows[r].q[b][i], S[r][h]);
+        score_piece<NB, RT, F, 2>(k, rows, q, S);
+        score_piece<NB, RT, F, 1>(k, rows, q, S);
+        score_piece<NB, RT, F, 0>(k, rows, q, S);
     }
     if constexpr (F == kFolded) {
 #pragma unroll
@@ -356,7 +438,7 @@ __device__ inline void mask_step(Values<NB>& v, Rows<NB, F> (&rows)[RT], v4f (&S
 template <int NB, int RT, Fold F>
 __device__ inline void softmax_and_values(const Values<NB>& v, Rows<NB, F> (&rows)[RT], v4f (&S)[RT][2],
                                           float c, float lag, uint32_t keep) {
-    constexpr int P = Rows<NB, F>::P;
+    constexpr int P = F == kWide ? 3 : 2;
     u4 p[RT][P];
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
@@ -366,8 +448,18 @@ __device__ inline void softmax_and_values(const Values<NB>& v, Rows<NB, F> (&row
         t = max_over_quarters(t);
         // The maximum is raised only when it grew by more than 2^8: weights
         // up to 256 lose nothing in floating point, and most steps skip the rescaling.
-        const bool grow = t > rows[r].m + lag;
+        bool grow = t > rows[r].m + lag;
         if (__any(grow)) {
+            // scores beyond fp32's range without the shift are infinities
+            const float huge = __uint_as_float((uint32_t)(127 + 128 - kScoreShift) << 23);
+            if (__any(fabsf(t) >= huge)) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float y = S[r][i >> 2][i & 3];
+                    S[r][i >> 2][i & 3] = y >= huge ? __builtin_inff() : y <= -huge ? -__builtin_inff() : y;
+                }
+                t = t >= huge ? __builtin_inff() : t <= -huge ? -__builtin_inff() : t;
+            }
             const float m = grow ? t : rows[r].m;
             const float f = grow ? __builtin_amdgcn_exp2f((rows[r].m - m) * c) : 1.0f;
             rows[r].m = m;
@@ -485,7 +577,7 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int rec_rows, int max_splits) {
     using Sh = Shared<NB, RT, F>;
     constexpr int D = NB * 32;
     constexpr int kWaves = Sh::kWaves, kThreads = 64 * kWaves;
-    constexpr int kCols = Sh::kCols, kRows = Sh::kRows;
+    constexpr int kCols = Sh::kCols, kRows = Sh::kRows, kQuads = Keys<NB>::kQuads;
     __shared__ __align__(16) Sh sh;
 
     const int lane = threadIdx.x & 63;
@@ -493,7 +585,7 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int rec_rows, int max_splits) {
     const int col = F == kFolded ? lane & 7 : lane & 15, g = lane >> 4;
     const bool owner = F == kFolded ? (lane & 15) < 8 && g == 0 : g == 0;  // one lane of a row
     const uint32_t keep = lane & 8 ? 0xffff0000u : 0u;
-    const float c = a.scale_log2, lag = 8.0f / c;
+    const float c = a.scale_log2 * kScoreUnit, lag = 8.0f / c;
     const int n_rows = a.tokens * a.group;
     const int groups_per_page = a.c.page_tokens / kKvTile;
     const int cap = a.c.max_pages * a.c.page_tokens;
@@ -562,7 +654,7 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int rec_rows, int max_splits) {
         if (first < t1) ids = load_ids(page0);
         Rows<NB, F> rows[RT];
         int row_pos[RT], row_slot[RT];
-        f4u q_in[RT][NB][2];
+        f4u q_in[RT][kQuads][8];
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
             const int row = min(rb * kRows + r * kCols + col, n_rows - 1);  // past the last: that again
@@ -570,12 +662,12 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int rec_rows, int max_splits) {
             const int64_t t = (int64_t)seq * a.tokens + j;
             row_pos[r] = a.pos[t];
             row_slot[r] = a.batch_index[t];
-            const float* q = a.Q + t * a.q_stride + (int64_t)qh * D + 8 * g;
+            const float* q = a.Q + t * a.q_stride + (int64_t)qh * D;
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                q_in[r][b][0] = *reinterpret_cast<const f4u*>(q + 32 * b);
-                q_in[r][b][1] = *reinterpret_cast<const f4u*>(q + 32 * b + 4);
-            }
+            for (int k = 0; k < kQuads; ++k)  // block 4k + g
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    q_in[r][k][i] = *reinterpret_cast<const f4u*>(q + 32 * min(4 * k + g, NB - 1) + 4 * i);
         }
         // They are here before the groups set out, which come in behind them.
         __builtin_amdgcn_s_waitcnt(kNoVmem);
@@ -619,13 +711,15 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int rec_rows, int max_splits) {
             all_hi = min(all_hi, rows[r].hi);
             if (wave == 0 && owner) sh.flag[r * kCols + col] = flag;
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                float x[8];
+            for (int k = 0; k < kQuads; ++k) {
+                float x[32];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = flag == 0 ? q_in[r][b][i >> 2][i & 3] : 0.0f;
-                split<F>(x, keep, rows[r].q[b]);
-                rows[r].o[b][0] = rows[r].o[b][1] = v4f{0.f, 0.f, 0.f, 0.f};
+                for (int i = 0; i < 32; ++i)
+                    x[i] = flag == 0 && 4 * k + g < NB ? q_in[r][k][i >> 2][i & 3] : 0.0f;
+                make_query<F>(x, keep, rows[r].q[k]);
             }
+#pragma unroll
+            for (int b = 0; b < NB; ++b) rows[r].o[b][0] = rows[r].o[b][1] = v4f{0.f, 0.f, 0.f, 0.f};
         }
 #pragma unroll
         for (int d = 1; d < 16; d <<= 1) {
@@ -772,7 +866,7 @@ kv4_join_kernel(AttendArgs a, int n_rb, int per_wg, int rec_rows, int max_splits
         float top = m;
 #pragma unroll
         for (int k = 1; k < 64; k <<= 1) top = fmaxf(top, __shfl_xor(top, k));
-        const float w = part_weight(m, top, a.scale_log2);
+        const float w = part_weight(m, top, a.scale_log2 * kScoreUnit);
         l *= w;
 #pragma unroll
         for (int k = 1; k < 64; k <<= 1) l += __shfl_xor(l, k);

@@ -6,11 +6,9 @@
 // a wave brings to LDS as it stands:
 //
 //   K codes, 512 NB bytes, in two tiles of 16 positions.  A tile is the A operand
-//     of v_mfma_f32_16x16x32_bf16 for NB blocks: lane (r = position & 15,
-//     g = 0..3) takes values 8g .. 8g+7 of each block, 4 bytes, low nibble
-//     first.  The blocks of a lane lie side by side, four to a 16-byte read:
-//     byte  q*1024 + (16g + r)*W + 4*(b & 3)   of the tile, q = b / 4 and W =
-//     4 * (blocks of this quad, 4 but for the last).
+//     of v_mfma_scale_f32_16x16x128_f8f6f4 for four blocks at a time: lane (r =
+//     position & 15, g = 0..3) takes block 4q + g of a position, 16 bytes, low
+//     nibble first:  byte  b*256 + 16r  of the tile.
 //   V codes, 512 NB bytes: the A operand (V transposed) of NB pairs of the
 //     same instruction, with the 32 positions along k: lane (c = 0..15, g)
 //     takes values 2c and 2c+1 (the two nibbles of a byte) of each block at 8
@@ -19,8 +17,8 @@
 //     are the B operand as they stand.  Two blocks to a 16-byte read:
 //     byte  p*1024 + (16g + c)*W + 8*(b & 1) + j,  p = b / 2, W = 8 * (blocks
 //     of this pair, 2 but for the last).
-//   K scales, 32 SP bytes, SP = NB rounded up to a power of two: byte b of a
-//     position's SP bytes.
+//   K scales, 32 NB bytes: byte (16b + r)*2 + h for tile h = 0, 1 (the two
+//     tiles' scales of a lane side by side).
 //   V scales, 32 NB bytes: byte g*8NB + 8b + j, j as above.
 #pragma once
 
@@ -35,15 +33,11 @@ constexpr int kKvTile = 32;       // positions of one step of the attention
 constexpr int kScaleBias = 127;   // E8M0
 constexpr int kNanByte = 255;
 
-__host__ __device__ constexpr int scale_pitch(int nb) {
-    return nb <= 1 ? 1 : nb <= 2 ? 2 : nb <= 4 ? 4 : 8;
-}
-
-// Starts of a group's parts, and its bytes (a multiple of 32).
+// Starts of a group's parts, and its bytes (17 for 32 values).
 __host__ __device__ constexpr int group_v(int nb) { return 512 * nb; }
 __host__ __device__ constexpr int group_ks(int nb) { return 1024 * nb; }
-__host__ __device__ constexpr int group_vs(int nb) { return 1024 * nb + 32 * scale_pitch(nb); }
-__host__ __device__ constexpr int group_bytes(int nb) { return group_vs(nb) + 32 * nb; }
+__host__ __device__ constexpr int group_vs(int nb) { return 1056 * nb; }
+__host__ __device__ constexpr int group_bytes(int nb) { return 1088 * nb; }
 __host__ __device__ constexpr int64_t head_bytes(int nb, int page_tokens) {
     return (int64_t)(page_tokens / kKvTile) * group_bytes(nb);
 }
@@ -51,9 +45,8 @@ __host__ __device__ constexpr int64_t head_bytes(int nb, int page_tokens) {
 // Offsets in a head's part of a page, t = position of the page.
 // The 4 bytes of K codes of segment g (8 values) of block b:
 __host__ __device__ constexpr int64_t k_code_offset(int nb, int t, int b, int g) {
-    const int q = b >> 2, in_quad = nb - 4 * q < 4 ? nb - 4 * q : 4;
-    return (int64_t)(t >> 5) * group_bytes(nb) + (t >> 4 & 1) * (256 * nb) + q * 1024 +
-           (g * 16 + (t & 15)) * (4 * in_quad) + 4 * (b & 3);
+    return (int64_t)(t >> 5) * group_bytes(nb) + (t >> 4 & 1) * (256 * nb) + b * 256 + (t & 15) * 16 +
+           4 * g;
 }
 // j (byte of a lane's 8) and g (lane quarter) of a position in its group
 __host__ __device__ constexpr int v_byte(int t) { return ((t >> 4 & 1) << 2) | (t & 3); }
@@ -65,7 +58,8 @@ __host__ __device__ constexpr int64_t v_code_offset(int nb, int t, int b, int c)
            (v_quarter(t) * 16 + c) * (8 * in_pair) + 8 * (b & 1) + v_byte(t);
 }
 __host__ __device__ constexpr int64_t k_scale_offset(int nb, int t, int b) {
-    return (int64_t)(t >> 5) * group_bytes(nb) + group_ks(nb) + (t & 31) * scale_pitch(nb) + b;
+    return (int64_t)(t >> 5) * group_bytes(nb) + group_ks(nb) + (16 * b + (t & 15)) * 2 +
+           (t >> 4 & 1);
 }
 __host__ __device__ constexpr int64_t v_scale_offset(int nb, int t, int b) {
     return (int64_t)(t >> 5) * group_bytes(nb) + group_vs(nb) + v_quarter(t) * (8 * nb) + 8 * b +

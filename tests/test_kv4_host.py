@@ -38,10 +38,10 @@ def test_header_and_binding_agree(q8):
 
 
 def test_page_bytes(q8):
-    # 17 bytes per 32 values, the key scales padded to a power of two a position
+    # 17 bytes per 32 values
     for kv, d, t in ((8, 128, 64), (12, 64, 32), (1, 256, 4096), (3, 32, 32)):
         assert q8.q8_kv4_page_bytes(kv, d, t) == kv * t * 2 * (d // 2 + d // 32)
-    assert q8.q8_kv4_page_bytes(5, 96, 96) == 5 * 96 * (96 + 4 + 3)
+    assert q8.q8_kv4_page_bytes(5, 96, 96) == 5 * 96 * 2 * 3 * 17
     for bad in ((0, 128, 64), (1025, 128, 64), (8, 0, 64), (8, 48, 64), (8, 288, 64), (8, 128, 0),
                 (8, 128, 48), (8, 128, 4128), (-1, 128, 64)):
         assert q8.q8_kv4_page_bytes(*bad) == 0, bad
@@ -182,7 +182,7 @@ def test_attend_refuses(q8):
     _refuses(lib.q8_kv4_attend, ok,
              [(0, None), (1, None), (1, P + 2), (2, 5119), (2, 1 << 37), (3, 0), (3, 4097), (4, 0),
               (4, 65), (5, 0), (5, 41), (5, -8), (5, 8200), (6, None), (6, P + 2), (7, None),
-              (7, P + 2), (8, 0.0), (8, -1.0), (8, nan), (8, inf), (9, -1), (10, None), (10, P + 2),
+              (7, P + 2), (8, 0.0), (8, -1.0), (8, nan), (8, inf), (8, 1.2e12), (9, -1), (10, None), (10, P + 2),
               (11, 5119), (11, 1 << 37), (12, None), (12, P + 128), (13, need - 1), (13, 0)])
     _refuses(lib.q8_kv4_attend, ok, [(0, A(b)) for b in bad_caches])
     ws = lib.q8_kv4_attend_workspace_bytes
