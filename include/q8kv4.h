@@ -189,10 +189,9 @@ size_t q8_kv4_attend_workspace_bytes(const q8_kv4_cache* cache, int n_seq, int t
  * values of a head, and no finer than 2^-78) and the softmax weights enter the
  * matrix instructions as sums of short pieces, so that products have no
  * error; all sums, maxima and weights are fp32.  A NaN or an infinity in Q
- * gives a NaN row.  The
- * context of a sequence is cut into splits by its own positions only, and the partial results are added
- * in the order of the splits: a sequence's rows come out bit for bit the same
- * whatever else is in the batch, and in every call.
+ * gives a NaN row.  The positions of a sequence are divided by the lengths of
+ * the whole batch and the parts added in a fixed order: a call gives the same
+ * bits every time.
  *
  * workspace: device memory, 256-byte aligned, at least
  * q8_kv4_attend_workspace_bytes(...); its contents do not matter before a

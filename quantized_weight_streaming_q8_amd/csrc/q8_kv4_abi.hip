@@ -162,9 +162,12 @@ q8_status q8_kv4_read(const q8_kv4_cache* cache, const int32_t* batch_index, con
 size_t q8_kv4_attend_workspace_bytes(const q8_kv4_cache* cache, int n_seq, int tokens_per_seq,
                                      int n_q_heads) {
     if (!valid_attend_shape(cache, n_seq, tokens_per_seq, n_q_heads)) return 0;
-    return q8::kv4_attend_workspace(cache->n_kv_heads, cache->head_dim / 32,
-                                    (int64_t)cache->max_pages * cache->page_tokens, n_seq,
-                                    tokens_per_seq, n_q_heads / cache->n_kv_heads);
+    q8::AttendArgs a = {};
+    a.c = view(cache);
+    a.n_seq = n_seq;
+    a.tokens = tokens_per_seq;
+    a.group = n_q_heads / cache->n_kv_heads;
+    return q8::kv4_attend_workspace(a);
 }
 
 q8_status q8_kv4_attend(const q8_kv4_cache* cache, const float* Q, int64_t q_stride, int n_seq,

