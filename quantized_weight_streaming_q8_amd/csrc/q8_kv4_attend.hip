@@ -52,7 +52,7 @@ namespace {
 // Waves of a workgroup (2 for the heads whose slots of 4 would pass 64 KB).
 __host__ __device__ constexpr int waves_of(int nb) { return nb <= 4 ? 4 : 2; }
 constexpr int kMaxShares = 768;  // three workgroups on each of 256 CUs
-constexpr int kUnitCost = 4;
+constexpr int kUnitCost = 12;
 constexpr int kMinSteps = 8;
 constexpr int kNoVmem = 0x0f70;  // s_waitcnt vmcnt(0), no other count
 
@@ -123,7 +123,7 @@ __device__ inline uint32_t lds_address(const void* p) {
 
 // 64 lanes x 16 (4) bytes from base + voff to the LDS bytes from `lds` on.
 __device__ inline void lds_load16(uint32_t lds, const uint8_t* base, uint32_t voff) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt"
                  ::"s"(lds), "v"(voff), "s"(base) : "memory");
 }
 __device__ inline void lds_load4(uint32_t lds, const uint8_t* base, uint32_t voff) {
@@ -501,24 +501,32 @@ struct Extent {
     int lo, hi, tiles, slot;
 };
 
-__device__ inline Extent extent_of(const AttendArgs& a, int s) {
+__device__ inline int tiles_of(int lo, int hi) { return (hi + kKvTile - 1) / kKvTile - lo / kKvTile; }
+
+// Extents of the sequences s0 + lane / tp, tp a power of two at least
+// a.tokens: a lane a row, every lane gets its sequence's.
+__device__ inline Extent extent_of(const AttendArgs& a, int s0, int lane, int tp) {
     const int cap = a.c.max_pages * a.c.page_tokens;
-    int lo = INT32_MAX, hi = 0, slot = -1;
-    bool idle = true;
-    for (int j = 0; j < a.tokens; ++j) {
+    const int s = s0 + lane / tp, j = lane & (tp - 1);
+    int p = -1, own_slot = -1;
+    if (s < a.n_seq && j < a.tokens) {
         const int64_t t = (int64_t)s * a.tokens + j;
-        const int p = a.pos[t], own_slot = a.batch_index[t];
-        if (p < 0) continue;
-        if (idle) slot = own_slot;
-        idle = false;
-        if (p >= cap) continue;
-        hi = max(hi, p + 1);
-        lo = min(lo, a.window > 0 ? max(0, p + 1 - a.window) : 0);
+        p = a.pos[t];
+        own_slot = a.batch_index[t];
     }
-    if (slot < 0 || slot >= a.c.n_slots) hi = 0;
+    const bool counts = p >= 0 && p < cap;
+    int hi = counts ? p + 1 : 0;
+    int lo = !counts ? INT32_MAX : a.window > 0 ? max(0, p + 1 - a.window) : 0;
+    int first = p >= 0 ? lane : 64;  // lane of the sequence's first row that is not idle
+    for (int d = 1; d < tp; d <<= 1) {
+        hi = max(hi, __shfl_xor(hi, d));
+        lo = min(lo, __shfl_xor(lo, d));
+        first = min(first, __shfl_xor(first, d));
+    }
+    int slot = __shfl(own_slot, first & 63);
+    if (first == 64 || slot < 0 || slot >= a.c.n_slots) slot = first == 64 ? -1 : slot, hi = 0;
     if (hi == 0) lo = 0;
-    const int tiles = (hi + kKvTile - 1) / kKvTile - lo / kKvTile;
-    return {lo, hi, tiles, slot};
+    return {lo, hi, tiles_of(lo, hi), slot};
 }
 
 // 0: a row to compute, 1: idle (zeros), 2: outside the cache (NaN).
@@ -556,8 +564,9 @@ struct Room {
 
 // Extents of 64 sequences and the room up to each one's end.
 struct Sequences {
-    int64_t upto[64];
-    int lo[64], hi[64], tiles[64], slot[64];
+    int64_t upto[64];              // end to end
+    int even[64];                  // each unit on a share (held to 2^30: then it is not used)
+    int lo[64], hi[64], slot[64];
 };
 
 // What the main launch leaves at the start of the workspace for the join:
@@ -610,68 +619,67 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int rec_rows, float* records) {
     const int cap = a.c.max_pages * a.c.page_tokens;
     SequenceRoom* rooms = reinterpret_cast<SequenceRoom*>(a.workspace + sizeof(Layout));
 
-    // Each lane of the first wave measures one sequence.
+    // The room of sequences s0 .. s0 + 63, in either layout.
     const int units_per_seq = a.c.n_kv * n_rb;
-    Room lay = {true};
-    const auto measure = [&](int s0, bool extents) {
+    const int tp = a.tokens > 1 ? 1 << (32 - __builtin_clz(a.tokens - 1)) : 1;
+    const auto measure = [&](int s0) {
+        for (int r = wave; r * (64 / tp) < 64 && s0 + r * (64 / tp) < a.n_seq; r += kWaves) {
+            const Extent e = extent_of(a, s0 + r * (64 / tp), lane, tp);
+            const int i = r * (64 / tp) + lane / tp;
+            if ((lane & (tp - 1)) == 0) {
+                sh.seqs.lo[i] = e.lo;
+                sh.seqs.hi[i] = e.hi;
+                sh.seqs.slot[i] = e.slot;
+            }
+        }
+        __syncthreads();
         if (wave == 0) {
             const bool there = s0 + lane < a.n_seq;
-            int tiles = sh.seqs.tiles[lane];
-            if (extents) {
-                Extent e = {0, 0, 0, -1};
-                if (there) e = extent_of(a, s0 + lane);
-                tiles = e.tiles;
-                sh.seqs.lo[lane] = e.lo;
-                sh.seqs.hi[lane] = e.hi;
-                sh.seqs.tiles[lane] = e.tiles;
-                sh.seqs.slot[lane] = e.slot;
-            }
-            int64_t upto = there ? (int64_t)lay.unit(tiles) * units_per_seq : 0;
+            const int tiles = tiles_of(sh.seqs.lo[lane], sh.seqs.hi[lane]);
+            int64_t upto = there ? (int64_t)Room{false}.unit(tiles) * units_per_seq : 0;
+            int64_t even = there ? (int64_t)Room{true}.unit(tiles) * units_per_seq : 0;
 #pragma unroll
             for (int d = 1; d < 64; d <<= 1) {
-                const int64_t o = __shfl_up(upto, d);
-                if (lane >= d) upto += o;
+                const int64_t o = __shfl_up(upto, d), e = __shfl_up(even, d);
+                if (lane >= d) {
+                    upto += o;
+                    even += e;
+                }
             }
             sh.seqs.upto[lane] = upto;
+            sh.seqs.even[lane] = (int)min(even, (int64_t)1 << 30);
         }
         __syncthreads();
     };
-    // All of it in rooms of whole least shares, and if those are too many, end
-    // to end.  64 sequences stay measured; more are measured again.
-    int64_t room = 0;
-    for (int pass = 0; pass < 2; ++pass) {
-        room = 0;
-        for (int s0 = 0; s0 < a.n_seq; s0 += 64) {
-            if (s0 > 0 || pass > 0) __syncthreads();  // everyone is done with those before
-            measure(s0, pass == 0 || a.n_seq > 64);
-            room += sh.seqs.upto[63];
-        }
-        if (pass == 0 && room <= (int64_t)kMinSteps * gridDim.x) break;
-        lay.even = false;
+    int64_t room_to_end = 0, room_even = 0;
+    for (int s0 = 0; s0 < a.n_seq; s0 += 64) {
+        if (s0 > 0) __syncthreads();  // everyone is done with those before
+        measure(s0);
+        room_to_end += sh.seqs.upto[63];
+        room_even += sh.seqs.even[63];
     }
+    const Room lay = {room_even <= (int64_t)kMinSteps * gridDim.x};
+    const int64_t room = lay.even ? room_even : room_to_end;
     const int64_t share = lay.even ? kMinSteps : (room + gridDim.x - 1) / gridDim.x;
-    if (a.n_seq > 64) {
-        __syncthreads();
-        measure(0, true);
-    }
+    const auto upto_of = [&](int i) { return lay.even ? (int64_t)sh.seqs.even[i] : sh.seqs.upto[i]; };
     if (blockIdx.x == 0) {  // for the join
         if (threadIdx.x == 0) *reinterpret_cast<Layout*>(a.workspace) = {share, lay.even};
         int64_t sum = 0;
         for (int s0 = 0; s0 < a.n_seq; s0 += 64) {
-            if (s0 > 0) {
+            if (a.n_seq > 64) {
                 __syncthreads();
-                measure(s0, true);
+                measure(s0);
             }
-            const int tiles = sh.seqs.tiles[lane];
+            const int tiles = tiles_of(sh.seqs.lo[lane], sh.seqs.hi[lane]);
             if (wave == 0 && s0 + lane < a.n_seq)
-                rooms[s0 + lane] = {sum + sh.seqs.upto[lane] - (int64_t)lay.unit(tiles) * units_per_seq, tiles,
+                rooms[s0 + lane] = {sum + upto_of(lane) - (int64_t)lay.unit(tiles) * units_per_seq, tiles,
                                     sh.seqs.slot[lane]};
-            sum += sh.seqs.upto[63];
+            sum += upto_of(63);
         }
-        if (a.n_seq > 64) {
-            __syncthreads();
-            measure(0, true);
-        }
+    }
+    if (a.n_seq > 64) {
+        __syncthreads();
+        measure(0);
     }
     // This workgroup's share: [at, end) of the room.
     int64_t at = share * blockIdx.x;
@@ -683,19 +691,22 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int rec_rows, float* records) {
     while (at < end) {
         // ---- the unit (sequence, head, row block) at `at`, and its steps here
         uint64_t past;
-        while ((past = __ballot(sh.seqs.upto[lane] > at - before)) == 0) {
-            before += sh.seqs.upto[63];
+        while ((past = __ballot(upto_of(lane) > at - before)) == 0) {
+            before += upto_of(63);
             seq0 += 64;
             __syncthreads();
-            measure(seq0, true);
+            measure(seq0);
         }
         const int f = __builtin_ctzll(past);
         const auto of = [&](const int (&v)[64]) { return __builtin_amdgcn_readfirstlane(v[f]); };
         const int seq = seq0 + f;
-        const Extent ex = {of(sh.seqs.lo), of(sh.seqs.hi), of(sh.seqs.tiles), of(sh.seqs.slot)};
+        const int ex_lo = of(sh.seqs.lo), ex_hi = of(sh.seqs.hi);
+        const Extent ex = {ex_lo, ex_hi, tiles_of(ex_lo, ex_hi), of(sh.seqs.slot)};
         const int unit_size = lay.unit(ex.tiles);
-        const int64_t seq_start = before + (f > 0 ? sh.seqs.upto[f - 1] : 0);
-        const int unit_of_seq = __builtin_amdgcn_readfirstlane((int)((at - seq_start) / unit_size));
+        const int64_t seq_start = before + (f > 0 ? upto_of(f - 1) : 0);
+        const int64_t into = at - seq_start;
+        const int unit_of_seq = __builtin_amdgcn_readfirstlane(
+            into >> 32 == 0 ? (int)((uint32_t)into / (uint32_t)unit_size) : (int)(into / unit_size));
         const int64_t steps_at = seq_start + (int64_t)unit_of_seq * unit_size + lay.cost();
         const int steps = max(ex.tiles, 1);
         const int from = __builtin_amdgcn_readfirstlane((int)max(at - steps_at, (int64_t)0));
@@ -931,6 +942,15 @@ kv4_join_kernel(AttendArgs a, int n_rb, int per_wg, int rec_rows, const float* r
     if (w0 == w1) return;
     const int parts = w1 - w0 + 1, size = record_floats(rec_rows, a.c.nb);
     const auto record = [&](int i) { return records + (2 * (int64_t)(w0 + i) + (i == 0 ? 1 : 0)) * size; };
+    const int d = (int)threadIdx.x % lanes, p = (int)threadIdx.x / lanes;
+    const int i0 = p < runs ? parts * p / runs : 0, i1 = p < runs ? parts * (p + 1) / runs : 0;
+    constexpr int kEarly = 4;  // parts of a run that are loaded before the weights are known
+    v4f early[kEarly];
+#pragma unroll
+    for (int k = 0; k < kEarly; ++k) {
+        const f4u y = *reinterpret_cast<const f4u*>(record(min(i0 + k, parts - 1)) + row * D + 4 * d);
+        early[k] = v4f{y[0], y[1], y[2], y[3]};
+    }
     float top = -__builtin_inff();
     for (int i = threadIdx.x; i < parts; i += kJoinThreads) {
         const float* r = record(i) + rec_rows * D + row;
@@ -946,13 +966,13 @@ kv4_join_kernel(AttendArgs a, int n_rb, int per_wg, int rec_rows, const float* r
     for (int i = threadIdx.x; i < parts; i += kJoinThreads)
         weight[i] = part_weight(weight[i], top, a.scale_log2 * kScoreUnit);
     __syncthreads();
-    const int d = (int)threadIdx.x % lanes, p = (int)threadIdx.x / lanes;
     v4f x = {0.f, 0.f, 0.f, 0.f};
-    if (p < runs) {
-        const int i0 = parts * p / runs, i1 = parts * (p + 1) / runs;
-#pragma unroll 4
-        for (int i = i0; i < i1; ++i)
-            x += *reinterpret_cast<const f4u*>(record(i) + row * D + 4 * d) * weight[i];
+#pragma unroll
+    for (int k = 0; k < kEarly; ++k)
+        if (i0 + k < i1) x += early[k] * weight[i0 + k];
+    for (int i = i0 + kEarly; i < i1; ++i) {
+        const f4u y = *reinterpret_cast<const f4u*>(record(i) + row * D + 4 * d);
+        x += v4f{y[0], y[1], y[2], y[3]} * weight[i];
     }
     *reinterpret_cast<v4f*>(run + 4 * threadIdx.x) = x;
     if (threadIdx.x == 0) {
