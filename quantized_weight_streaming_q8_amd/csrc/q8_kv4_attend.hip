@@ -41,6 +41,10 @@
 // a second, short launch joins them in order.  The cut is made on the GPU,
 // from pos: the host need not know the lengths, and a launch captured in a
 // graph serves any.
+//
+// Heads abreast.  A page holds its positions for all key/value heads side by
+// side.  Workgroups that differ only in the head go through the same share of
+// the steps at the same time, so that what is read together lies together.
 
 #include "q8_kv4_internal.h"
 
@@ -58,6 +62,7 @@ constexpr int kNoVmem = 0x0f70;  // s_waitcnt vmcnt(0), no other count
 
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef float f4u __attribute__((ext_vector_type(4), aligned(4)));
+typedef float f16u __attribute__((ext_vector_type(16), aligned(4)));
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 typedef uint32_t v6u __attribute__((ext_vector_type(6)));
 typedef int v8i __attribute__((ext_vector_type(8)));
@@ -286,46 +291,62 @@ struct Query {
     uint32_t s[(P + 3) / 4];  // their scale bytes, four to a word
 };
 
+// A query operand in LDS, lane by lane.
 template <Fold F>
-__device__ inline void make_query(float (&x)[32], uint32_t keep, Query<F>& q) {
+struct QueryLds {
+    uint2 p[Query<F>::P * 3][64];
+    uint32_t s[(Query<F>::P + 3) / 4][64];
+};
+
+// The first and the last 16 values; the conversion takes them in turn, which
+// is the order of the cache's codes.
+template <Fold F>
+__device__ inline void make_query(v16f x, v16f y, int lane, QueryLds<F>& out) {
     uint32_t top = 0;  // of the magnitudes' bits: NaN and infinity are the largest
 #pragma unroll
-    for (int i = 0; i < 32; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+    for (int i = 0; i < 16; ++i)
+        top = max(top, max(__float_as_uint(x[i]) & 0x7fffffffu, __float_as_uint(y[i]) & 0x7fffffffu));
     const bool bad = top > 0x7f7fffffu;
     // largest value / 2^e in 3.75 .. 7.5
     const int e = max((int)(top >> 23) - 127 - 2 + ((top & 0x7fffffu) > 0x700000u ? 1 : 0), -100);
-#pragma unroll
-    for (int w = 0; w < (Query<F>::P + 3) / 4; ++w) q.s[w] = 0;
+    uint32_t scales[(Query<F>::P + 3) / 4] = {};
 #pragma unroll
     for (int n = 0; n < kPieces; ++n) {
         const int en = e - kPieceDown[n];
         const float scale = __uint_as_float((uint32_t)(en + 127) << 23);
-        v16f even, odd;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            even[i] = x[2 * i];
-            odd[i] = x[2 * i + 1];
-        }
-        v6u f = __builtin_amdgcn_cvt_scalef32_2xpk16_fp6_f32(even, odd, scale);
+        const v6u f = __builtin_amdgcn_cvt_scalef32_2xpk16_fp6_f32(x, y, scale);
         const v32f back = __builtin_amdgcn_cvt_scalef32_pk32_f32_fp6(f, scale);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] -= back[i];
+        for (int i = 0; i < 16; ++i) {
+            x[i] -= back[2 * i];
+            y[i] -= back[2 * i + 1];
+        }
         const int byte = en + 127 - kScoreShift;
         const bool drop = byte < 1 && !bad;
         const uint32_t sb = bad ? 255u : drop ? 1u : (uint32_t)byte;
-#pragma unroll
-        for (int i = 0; i < 6; ++i) f[i] = drop ? 0u : f[i];
         const int o = F == kFolded ? n >> 1 : n;  // its operand
-        if (F == kWide || (n & 1) == 0) {
-            q.p[o] = f;
-            q.s[o >> 2] |= sb << (8 * (o & 3));
-        } else {  // columns 8..15 take this piece instead of the one before
+        // folded: columns 8..15 take the odd pieces
+        if (F == kWide || (lane >> 3 & 1) == (n & 1)) {
+            scales[o >> 2] |= sb << (8 * (o & 3));
 #pragma unroll
-            for (int i = 0; i < 6; ++i) q.p[o][i] = keep != 0 ? f[i] : q.p[o][i];
-            const uint32_t m = keep != 0 ? 0xffu << (8 * (o & 3)) : 0u;
-            q.s[o >> 2] = (q.s[o >> 2] & ~m) | (sb << (8 * (o & 3)) & m);
+            for (int i = 0; i < 3; ++i)
+                out.p[3 * o + i][lane] = make_uint2(drop ? 0u : f[2 * i], drop ? 0u : f[2 * i + 1]);
         }
     }
+#pragma unroll
+    for (int w = 0; w < (Query<F>::P + 3) / 4; ++w) out.s[w][lane] = scales[w];
+}
+
+template <Fold F>
+__device__ inline void read_query(const QueryLds<F>& in, int lane, Query<F>& q) {
+#pragma unroll
+    for (int v = 0; v < Query<F>::P * 3; ++v) {
+        const uint2 w = in.p[v][lane];
+        q.p[v / 3][v % 3 * 2] = w.x;
+        q.p[v / 3][v % 3 * 2 + 1] = w.y;
+    }
+#pragma unroll
+    for (int w = 0; w < (Query<F>::P + 3) / 4; ++w) q.s[w] = in.s[w][lane];
 }
 
 // Carried state of one column tile.
@@ -592,7 +613,10 @@ struct Shared {
     static constexpr int kRows = kCols * RT;
     static constexpr int kPitch = NB * 32 + 4;           // floats of a row's accumulator
     uint8_t slots[kWaves][kSlots][slot_bytes(NB)];
-    float o[kWaves][kCols][kPitch];
+    union {
+        float o[kWaves][kCols][kPitch];
+        QueryLds<F> query[RT][Keys<NB>::kQuads];  // a unit's, each made by one wave
+    };
     float m[kWaves][kRows], l[kWaves][kRows];  // of the waves
     float inv[kRows];
     int flag[kRows];
@@ -601,18 +625,15 @@ struct Shared {
 
 template <int NB, int RT, Fold F>
 __global__ void __launch_bounds__(64 * waves_of(NB), RT == 1 && NB <= 4 ? (F == kFolded ? 3 : 2) : 1)
-kv4_attend_kernel(AttendArgs a, int n_rb, int rec_rows, float* records) {
+kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int rec_rows, float* records) {
     using Sh = Shared<NB, RT, F>;
     constexpr int D = NB * 32;
     constexpr int kWaves = Sh::kWaves, kThreads = 64 * kWaves;
     constexpr int kCols = Sh::kCols, kRows = Sh::kRows, kQuads = Keys<NB>::kQuads;
     __shared__ __align__(16) Sh sh;
 
-    const int lane = threadIdx.x & 63;
+    int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int col = F == kFolded ? lane & 7 : lane & 15, g = lane >> 4;
-    const bool owner = F == kFolded ? (lane & 15) < 8 && g == 0 : g == 0;  // one lane of a row
-    const uint32_t keep = lane & 8 ? 0xffff0000u : 0u;
     const float c = a.scale_log2 * kScoreUnit, lag = 8.0f / c;
     const int n_rows = a.tokens * a.group;
     const int groups_per_page = a.c.page_tokens / kKvTile;
@@ -620,7 +641,9 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int rec_rows, float* records) {
     SequenceRoom* rooms = reinterpret_cast<SequenceRoom*>(a.workspace + sizeof(Layout));
 
     // The room of sequences s0 .. s0 + 63, in either layout.
-    const int units_per_seq = a.c.n_kv * n_rb;
+    const int units_per_seq = a.c.n_kv / abreast * n_rb;
+    const int n_shares = gridDim.x / abreast, my_share = blockIdx.x / abreast;
+    const int my_head = blockIdx.x - my_share * abreast;
     const int tp = a.tokens > 1 ? 1 << (32 - __builtin_clz(a.tokens - 1)) : 1;
     const auto measure = [&](int s0) {
         for (int r = wave; r * (64 / tp) < 64 && s0 + r * (64 / tp) < a.n_seq; r += kWaves) {
@@ -658,9 +681,9 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int rec_rows, float* records) {
         room_to_end += sh.seqs.upto[63];
         room_even += sh.seqs.even[63];
     }
-    const Room lay = {room_even <= (int64_t)kMinSteps * gridDim.x};
+    const Room lay = {room_even <= (int64_t)kMinSteps * n_shares};
     const int64_t room = lay.even ? room_even : room_to_end;
-    const int64_t share = lay.even ? kMinSteps : (room + gridDim.x - 1) / gridDim.x;
+    const int64_t share = lay.even ? kMinSteps : (room + n_shares - 1) / n_shares;
     const auto upto_of = [&](int i) { return lay.even ? (int64_t)sh.seqs.even[i] : sh.seqs.upto[i]; };
     if (blockIdx.x == 0) {  // for the join
         if (threadIdx.x == 0) *reinterpret_cast<Layout*>(a.workspace) = {share, lay.even};
@@ -682,13 +705,20 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int rec_rows, float* records) {
         measure(0);
     }
     // This workgroup's share: [at, end) of the room.
-    int64_t at = share * blockIdx.x;
+    int64_t at = share * my_share;
     const int64_t end = min(at + share, room);
     if (at >= end) return;
     int seq0 = 0;        // sequences seq0 .. seq0 + 63 are in LDS,
     int64_t before = 0;  // and so much room lies before them
 
     while (at < end) {
+        // What follows from the lane is worked out for each unit: kept from
+        // one to the next it would take registers that the steps need.
+        asm volatile("" : "+v"(lane));
+        const int col = F == kFolded ? lane & 7 : lane & 15, g = lane >> 4;
+        const bool owner = F == kFolded ? (lane & 15) < 8 && g == 0 : g == 0;  // one lane of a row
+        const uint32_t keep = lane & 8 ? 0xffff0000u : 0u;
+
         // ---- the unit (sequence, head, row block) at `at`, and its steps here
         uint64_t past;
         while ((past = __ballot(upto_of(lane) > at - before)) == 0) {
@@ -714,7 +744,8 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int rec_rows, float* records) {
         at = steps_at - lay.cost() + unit_size;
         if (from >= upto) continue;  // only room before or after its steps
         const bool whole = from == 0 && upto == steps;
-        const int head = unit_of_seq / n_rb, rb = unit_of_seq - head * n_rb;
+        const int heads = unit_of_seq / n_rb, rb = unit_of_seq - heads * n_rb;
+        const int head = heads * abreast + my_head;
         const int t0 = ex.lo / kKvTile + from, t1 = ex.tiles > 0 ? ex.lo / kKvTile + upto : t0;
         const int slot = ex.slot;
         __syncthreads();  // the rows of the unit before are stored
@@ -731,20 +762,29 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int rec_rows, float* records) {
         if (slot >= 0) ids = load_ids(page0);
         Rows<NB, F> rows[RT];
         int row_pos[RT], row_slot[RT];
-        f4u q_in[RT][kQuads][8];
+        // Operand (r, k) of the queries is made by one wave, not the same one
+        // for the workgroups that share a CU.
+        constexpr int kMine = (RT * kQuads + kWaves - 1) / kWaves;
+        const int turn = (wave + kWaves - blockIdx.x / 256 % kWaves) % kWaves;
+        v16f q_in[kMine][2];
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
             const int row = min(rb * kRows + r * kCols + col, n_rows - 1);  // past the last: that again
-            const int j = row / a.group, qh = head * a.group + row - j * a.group;
-            const int64_t t = (int64_t)seq * a.tokens + j;
+            const int64_t t = (int64_t)seq * a.tokens + row / a.group;
             row_pos[r] = a.pos[t];
             row_slot[r] = a.batch_index[t];
-            const float* q = a.Q + t * a.q_stride + (int64_t)qh * D;
+        }
 #pragma unroll
-            for (int k = 0; k < kQuads; ++k)  // block 4k + g
+        for (int i = 0; i < kMine; ++i) {
+            const int n = turn + i * kWaves, r = n / kQuads, k = n - r * kQuads;
+            if (n >= RT * kQuads) break;
+            const int row = min(rb * kRows + r * kCols + col, n_rows - 1);
+            const int j = row / a.group, qh = head * a.group + row - j * a.group;
+            const float* q = a.Q + ((int64_t)seq * a.tokens + j) * a.q_stride + (int64_t)qh * D +
+                             32 * min(4 * k + g, NB - 1);  // block 4k + g
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    q_in[r][k][i] = *reinterpret_cast<const f4u*>(q + 32 * min(4 * k + g, NB - 1) + 4 * i);
+            for (int h = 0; h < 2; ++h)
+                q_in[i][h] = *reinterpret_cast<const f16u*>(q + 16 * h);
         }
         // They are here before the groups set out, which come in behind them.
         __builtin_amdgcn_s_waitcnt(kNoVmem);
@@ -788,15 +828,29 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int rec_rows, float* records) {
             all_lo = max(all_lo, rows[r].lo);
             all_hi = min(all_hi, rows[r].hi);
             if (wave == 0 && owner) sh.flag[r * kCols + col] = flag;
-#pragma unroll
-            for (int k = 0; k < kQuads; ++k) {
-                float x[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    x[i] = flag == 0 && 4 * k + g < NB ? q_in[r][k][i >> 2][i & 3] : 0.0f;
-                make_query<F>(x, keep, rows[r].q[k]);
-            }
         }
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            const int n = turn + i * kWaves, r = n / kQuads, k = n - r * kQuads;
+            if (n >= RT * kQuads) break;
+            int flag = row_flag(row_pos[0], row_slot[0], slot, a.c.n_slots, cap);
+#pragma unroll
+            for (int o = 1; o < RT; ++o)
+                if (r == o) flag = row_flag(row_pos[o], row_slot[o], slot, a.c.n_slots, cap);
+            const bool there = flag == 0 && 4 * k + g < NB;
+            v16f &x = q_in[i][0], &y = q_in[i][1];
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+                x[v] = there ? x[v] : 0.0f;
+                y[v] = there ? y[v] : 0.0f;
+            }
+            make_query<F>(x, y, lane, sh.query[r][k]);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int k = 0; k < kQuads; ++k) read_query<F>(sh.query[r][k], lane, rows[r].q[k]);
 #pragma unroll
         for (int d = 1; d < 16; d <<= 1) {
             all_lo = max(all_lo, __shfl_xor(all_lo, d));
@@ -839,6 +893,8 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int rec_rows, float* records) {
         }
 
         // ---- join the waves
+        asm volatile("" : "+v"(lane));  // as above
+        const int thread = wave * 64 + lane;
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
             float l = rows[r].l;
@@ -860,8 +916,8 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int rec_rows, float* records) {
             for (int w = 1; w < kWaves; ++w) m = fmaxf(m, sh.m[w][i]);
             wave_max[r] = m;
         }
-        if (threadIdx.x < kRows) {
-            const int r = threadIdx.x;
+        if (thread < kRows) {
+            const int r = thread;
             float m = sh.m[0][r], l = 0.0f;
             for (int w = 1; w < kWaves; ++w) m = fmaxf(m, sh.m[w][r]);
             for (int w = 0; w < kWaves; ++w) l += sh.l[w][r] * part_weight(sh.m[w][r], m, c);
@@ -894,7 +950,7 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int rec_rows, float* records) {
             }
             __syncthreads();
             const int here = min(kCols, n_rows - rb * kRows - r * kCols);  // rows of this tile
-            for (int u = threadIdx.x; u < here * (D / 4); u += kThreads) {
+            for (int u = thread; u < here * (D / 4); u += kThreads) {
                 const int row = u / (D / 4), d = (u - row * (D / 4)) * 4;
                 v4f x = *reinterpret_cast<const v4f*>(&sh.o[0][row][d]);
 #pragma unroll
@@ -921,15 +977,16 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int rec_rows, float* records) {
 constexpr int kJoinThreads = 256;
 
 __global__ void __launch_bounds__(kJoinThreads)
-kv4_join_kernel(AttendArgs a, int n_rb, int per_wg, int rec_rows, const float* records) {
+kv4_join_kernel(AttendArgs a, int n_rb, int abreast, int per_wg, int rec_rows, const float* records) {
     __shared__ float weight[kMaxShares], sums[kMaxShares];
     __shared__ float wave_top[kJoinThreads / 64];
     __shared__ float total;
     __shared__ __align__(16) float run[kJoinThreads * 4];
     const int D = a.c.nb * 32, lanes = D / 4, runs = kJoinThreads / lanes;
-    const int units_per_seq = a.c.n_kv * n_rb;
-    const int seq = (int)(blockIdx.x / units_per_seq), unit_of_seq = (int)blockIdx.x - seq * units_per_seq;
-    const int head = unit_of_seq / n_rb, rb = unit_of_seq - head * n_rb;
+    const int per_seq = a.c.n_kv * n_rb;
+    const int seq = (int)(blockIdx.x / per_seq), in_seq = (int)blockIdx.x - seq * per_seq;
+    const int head = in_seq / n_rb, rb = in_seq - head * n_rb;
+    const int unit_of_seq = head / abreast * n_rb + rb, my_head = head % abreast;
     const int row = blockIdx.y, abs_row = rb * per_wg + row;
     if (abs_row >= a.tokens * a.group) return;
     const Layout layout = *reinterpret_cast<const Layout*>(a.workspace);
@@ -941,7 +998,9 @@ kv4_join_kernel(AttendArgs a, int n_rb, int per_wg, int rec_rows, const float* r
     const int w0 = (int)(steps_at / share), w1 = (int)((steps_at + max(s.tiles, 1) - 1) / share);
     if (w0 == w1) return;
     const int parts = w1 - w0 + 1, size = record_floats(rec_rows, a.c.nb);
-    const auto record = [&](int i) { return records + (2 * (int64_t)(w0 + i) + (i == 0 ? 1 : 0)) * size; };
+    const auto record = [&](int i) { 
+        return records + (2 * ((int64_t)(w0 + i) * abreast + my_head) + (i == 0 ? 1 : 0)) * size;
+    };
     const int d = (int)threadIdx.x % lanes, p = (int)threadIdx.x / lanes;
     const int i0 = p < runs ? parts * p / runs : 0, i1 = p < runs ? parts * (p + 1) / runs : 0;
     constexpr int kEarly = 4;  // parts of a run that are loaded before the weights are known
@@ -992,9 +1051,9 @@ kv4_join_kernel(AttendArgs a, int n_rb, int per_wg, int rec_rows, const float* r
 }
 
 struct Plan {
-    int rt, per_wg, n_rb, rec_rows;
+    int rt, per_wg, n_rb, abreast, rec_rows;
     bool folded;
-    unsigned shares;
+    unsigned wgs;
     bool cut;  // units may be cut
     int64_t units;
 };
@@ -1014,19 +1073,24 @@ Plan plan_attend(const AttendArgs& a) {
     // Fewer where full sequences have no more least shares.
     const int per_cu = p.rt > 1 ? 1 : nb <= 4 && p.folded ? 3 : 2;
     const int64_t tiles = ((int64_t)a.c.max_pages * a.c.page_tokens + kKvTile - 1) / kKvTile;
-    p.shares = (unsigned)std::min<int64_t>(256 * per_cu, p.units * ((tiles + kMinSteps - 1) / kMinSteps));
-    p.cut = tiles > kMinSteps || p.units > p.shares;
+    p.abreast = 1;
+    for (int d = 2; d <= 32 && d <= a.c.n_kv; ++d)
+        if (a.c.n_kv % d == 0) p.abreast = d;
+    const int64_t most = p.units / p.abreast * ((tiles + kMinSteps - 1) / kMinSteps);
+    const int64_t shares = std::min<int64_t>(256 * per_cu / p.abreast, most);
+    p.wgs = (unsigned)(shares * p.abreast);
+    p.cut = tiles > kMinSteps || p.units / p.abreast > shares;
     return p;
 }
 
 size_t records_bytes(const Plan& p, int nb) {
-    return 2 * (size_t)p.shares * record_floats(p.rec_rows, nb) * sizeof(float);
+    return 2 * (size_t)p.wgs * record_floats(p.rec_rows, nb) * sizeof(float);
 }
 
 template <int NB, int RT, Fold F>
 hipError_t launch_one(const Plan& p, const AttendArgs& a, float* records, hipStream_t st) {
-    hipLaunchKernelGGL((kv4_attend_kernel<NB, RT, F>), dim3(p.shares), dim3(64 * waves_of(NB)), 0, st, a,
-                       p.n_rb, p.rec_rows, records);
+    hipLaunchKernelGGL((kv4_attend_kernel<NB, RT, F>), dim3(p.wgs), dim3(64 * waves_of(NB)), 0, st, a,
+                       p.n_rb, p.abreast, p.rec_rows, records);
     return hipGetLastError();
 }
 
@@ -1060,7 +1124,7 @@ hipError_t launch_kv4_attend(const AttendArgs& a, hipStream_t st) {
     }
     if (e != hipSuccess || !p.cut) return e;
     hipLaunchKernelGGL(kv4_join_kernel, dim3((unsigned)p.units, (unsigned)p.rec_rows), dim3(kJoinThreads),
-                       0, st, a, p.n_rb, p.per_wg, p.rec_rows, records);
+                       0, st, a, p.n_rb, p.abreast, p.per_wg, p.rec_rows, records);
     return hipGetLastError();
 }
 

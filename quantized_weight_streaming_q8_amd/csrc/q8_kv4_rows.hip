@@ -125,9 +125,8 @@ __device__ inline int scale_byte(float a) {
     return min(max(e, -125), 125) + kScaleBias;
 }
 
-// A block's 4 values per lane over 8 consecutive lanes -> this lane's two
-// code bytes (low 16 bits) and the block's scale byte.
-__device__ inline uint32_t encode4(const float (&v)[4], int& scale) {
+// Scale byte of a block held by 8 consecutive lanes, 4 values each.
+__device__ inline int block_scale(const float (&v)[4]) {
     float a = 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -136,16 +135,15 @@ __device__ inline uint32_t encode4(const float (&v)[4], int& scale) {
     }
 #pragma unroll
     for (int m = 1; m < 8; m <<= 1) a = fmaxf(a, __shfl_xor(a, m, 8));
-    if (!(a <= __FLT_MAX__)) {
-        scale = kNanByte;
-        return 0u;
-    }
-    scale = scale_byte(a);
-    // value / 2^(scale - 127), to the nearest code, ties to even, saturating
-    const float unit = __uint_as_float((uint32_t)scale << 23);
-    uint32_t q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, v[0], v[1], unit, 0);
-    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[2], v[3], unit, 1);
-    return q & 0xffffu;
+    return a <= __FLT_MAX__ ? scale_byte(a) : kNanByte;
+}
+
+// Codes of a and b (low nibble, high nibble) into byte B of q: value / 2^(s -
+// 127) to the nearest code, ties to even, saturating; 0 in a NaN block.
+template <int B>
+__device__ inline uint32_t encode2(uint32_t q, float a, float b, int s) {
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, s == kNanByte ? 0.0f : a, s == kNanByte ? 0.0f : b,
+                                                    __uint_as_float((uint32_t)s << 23), B);
 }
 
 // One workgroup: one row and either a share of its query heads (blockIdx.y <
@@ -202,20 +200,23 @@ kv4_append_kernel(KvView c, const float* q, const float* __restrict__ k, const f
                 x[j] = first ? (float)(a * w.x - b * w.y) : (float)(b * w.y + a * w.x);
             }
         }
-        int s;
-        uint32_t code = encode4(x, s);
+        const int s = block_scale(x);
         const int b = d >> 5, l = (d & 31) >> 2;  // block of the head, lane of the block
         uint8_t* head = c.pages + pg * c.page_bytes + h * c.head_bytes;
         if (is_v) {
             uint8_t* o = head + v_code_offset(c.nb, tok, b, 2 * l);
+            const uint32_t code = encode2<1>(encode2<0>(0u, x[0], x[1], s), x[2], x[3], s);
             const int w = 8 * min(2, c.nb - (b & ~1));  // bytes from c to c + 1
             o[0] = (uint8_t)code;
             o[w] = (uint8_t)(code >> 8);
             if (l == 0) head[v_scale_offset(c.nb, tok, b)] = (uint8_t)s;
         } else {
-            code |= __shfl_down(code, 1, 8) << 16;
-            if ((l & 1) == 0)
-                *reinterpret_cast<uint32_t*>(head + k_code_offset(c.nb, tok, b, l >> 1)) = code;
+            float y[4];  // lanes 0..3 of the block: the values 16 further on
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] = __shfl_down(x[j], 4, 8);
+            uint32_t code = encode2<1>(encode2<0>(0u, x[0], y[0], s), x[1], y[1], s);
+            code = encode2<3>(encode2<2>(code, x[2], y[2], s), x[3], y[3], s);
+            if (l < 4) *reinterpret_cast<uint32_t*>(head + k_code_offset(c.nb, tok, b, l)) = code;
             if (l == 0) head[k_scale_offset(c.nb, tok, b)] = (uint8_t)s;
         }
     }
@@ -241,15 +242,16 @@ kv4_read_kernel(KvView c, const int32_t* __restrict__ batch_index, const int32_t
     if (pg >= 0) {
             const uint8_t* head = c.pages + pg * c.page_bytes + h * c.head_bytes;
         const int tok = p % c.page_tokens, b = d >> 5, l = (d & 31) >> 2;
-        uint32_t code;
+        uint32_t code;  // four nibbles
         int s;
         if (is_v) {
             const uint8_t* o = head + v_code_offset(c.nb, tok, b, 2 * l);
             code = o[0] | (uint32_t)o[8 * min(2, c.nb - (b & ~1))] << 8;
             s = head[v_scale_offset(c.nb, tok, b)];
         } else {
-            code = *reinterpret_cast<const uint16_t*>(head + k_code_offset(c.nb, tok, b, l >> 1) +
-                                                      2 * (l & 1));
+            const uint32_t w =
+                *reinterpret_cast<const uint32_t*>(head + k_code_offset(c.nb, tok, b, l & 3)) >> (l & 4);
+            code = (w & 0xfu) | (w >> 4 & 0xf0u) | (w >> 8 & 0xf00u) | (w >> 12 & 0xf000u);
             s = head[k_scale_offset(c.nb, tok, b)];
         }
         if (s != kNanByte) {
