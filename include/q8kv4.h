@@ -159,7 +159,7 @@ q8_status q8_kv4_read(const q8_kv4_cache* cache, const int32_t* batch_index, con
 
 /* ---------------------------------------------------------- attention */
 
-/* Bytes of workspace q8_kv4_attend needs (at least 16); 0 if an argument is
+/* Bytes of workspace q8_kv4_attend needs; 0 if an argument is
  * invalid, among them a call of more than 2^18 row blocks, n_seq * n_kv_heads *
  * ceil(tokens_per_seq * (n_q_heads / n_kv_heads) / 8).  It
  * depends on the cache's shape fields only (its pointers are not looked at)
@@ -194,9 +194,10 @@ size_t q8_kv4_attend_workspace_bytes(const q8_kv4_cache* cache, int n_seq, int t
  * bits every time.
  *
  * workspace: device memory, 256-byte aligned, at least
- * q8_kv4_attend_workspace_bytes(...); its contents do not matter before a
- * call and are undefined after it.  It must not be shared by calls that can
- * run at the same time.
+ * q8_kv4_attend_workspace_bytes(...), zero-filled before its first use.
+ * Every completed call leaves it ready for the next, of any shape that it is
+ * large enough for.  It must not be shared by calls that can run at the same
+ * time.
  *
  * 1 <= n_seq <= Q8_KV4_MAX_SEQS, 1 <= tokens_per_seq <= Q8_KV4_MAX_TOKENS,
  * n_q_heads a multiple of n_kv_heads, at most 8192; window >= 0; 0 < scale <=

@@ -420,6 +420,7 @@ class Rotary:
         self.interleaved = bool(interleaved)
         self.amplitude = float(amplitude)
         self.device = inv_freq.device
+        self._device_index = inv_freq.get_device()
         self._c = _RotaryPlan(addr, self.amplitude, self.rot_dim, int(self.interleaved))
         self._ref = ctypes.addressof(self._c)
 
@@ -474,6 +475,7 @@ class KV4Cache:
         self.n_slots, self.max_pages = block_table.shape
         self.page_bytes = nbytes
         self.device = block_table.device
+        self._device_index = block_table.get_device()
         self._c = _KV4Cache(addr, table, n_pages, self.n_slots, self.max_pages, page_tokens,
                             n_kv_heads, head_dim)
         self._ref = ctypes.addressof(self._c)
@@ -483,10 +485,42 @@ def _handle(h, kind, name: str):
     """Address of a handle's C struct, its device checked."""
     if not isinstance(h, kind):
         raise TypeError(f"{name}: expected a {kind.__name__}, got {type(h).__name__}")
-    if h.device.index != torch.cuda.current_device():
+    if h._device_index != torch._C._cuda_getDevice():
         raise ValueError(f"{name}: on {h.device}, but the current device is "
                          f"cuda:{torch.cuda.current_device()}")
     return h._ref
+
+
+def _fast(x, name: str, dtype, need_bytes: int, device: int):
+    """_dev(_arg(x, name, (dtype,), need_bytes)) for one argument, in a
+    fraction of the time where x passes (a decode step's calls take a few
+    microseconds on the GPU); anything else goes the long way, which says what
+    is wrong with it."""
+    if x is None or type(x) is int:
+        return x
+    if type(x) is torch.Tensor and (x.dtype is dtype or dtype is None) and x.is_cuda and x.get_device() == device \
+            and x.is_contiguous() and x.nbytes >= need_bytes:
+        return x.data_ptr()
+    return _arg(x, name, None if dtype is None else (dtype,), need_bytes)
+
+
+def _fast_all(*addresses):
+    """The device check of the arguments that _fast left to _dev."""
+    for a in addresses:
+        if type(a) is tuple:
+            return _dev(*(a if type(a) is tuple else ("argument", a) for a in addresses))
+    return addresses
+
+
+def _current_device() -> int:
+    """The current device, -1 without one."""
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
+
+
+def _raw_stream(stream, device: int):
+    if stream is None and device >= 0:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return _stream(stream)
 
 
 def _span(rows: int, stride: int, width: int) -> int:
@@ -501,10 +535,12 @@ def q8_rotary(X, Y, n_rows: int, x_stride: int, pos, n_heads: int, head_dim: int
     w = n_heads * head_dim
     if y_stride is None:
         y_stride = w
-    x, y, p = _dev(_arg(X, "X", _F32, _span(n_rows, x_stride, w)),
-                   _arg(Y, "Y", _F32, _span(n_rows, y_stride, w)), _arg(pos, "pos", _I32, _n(n_rows, 4)))
+    dev = _current_device()
+    x, y, p = _fast_all(_fast(X, "X", torch.float32, _span(n_rows, x_stride, w), dev),
+                        _fast(Y, "Y", torch.float32, _span(n_rows, y_stride, w), dev),
+                        _fast(pos, "pos", torch.int32, _n(n_rows, 4), dev))
     _check(_lib.q8_rotary(x, x_stride, y, y_stride, n_rows, p, n_heads, head_dim,
-                          _handle(rotary, Rotary, "rotary"), _stream(stream)), "q8_rotary")
+                          _handle(rotary, Rotary, "rotary"), _raw_stream(stream, dev)), "q8_rotary")
 
 
 def q8_kv4_page_bytes(n_kv_heads: int, head_dim: int, page_tokens: int) -> int:
@@ -523,27 +559,29 @@ def q8_kv4_append(cache: KV4Cache, QKV, n_rows: int, row_stride: int, batch_inde
     width = wq + 2 * kv * d
     if row_stride < width:
         raise ValueError(f"row_stride: {row_stride} is less than the {width} values of a row")
-    rows, bi, p = _dev(_arg(QKV, "QKV", _F32, _span(n_rows, row_stride, width)),
-                       _arg(batch_index, "batch_index", _I32, _n(n_rows, 4)),
-                       _arg(pos, "pos", _I32, _n(n_rows, 4)))
-    out = None
-    if Q is not None:
-        if q_stride is None:
-            q_stride = wq
-        (out,) = _dev(_arg(Q, "Q", _F32, _span(n_rows, q_stride, wq)))
+    if q_stride is None:
+        q_stride = wq
+    dev = _current_device()
+    rows, bi, p, out = _fast_all(
+        _fast(QKV, "QKV", torch.float32, _span(n_rows, row_stride, width), dev),
+        _fast(batch_index, "batch_index", torch.int32, _n(n_rows, 4), dev),
+        _fast(pos, "pos", torch.int32, _n(n_rows, 4), dev),
+        _fast(Q, "Q", torch.float32, _span(n_rows, q_stride, wq), dev))
     _check(_lib.q8_kv4_append(_handle(cache, KV4Cache, "cache"), rows, rows and rows + 4 * wq,
                               rows and rows + 4 * (wq + kv * d), row_stride, n_rows, bi, p,
                               None if rotary is None else _handle(rotary, Rotary, "rotary"),
-                              0 if Q is None else n_q_heads, out, q_stride or 0, _stream(stream)),
+                              0 if Q is None else n_q_heads, out, q_stride, _raw_stream(stream, dev)),
            "q8_kv4_append")
 
 
 def q8_kv4_read(cache: KV4Cache, batch_index, pos, n_rows: int, K, V, stream=None) -> None:
     need = _n(n_rows * cache.n_kv_heads * cache.head_dim, 4)
-    bi, p, k, v = _dev(_arg(batch_index, "batch_index", _I32, _n(n_rows, 4)),
-                       _arg(pos, "pos", _I32, _n(n_rows, 4)),
-                       _arg(K, "K", _F32, need), _arg(V, "V", _F32, need))
-    _check(_lib.q8_kv4_read(_handle(cache, KV4Cache, "cache"), bi, p, n_rows, k, v, _stream(stream)),
+    dev = _current_device()
+    bi, p, k, v = _fast_all(_fast(batch_index, "batch_index", torch.int32, _n(n_rows, 4), dev),
+                            _fast(pos, "pos", torch.int32, _n(n_rows, 4), dev),
+                            _fast(K, "K", torch.float32, need, dev), _fast(V, "V", torch.float32, need, dev))
+    _check(_lib.q8_kv4_read(_handle(cache, KV4Cache, "cache"), bi, p, n_rows, k, v,
+                            _raw_stream(stream, dev)),
            "q8_kv4_read")
 
 
@@ -561,25 +599,26 @@ def q8_kv4_attend(cache: KV4Cache, Q, n_seq: int, tokens_per_seq: int, n_q_heads
     w, rows = n_q_heads * cache.head_dim, n_seq * tokens_per_seq
     q_stride = w if q_stride is None else q_stride
     o_stride = w if o_stride is None else o_stride
-    q, bi, p, o, ws = _dev(_arg(Q, "Q", _F32, _span(rows, q_stride, w)),
-                           _arg(batch_index, "batch_index", _I32, _n(rows, 4)),
-                           _arg(pos, "pos", _I32, _n(rows, 4)),
-                           _arg(O, "O", _F32, _span(rows, o_stride, w)),
-                           _arg(workspace, "workspace"))
+    dev = _current_device()
+    q, bi, p, o, ws = _fast_all(_fast(Q, "Q", torch.float32, _span(rows, q_stride, w), dev),
+                                _fast(batch_index, "batch_index", torch.int32, _n(rows, 4), dev),
+                                _fast(pos, "pos", torch.int32, _n(rows, 4), dev),
+                                _fast(O, "O", torch.float32, _span(rows, o_stride, w), dev),
+                                _fast(workspace, "workspace", None, 0, dev))
     _check(_lib.q8_kv4_attend(_handle(cache, KV4Cache, "cache"), q, q_stride, n_seq, tokens_per_seq,
                               n_q_heads, bi, p, cache.head_dim ** -0.5 if scale is None else scale,
                               window, o, o_stride, ws, _ws_bytes(workspace, workspace_bytes),
-                              _stream(stream)), "q8_kv4_attend")
+                              _raw_stream(stream, dev)), "q8_kv4_attend")
 
 
 def kv4_attend_workspace(cache: KV4Cache, n_seq: int, tokens_per_seq: int,
                          n_q_heads: int) -> torch.Tensor:
-    """A workspace for q8_kv4_attend."""
+    """A zero-filled workspace for q8_kv4_attend."""
     nbytes = q8_kv4_attend_workspace_bytes(cache, n_seq, tokens_per_seq, n_q_heads)
     if nbytes == 0:
         raise ValueError(f"invalid attention shape: {n_seq} sequences of {tokens_per_seq} tokens, "
                          f"{n_q_heads} query heads over {cache.n_kv_heads}")
-    return torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
+    return torch.zeros(nbytes, dtype=torch.uint8, device=cache.device)
 
 
 # ------------------------------------------------- torch allocation helpers

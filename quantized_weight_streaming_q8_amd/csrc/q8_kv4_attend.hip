@@ -38,9 +38,9 @@
 // to take up, and cut into as many equal shares as are resident: every
 // workgroup has the same to do however ragged the sequences are, and a unit
 // is cut only where a share ends.  A cut unit's parts go to the workspace, and
-// a second, short launch joins them in order.  The cut is made on the GPU,
-// from pos: the host need not know the lengths, and a launch captured in a
-// graph serves any.
+// the last workgroup to leave one joins them, in their order.  The cut is made on
+// the GPU, from pos: the host need not know the lengths, and a launch captured
+// in a graph serves any.
 //
 // Heads abreast.  A page holds its positions for all key/value heads side by
 // side.  Workgroups that differ only in the head go through the same share of
@@ -55,7 +55,9 @@ namespace {
 
 // Waves of a workgroup (2 for the heads whose slots of 4 would pass 64 KB).
 __host__ __device__ constexpr int waves_of(int nb) { return nb <= 4 ? 4 : 2; }
-constexpr int kMaxShares = 768;  // three workgroups on each of 256 CUs
+// The workspace starts with a counter for each unit, at the same place for
+// every shape: calls of other shapes find them at zero too.
+constexpr size_t kCounterBytes = kMaxRowBlocks * sizeof(uint32_t);
 constexpr int kUnitCost = 12;
 constexpr int kMinSteps = 8;
 constexpr int kNoVmem = 0x0f70;  // s_waitcnt vmcnt(0), no other count
@@ -567,9 +569,28 @@ __device__ inline float part_weight(float m_part, float m, float c) {
     return m_part == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f((m_part - m) * c);
 }
 
-// The partial record of a workgroup's rows: accumulators [rows][D], then
-// their maxima and sums.
+// The partial record of a workgroup's rows: accumulators [rows][D] as two
+// halves of their float4 (floats 0, 1 of all, then 2, 3: what a wave stores or loads
+// at once is contiguous), then maxima and sums.
 __host__ __device__ constexpr int record_floats(int rows, int nb) { return rows * (nb * 32 + 2); }
+
+// Records pass from one CU to another within the launch: device-coherent
+// accesses.
+__device__ inline void publish(float* p, float v) {
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ inline void publish2(float* p, float a, float b) {
+    __hip_atomic_store(reinterpret_cast<uint64_t*>(p),
+                       (uint64_t)__float_as_uint(b) << 32 | __float_as_uint(a), __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ inline float fetch(const float* p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ inline uint64_t fetch2(const float* p) {
+    return __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED,
+                             __HIP_MEMORY_SCOPE_AGENT);
+}
 
 // How units are laid out: each starts on a share (even), or end to end.
 struct Room {
@@ -590,20 +611,6 @@ struct Sequences {
     int lo[64], hi[64], slot[64];
 };
 
-// What the main launch leaves at the start of the workspace for the join:
-// the size of a share, then the start of each sequence's room and its steps.
-struct Layout {
-    int64_t share;
-    int64_t even;
-};
-struct SequenceRoom {
-    int64_t start;
-    int32_t tiles, slot;
-};
-constexpr size_t layout_bytes(int n_seq) {
-    return (sizeof(Layout) + (size_t)n_seq * sizeof(SequenceRoom) + 255) / 256 * 256;
-}
-
 // LDS of a workgroup: the waves' slots, what the join of the waves needs
 // (apart from them: the next steps are on their way meanwhile), the counts.
 template <int NB, int RT, Fold F>
@@ -621,6 +628,7 @@ struct Shared {
     float inv[kRows];
     int flag[kRows];
     Sequences seqs;                            // 64 at a time
+    uint32_t last;
 };
 
 template <int NB, int RT, Fold F>
@@ -638,7 +646,7 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int rec_rows, float* reco
     const int n_rows = a.tokens * a.group;
     const int groups_per_page = a.c.page_tokens / kKvTile;
     const int cap = a.c.max_pages * a.c.page_tokens;
-    SequenceRoom* rooms = reinterpret_cast<SequenceRoom*>(a.workspace + sizeof(Layout));
+    uint32_t* counters = reinterpret_cast<uint32_t*>(a.workspace);  // of each unit's parts
 
     // The room of sequences s0 .. s0 + 63, in either layout.
     const int units_per_seq = a.c.n_kv / abreast * n_rb;
@@ -685,21 +693,6 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int rec_rows, float* reco
     const int64_t room = lay.even ? room_even : room_to_end;
     const int64_t share = lay.even ? kMinSteps : (room + n_shares - 1) / n_shares;
     const auto upto_of = [&](int i) { return lay.even ? (int64_t)sh.seqs.even[i] : sh.seqs.upto[i]; };
-    if (blockIdx.x == 0) {  // for the join
-        if (threadIdx.x == 0) *reinterpret_cast<Layout*>(a.workspace) = {share, lay.even};
-        int64_t sum = 0;
-        for (int s0 = 0; s0 < a.n_seq; s0 += 64) {
-            if (a.n_seq > 64) {
-                __syncthreads();
-                measure(s0);
-            }
-            const int tiles = tiles_of(sh.seqs.lo[lane], sh.seqs.hi[lane]);
-            if (wave == 0 && s0 + lane < a.n_seq)
-                rooms[s0 + lane] = {sum + upto_of(lane) - (int64_t)lay.unit(tiles) * units_per_seq, tiles,
-                                    sh.seqs.slot[lane]};
-            sum += upto_of(63);
-        }
-    }
     if (a.n_seq > 64) {
         __syncthreads();
         measure(0);
@@ -907,7 +900,19 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int rec_rows, float* reco
         }
         __syncthreads();
         // a share's records: of the unit it goes on with, of the one it leaves
-        float* const rec = records + (2 * (int64_t)blockIdx.x + (from == 0 ? 1 : 0)) * record_floats(rec_rows, NB);
+        const auto record_of = [&](int share_no, bool goes_on) {
+            return records + (2 * ((int64_t)share_no * abreast + my_head) + (goes_on ? 0 : 1)) *
+                                 record_floats(rec_rows, NB);
+        };
+        float* const rec = record_of(my_share, from > 0);
+        const int half = rec_rows * D / 2;  // floats of a half of a record's accumulators
+        const auto store_out = [&](int row, int d, v4f x) {  // 4 values of a row of the block
+            const int abs_row = rb * kRows + row;
+            const int j = abs_row / a.group, qh = head * a.group + abs_row - j * a.group;
+            const v4f y = flagged(x, sh.flag[row]);
+            *reinterpret_cast<f4u*>(a.O + ((int64_t)seq * a.tokens + j) * a.o_stride + (int64_t)qh * D +
+                                    d) = f4u{y[0], y[1], y[2], y[3]};
+        };
         float wave_max[RT];
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
@@ -923,8 +928,8 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int rec_rows, float* reco
             for (int w = 0; w < kWaves; ++w) l += sh.l[w][r] * part_weight(sh.m[w][r], m, c);
             sh.inv[r] = 1.0f / l;
             if (!whole && r < rec_rows) {
-                rec[rec_rows * D + r] = m;
-                rec[rec_rows * D + rec_rows + r] = l;
+                publish(rec + 2 * half + r, m);
+                publish(rec + 2 * half + rec_rows + r, l);
             }
         }
 #pragma unroll
@@ -958,103 +963,72 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int rec_rows, float* reco
                     x += *reinterpret_cast<const v4f*>(&sh.o[w][row][d]);
                 const int i = r * kCols + row;
                 if (whole) {
-                    const int abs_row = rb * kRows + i;
-                    const int j = abs_row / a.group, qh = head * a.group + abs_row - j * a.group;
-                    const v4f y = flagged(x * sh.inv[i], sh.flag[i]);
-                    *reinterpret_cast<f4u*>(a.O + ((int64_t)seq * a.tokens + j) * a.o_stride +
-                                            (int64_t)qh * D + d) = f4u{y[0], y[1], y[2], y[3]};
+                    store_out(i, d, x * sh.inv[i]);
                 } else {
-                    *reinterpret_cast<f4u*>(rec + i * D + d) = f4u{x[0], x[1], x[2], x[3]};
+                    float* o = rec + 2 * (i * (D / 4) + d / 4);
+                    publish2(o, x[0], x[1]);
+                    publish2(o + half, x[2], x[3]);
                 }
             }
         }
-    }
-}
+        if (whole) continue;
 
-// Join the parts of the units that were cut, in their order: a workgroup a
-// unit and row.  Its threads are D/4 lanes of 4 values by 256 / (D/4) runs of
-// the parts; the runs are added in order in LDS.
-constexpr int kJoinThreads = 256;
-
-__global__ void __launch_bounds__(kJoinThreads)
-kv4_join_kernel(AttendArgs a, int n_rb, int abreast, int per_wg, int rec_rows, const float* records) {
-    __shared__ float weight[kMaxShares], sums[kMaxShares];
-    __shared__ float wave_top[kJoinThreads / 64];
-    __shared__ float total;
-    __shared__ __align__(16) float run[kJoinThreads * 4];
-    const int D = a.c.nb * 32, lanes = D / 4, runs = kJoinThreads / lanes;
-    const int per_seq = a.c.n_kv * n_rb;
-    const int seq = (int)(blockIdx.x / per_seq), in_seq = (int)blockIdx.x - seq * per_seq;
-    const int head = in_seq / n_rb, rb = in_seq - head * n_rb;
-    const int unit_of_seq = head / abreast * n_rb + rb, my_head = head % abreast;
-    const int row = blockIdx.y, abs_row = rb * per_wg + row;
-    if (abs_row >= a.tokens * a.group) return;
-    const Layout layout = *reinterpret_cast<const Layout*>(a.workspace);
-    const int64_t share = layout.share;
-    const Room lay = {layout.even != 0};
-    const SequenceRoom s = reinterpret_cast<const SequenceRoom*>(a.workspace + sizeof(Layout))[seq];
-    const int64_t steps_at = s.start + (int64_t)unit_of_seq * lay.unit(s.tiles) + lay.cost();
-    // shares w0 .. w1 hold its steps
-    const int w0 = (int)(steps_at / share), w1 = (int)((steps_at + max(s.tiles, 1) - 1) / share);
-    if (w0 == w1) return;
-    const int parts = w1 - w0 + 1, size = record_floats(rec_rows, a.c.nb);
-    const auto record = [&](int i) { 
-        return records + (2 * ((int64_t)(w0 + i) * abreast + my_head) + (i == 0 ? 1 : 0)) * size;
-    };
-    const int d = (int)threadIdx.x % lanes, p = (int)threadIdx.x / lanes;
-    const int i0 = p < runs ? parts * p / runs : 0, i1 = p < runs ? parts * (p + 1) / runs : 0;
-    constexpr int kEarly = 4;  // parts of a run that are loaded before the weights are known
-    v4f early[kEarly];
+        // ---- join the parts of the unit: the last workgroup to leave one
+        const uint32_t step_share = (uint32_t)min(share, (int64_t)INT32_MAX);
+        const int parts_before = (int)(((uint32_t)from + step_share - 1) / step_share);
+        const int parts = parts_before + 1 + (int)(((uint32_t)(steps - upto) + step_share - 1) / step_share);
+        uint32_t* const counter = counters + ((int64_t)seq * a.c.n_kv + head) * n_rb + rb;
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's stores are there
+        __syncthreads();
+        if (thread == 0)
+            sh.last = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                      (uint32_t)parts - 1;
+        __syncthreads();
+        if (!sh.last) continue;
+        if (thread == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        const int live = min(kRows, n_rows - rb * kRows);
+        for (int u = thread; u < live * (D / 4); u += kThreads) {
+            const int row = u / (D / 4), d = (u - row * (D / 4)) * 4;
+            v4f x = {0.f, 0.f, 0.f, 0.f};
+            float top = -__builtin_inff(), sum = 0.0f;
+            constexpr int kAtOnce = 8;  // parts whose loads travel together
+            for (int i0 = 0; i0 < parts; i0 += kAtOnce) {
+                float m[kAtOnce], l[kAtOnce];
+                uint64_t lo[kAtOnce], hi[kAtOnce];
 #pragma unroll
-    for (int k = 0; k < kEarly; ++k) {
-        const f4u y = *reinterpret_cast<const f4u*>(record(min(i0 + k, parts - 1)) + row * D + 4 * d);
-        early[k] = v4f{y[0], y[1], y[2], y[3]};
-    }
-    float top = -__builtin_inff();
-    for (int i = threadIdx.x; i < parts; i += kJoinThreads) {
-        const float* r = record(i) + rec_rows * D + row;
-        weight[i] = r[0];
-        sums[i] = r[rec_rows];
-        top = fmaxf(top, r[0]);
-    }
+                for (int k = 0; k < kAtOnce; ++k) {
+                    const int i = min(i0 + k, parts - 1);  // past the last: that again, unused
+                    const float* p = record_of(my_share - parts_before + i, i > 0);
+                    m[k] = fetch(p + 2 * half + row);
+                    l[k] = fetch(p + 2 * half + rec_rows + row);
+                    lo[k] = fetch2(p + 2 * u);
+                    hi[k] = fetch2(p + half + 2 * u);
+                }
+                float now_top = top;
 #pragma unroll
-    for (int k = 1; k < 64; k <<= 1) top = fmaxf(top, __shfl_xor(top, k));
-    if ((threadIdx.x & 63) == 0) wave_top[threadIdx.x >> 6] = top;
-    __syncthreads();
-    for (int k = 0; k < kJoinThreads / 64; ++k) top = fmaxf(top, wave_top[k]);
-    for (int i = threadIdx.x; i < parts; i += kJoinThreads)
-        weight[i] = part_weight(weight[i], top, a.scale_log2 * kScoreUnit);
-    __syncthreads();
-    v4f x = {0.f, 0.f, 0.f, 0.f};
+                for (int k = 0; k < kAtOnce; ++k) now_top = fmaxf(now_top, m[k]);
+                const float f = part_weight(top, now_top, c);
+                top = now_top;
+                x *= f;
+                sum *= f;
 #pragma unroll
-    for (int k = 0; k < kEarly; ++k)
-        if (i0 + k < i1) x += early[k] * weight[i0 + k];
-    for (int i = i0 + kEarly; i < i1; ++i) {
-        const f4u y = *reinterpret_cast<const f4u*>(record(i) + row * D + 4 * d);
-        x += v4f{y[0], y[1], y[2], y[3]} * weight[i];
+                for (int k = 0; k < kAtOnce; ++k) {
+                    if (i0 + k >= parts) continue;
+                    const float w = part_weight(m[k], top, c);
+                    x += v4f{__uint_as_float((uint32_t)lo[k]), __uint_as_float((uint32_t)(lo[k] >> 32)),
+                             __uint_as_float((uint32_t)hi[k]), __uint_as_float((uint32_t)(hi[k] >> 32))} * w;
+                    sum += l[k] * w;
+                }
+            }
+            store_out(row, d, x * (1.0f / sum));
+        }
     }
-    *reinterpret_cast<v4f*>(run + 4 * threadIdx.x) = x;
-    if (threadIdx.x == 0) {
-        float l = 0.0f;
-        for (int i = 0; i < parts; ++i) l += sums[i] * weight[i];
-        total = l;
-    }
-    __syncthreads();
-    if (p != 0) return;
-    for (int k = 1; k < runs; ++k) x += *reinterpret_cast<const v4f*>(run + 4 * (k * lanes + d));
-    const int j = abs_row / a.group, qh = head * a.group + abs_row - j * a.group;
-    const int64_t t = (int64_t)seq * a.tokens + j;
-    const int flag = row_flag(a.pos[t], a.batch_index[t], s.slot, a.c.n_slots,
-                              a.c.max_pages * a.c.page_tokens);
-    const v4f y = flagged(x * (1.0f / total), flag);
-    *reinterpret_cast<f4u*>(a.O + t * a.o_stride + (int64_t)qh * D + 4 * d) = f4u{y[0], y[1], y[2], y[3]};
 }
 
 struct Plan {
     int rt, per_wg, n_rb, abreast, rec_rows;
     bool folded;
     unsigned wgs;
-    bool cut;  // units may be cut
     int64_t units;
 };
 
@@ -1079,7 +1053,6 @@ Plan plan_attend(const AttendArgs& a) {
     const int64_t most = p.units / p.abreast * ((tiles + kMinSteps - 1) / kMinSteps);
     const int64_t shares = std::min<int64_t>(256 * per_cu / p.abreast, most);
     p.wgs = (unsigned)(shares * p.abreast);
-    p.cut = tiles > kMinSteps || p.units / p.abreast > shares;
     return p;
 }
 
@@ -1105,27 +1078,23 @@ hipError_t launch(const Plan& p, const AttendArgs& a, float* records, hipStream_
 }  // namespace
 
 size_t kv4_attend_workspace(const AttendArgs& a) {
-    return layout_bytes(a.n_seq) + records_bytes(plan_attend(a), a.c.nb);
+    return kCounterBytes + records_bytes(plan_attend(a), a.c.nb);
 }
 
 hipError_t launch_kv4_attend(const AttendArgs& a, hipStream_t st) {
     const Plan p = plan_attend(a);
-    float* records = reinterpret_cast<float*>(a.workspace + layout_bytes(a.n_seq));
-    hipError_t e = hipErrorInvalidValue;
+    float* records = reinterpret_cast<float*>(a.workspace + kCounterBytes);
     switch (a.c.nb) {
-        case 1: e = launch<1>(p, a, records, st); break;
-        case 2: e = launch<2>(p, a, records, st); break;
-        case 3: e = launch<3>(p, a, records, st); break;
-        case 4: e = launch<4>(p, a, records, st); break;
-        case 5: e = launch<5>(p, a, records, st); break;
-        case 6: e = launch<6>(p, a, records, st); break;
-        case 7: e = launch<7>(p, a, records, st); break;
-        case 8: e = launch<8>(p, a, records, st); break;
+        case 1: return launch<1>(p, a, records, st);
+        case 2: return launch<2>(p, a, records, st);
+        case 3: return launch<3>(p, a, records, st);
+        case 4: return launch<4>(p, a, records, st);
+        case 5: return launch<5>(p, a, records, st);
+        case 6: return launch<6>(p, a, records, st);
+        case 7: return launch<7>(p, a, records, st);
+        case 8: return launch<8>(p, a, records, st);
     }
-    if (e != hipSuccess || !p.cut) return e;
-    hipLaunchKernelGGL(kv4_join_kernel, dim3((unsigned)p.units, (unsigned)p.rec_rows), dim3(kJoinThreads),
-                       0, st, a, p.n_rb, p.abreast, p.per_wg, p.rec_rows, records);
-    return hipGetLastError();
+    return hipErrorInvalidValue;
 }
 
 }  // namespace q8

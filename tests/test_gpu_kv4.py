@@ -399,8 +399,8 @@ def test_attend_idle_and_bad_rows(q8, tokens, group):
         assert (got[4 * t] == 0).all() and np.isnan(got[4 * t + 2]).all()
         for j in (1, 3):
             assert (np.abs(got[4 * t + j] - want[4 * t + j]) <= tol[4 * t + j]).all()
-    # the call repeats, whatever the workspace holds
-    s.ws.fill_(255)
+    # every counter of the workspace is back at zero, and the call repeats
+    assert not s.ws[:1 << 20].any()
     assert np.array_equal(s.run(), got, equal_nan=True)
 
 
@@ -472,6 +472,7 @@ def test_attend_more_than_runs_at_once(q8, n, tokens):
     s = Step(q8, 64, 4, 4, tokens, 32, lens, slots=n)
     got = s.check()
     assert np.array_equal(s.run(), got)
+    assert not s.ws[:1 << 20].any()
 
 
 def test_attend_many_sequences(q8):

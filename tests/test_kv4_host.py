@@ -201,7 +201,7 @@ def test_attend_workspace_is_bounded(q8):
     A = ctypes.addressof
     sizes = [ws(A(_cache(q8, max_pages=n)), 16, 1, 40) for n in (1, 8, 9, 100, 1000, 100000)]
     assert sizes == sorted(sizes) and sizes[0] < sizes[-1] == sizes[-2]
-    assert sizes[-1] <= 2 * 768 * 5 * 130 * 4 + 4096
+    assert sizes[-1] <= (1 << 20) + 2 * 768 * 5 * 130 * 4
 
 
 # --------------------------------------------------------- binding checks
