@@ -604,6 +604,44 @@ struct Room {
     }
 };
 
+// The room cut into shares.  Even layout: kMinSteps each.  End to end: one for
+// each resident workgroup.  Where three share a CU, those dispatched first
+// (the first third) get ahead of the others in its issue slots, and the last
+// ones would run on alone: the thirds' shares are in the ratio 23 : 20 : 17, at
+// which they end about together (16 sessions up to 8192 tokens 31.5 -> 28.6 us,
+// near 32768 tokens 103.8 -> 99.0, against equal shares; at 26 : 20 : 14, 29.0
+// and 100.8).
+struct Shares {
+    int64_t room;
+    double unit;  // room of a share of weight 1
+    int n, third;
+    bool even, equal;
+
+    __device__ Shares(int64_t room_, int n_, bool even_, bool equal_)
+        : room(room_), n(n_), third(n_ / 3), even(even_), equal(equal_) {
+        unit = (double)room / weight(n);
+    }
+    __device__ int weight(int i) const {  // of the first i shares
+        if (equal) return i;
+        return 23 * min(i, third) + 20 * max(min(i - third, third), 0) + 17 * max(i - 2 * third, 0);
+    }
+    __device__ int64_t start(int i) const {
+        if (even) return min((int64_t)kMinSteps * i, room);
+        return i >= n ? room : (int64_t)(unit * weight(i));
+    }
+    __device__ int at(int64_t pos) const {  // the share that holds pos
+        if (even) return (int)(pos / kMinSteps);
+        const int w = (int)((double)pos / unit);
+        int i = equal ? w
+                : w < 23 * third ? w / 23
+                : w < 43 * third ? third + (w - 23 * third) / 20 : 2 * third + (w - 43 * third) / 17;
+        i = min(i, n - 1);
+        while (start(i) > pos) --i;
+        while (start(i + 1) <= pos) ++i;
+        return i;
+    }
+};
+
 // Extents of 64 sequences and the room up to each one's end.
 struct Sequences {
     int64_t upto[64];              // end to end
@@ -633,7 +671,7 @@ struct Shared {
 
 template <int NB, int RT, Fold F>
 __global__ void __launch_bounds__(64 * waves_of(NB), RT == 1 && NB <= 4 ? (F == kFolded ? 3 : 2) : 1)
-kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int rec_rows, float* records) {
+kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int per_cu, int rec_rows, float* records) {
     using Sh = Shared<NB, RT, F>;
     constexpr int D = NB * 32;
     constexpr int kWaves = Sh::kWaves, kThreads = 64 * kWaves;
@@ -691,15 +729,15 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int rec_rows, float* reco
     }
     const Room lay = {room_even <= (int64_t)kMinSteps * n_shares};
     const int64_t room = lay.even ? room_even : room_to_end;
-    const int64_t share = lay.even ? kMinSteps : (room + n_shares - 1) / n_shares;
+    const Shares shares(room, n_shares, lay.even, per_cu != 3);
     const auto upto_of = [&](int i) { return lay.even ? (int64_t)sh.seqs.even[i] : sh.seqs.upto[i]; };
     if (a.n_seq > 64) {
         __syncthreads();
         measure(0);
     }
     // This workgroup's share: [at, end) of the room.
-    int64_t at = share * my_share;
-    const int64_t end = min(at + share, room);
+    int64_t at = shares.start(my_share);
+    const int64_t end = shares.start(my_share + 1);
     if (at >= end) return;
     int seq0 = 0;        // sequences seq0 .. seq0 + 63 are in LDS,
     int64_t before = 0;  // and so much room lies before them
@@ -974,9 +1012,9 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int rec_rows, float* reco
         if (whole) continue;
 
         // ---- join the parts of the unit: the last workgroup to leave one
-        const uint32_t step_share = (uint32_t)min(share, (int64_t)INT32_MAX);
-        const int parts_before = (int)(((uint32_t)from + step_share - 1) / step_share);
-        const int parts = parts_before + 1 + (int)(((uint32_t)(steps - upto) + step_share - 1) / step_share);
+        const int first_share = from == 0 ? my_share : shares.at(steps_at);
+        const int last_share = upto == steps ? my_share : shares.at(steps_at + steps - 1);
+        const int parts = __builtin_amdgcn_readfirstlane(last_share - first_share + 1);
         uint32_t* const counter = counters + ((int64_t)seq * a.c.n_kv + head) * n_rb + rb;
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's stores are there
         __syncthreads();
@@ -987,18 +1025,19 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int rec_rows, float* reco
         if (!sh.last) continue;
         if (thread == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         const int live = min(kRows, n_rows - rb * kRows);
+#pragma unroll RT
         for (int u = thread; u < live * (D / 4); u += kThreads) {
             const int row = u / (D / 4), d = (u - row * (D / 4)) * 4;
             v4f x = {0.f, 0.f, 0.f, 0.f};
             float top = -__builtin_inff(), sum = 0.0f;
-            constexpr int kAtOnce = 8;  // parts whose loads travel together
+            constexpr int kAtOnce = 4;  // parts whose loads travel together
             for (int i0 = 0; i0 < parts; i0 += kAtOnce) {
                 float m[kAtOnce], l[kAtOnce];
                 uint64_t lo[kAtOnce], hi[kAtOnce];
 #pragma unroll
                 for (int k = 0; k < kAtOnce; ++k) {
                     const int i = min(i0 + k, parts - 1);  // past the last: that again, unused
-                    const float* p = record_of(my_share - parts_before + i, i > 0);
+                    const float* p = record_of(first_share + i, i > 0);
                     m[k] = fetch(p + 2 * half + row);
                     l[k] = fetch(p + 2 * half + rec_rows + row);
                     lo[k] = fetch2(p + 2 * u);
@@ -1026,7 +1065,7 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int rec_rows, float* reco
 }
 
 struct Plan {
-    int rt, per_wg, n_rb, abreast, rec_rows;
+    int rt, per_wg, per_cu, n_rb, abreast, rec_rows;
     bool folded;
     unsigned wgs;
     int64_t units;
@@ -1045,13 +1084,13 @@ Plan plan_attend(const AttendArgs& a) {
     p.units = (int64_t)a.n_seq * a.c.n_kv * p.n_rb;
     // Workgroups resident at once: each takes one share, more would only wait.
     // Fewer where full sequences have no more least shares.
-    const int per_cu = p.rt > 1 ? 1 : nb <= 4 && p.folded ? 3 : 2;
+    p.per_cu = p.rt > 1 ? 1 : nb <= 4 && p.folded ? 3 : 2;
     const int64_t tiles = ((int64_t)a.c.max_pages * a.c.page_tokens + kKvTile - 1) / kKvTile;
     p.abreast = 1;
     for (int d = 2; d <= 32 && d <= a.c.n_kv; ++d)
         if (a.c.n_kv % d == 0) p.abreast = d;
     const int64_t most = p.units / p.abreast * ((tiles + kMinSteps - 1) / kMinSteps);
-    const int64_t shares = std::min<int64_t>(256 * per_cu / p.abreast, most);
+    const int64_t shares = std::min<int64_t>(256 * p.per_cu / p.abreast, most);
     p.wgs = (unsigned)(shares * p.abreast);
     return p;
 }
@@ -1063,7 +1102,7 @@ size_t records_bytes(const Plan& p, int nb) {
 template <int NB, int RT, Fold F>
 hipError_t launch_one(const Plan& p, const AttendArgs& a, float* records, hipStream_t st) {
     hipLaunchKernelGGL((kv4_attend_kernel<NB, RT, F>), dim3(p.wgs), dim3(64 * waves_of(NB)), 0, st, a,
-                       p.n_rb, p.abreast, p.rec_rows, records);
+                       p.n_rb, p.abreast, p.per_cu, p.rec_rows, records);
     return hipGetLastError();
 }
 
