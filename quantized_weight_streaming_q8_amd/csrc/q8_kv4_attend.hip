@@ -352,10 +352,13 @@ __device__ inline void read_query(const QueryLds<F>& in, int lane, Query<F>& q) 
 }
 
 // Carried state of one column tile.
-template <int NB, Fold F>
+template <int NB, int RT, Fold F>
 struct Rows {
+    // Two tiles' queries stay in LDS and are read at each step: their registers
+    // let two workgroups share a CU instead of one.
+    static constexpr bool kInLds = RT > 1;
     static constexpr int kQuads = (NB + 3) / 4;
-    Query<F> q[kQuads];
+    Query<F> q[kInLds ? 1 : kQuads];
     v4f o[NB][2];        // O^T: dim 32b + 2(4g + i) + e in o[b][e][i]
     float m, l;          // running maximum (of the scores) and this lane's share of the sum
     int lo, hi;          // positions this column sees
@@ -370,30 +373,47 @@ __device__ inline v4f mfma_scaled(u4 k, uint32_t ks, v6u q, uint32_t qs, v4f c) 
 }
 
 template <int NB, int RT, Fold F, int I>
-__device__ inline void score_piece(const Keys<NB>& k, const Rows<NB, F> (&rows)[RT], int q, v4f (&S)[RT][2]) {
+__device__ inline void score_piece(const Keys<NB>& k, const Rows<NB, RT, F> (&rows)[RT],
+                                   const QueryLds<F> (&query)[RT][Keys<NB>::kQuads], int lane, int q,
+                                   v4f (&S)[RT][2]) {
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-        const Query<F>& y = rows[r].q[q];
-        S[r][0] = mfma_scaled<0, (I & 3)>(k.c[0][q], k.s[q], y.p[I], y.s[I >> 2], S[r][0]);
-        S[r][1] = mfma_scaled<1, (I & 3)>(k.c[1][q], k.s[q], y.p[I], y.s[I >> 2], S[r][1]);
+        v6u y;
+        uint32_t ys;
+        if constexpr (Rows<NB, RT, F>::kInLds) {
+#pragma unroll
+            for (int v = 0; v < 3; ++v) {
+                const uint2 w = query[r][q].p[3 * I + v][lane];
+                y[2 * v] = w.x;
+                y[2 * v + 1] = w.y;
+            }
+            ys = query[r][q].s[I >> 2][lane];
+        } else {
+            y = rows[r].q[q].p[I];
+            ys = rows[r].q[q].s[I >> 2];
+        }
+        S[r][0] = mfma_scaled<0, (I & 3)>(k.c[0][q], k.s[q], y, ys, S[r][0]);
+        S[r][1] = mfma_scaled<1, (I & 3)>(k.c[1][q], k.s[q], y, ys, S[r][1]);
     }
 }
 
 template <int NB, int RT, Fold F>
-__device__ inline void scores(const Keys<NB>& k, const Rows<NB, F> (&rows)[RT], v4f (&S)[RT][2]) {
+__device__ inline void scores(const Keys<NB>& k, const Rows<NB, RT, F> (&rows)[RT],
+                              const QueryLds<F> (&query)[RT][Keys<NB>::kQuads], int lane,
+                              v4f (&S)[RT][2]) {
     const v4f zero = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int r = 0; r < RT; ++r) S[r][0] = S[r][1] = zero;
 #pragma unroll
     for (int q = 0; q < Keys<NB>::kQuads; ++q) {  // small pieces first
         if constexpr (F == kWide) {
-            score_piece<NB, RT, F, 5>(k, rows, q, S);
-            score_piece<NB, RT, F, 4>(k, rows, q, S);
-            score_piece<NB, RT, F, 3>(k, rows, q, S);
+            score_piece<NB, RT, F, 5>(k, rows, query, lane, q, S);
+            score_piece<NB, RT, F, 4>(k, rows, query, lane, q, S);
+            score_piece<NB, RT, F, 3>(k, rows, query, lane, q, S);
         }
-        score_piece<NB, RT, F, 2>(k, rows, q, S);
-        score_piece<NB, RT, F, 1>(k, rows, q, S);
-        score_piece<NB, RT, F, 0>(k, rows, q, S);
+        score_piece<NB, RT, F, 2>(k, rows, query, lane, q, S);
+        score_piece<NB, RT, F, 1>(k, rows, query, lane, q, S);
+        score_piece<NB, RT, F, 0>(k, rows, query, lane, q, S);
     }
     if constexpr (F == kFolded) {
 #pragma unroll
@@ -405,7 +425,7 @@ __device__ inline void scores(const Keys<NB>& k, const Rows<NB, F> (&rows)[RT], 
 
 // A step that some row does not see whole, or whose page is not there (bad).
 template <int NB, int RT, Fold F>
-__device__ inline void mask_step(Values<NB>& v, Rows<NB, F> (&rows)[RT], v4f (&S)[RT][2], int tok, int g,
+__device__ inline void mask_step(Values<NB>& v, Rows<NB, RT, F> (&rows)[RT], v4f (&S)[RT][2], int tok, int g,
                                  bool bad, int lo, int hi) {
     // Positions outside [lo, hi), which no row sees, may hold anything:
     // their values and scales become zeros, so that 0 * NaN cannot arise.
@@ -453,7 +473,7 @@ __device__ inline void mask_step(Values<NB>& v, Rows<NB, F> (&rows)[RT], v4f (&S
 }
 
 template <int NB, int RT, Fold F>
-__device__ inline void softmax_and_values(const Values<NB>& v, Rows<NB, F> (&rows)[RT], v4f (&S)[RT][2],
+__device__ inline void softmax_and_values(const Values<NB>& v, Rows<NB, RT, F> (&rows)[RT], v4f (&S)[RT][2],
                                           float c, float lag, uint32_t keep) {
     constexpr int P = F == kWide ? 3 : 2;
     u4 p[RT][P];
@@ -670,7 +690,7 @@ struct Shared {
 };
 
 template <int NB, int RT, Fold F>
-__global__ void __launch_bounds__(64 * waves_of(NB), RT == 1 && NB <= 4 ? (F == kFolded ? 3 : 2) : 1)
+__global__ void __launch_bounds__(64 * waves_of(NB), NB <= 4 ? (F == kFolded ? 3 : 2) : 1)
 kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int per_cu, int rec_rows, float* records) {
     using Sh = Shared<NB, RT, F>;
     constexpr int D = NB * 32;
@@ -791,7 +811,7 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int per_cu, int rec_rows,
         };
         int ids = 0;
         if (slot >= 0) ids = load_ids(page0);
-        Rows<NB, F> rows[RT];
+        Rows<NB, RT, F> rows[RT];
         int row_pos[RT], row_slot[RT];
         // Operand (r, k) of the queries is made by one wave, not the same one
         // for the workgroups that share a CU.
@@ -878,10 +898,11 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int per_cu, int rec_rows,
             make_query<F>(x, y, lane, sh.query[r][k]);
         }
         __syncthreads();
+        if constexpr (!Rows<NB, RT, F>::kInLds)
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
+            for (int r = 0; r < RT; ++r)
 #pragma unroll
-            for (int k = 0; k < kQuads; ++k) read_query<F>(sh.query[r][k], lane, rows[r].q[k]);
+                for (int k = 0; k < kQuads; ++k) read_query<F>(sh.query[r][k], lane, rows[r].q[k]);
 #pragma unroll
         for (int d = 1; d < 16; d <<= 1) {
             all_lo = max(all_lo, __shfl_xor(all_lo, d));
@@ -912,7 +933,7 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int per_cu, int rec_rows,
             Values<NB> vals;
             v4f S[RT][2];
             read_keys<NB>(in, lane, keys);
-            scores<NB, RT, F>(keys, rows, S);
+            scores<NB, RT, F>(keys, rows, sh.query, lane, S);
             read_values<NB>(in, lane, vals);
             wait_lds_reads();
             const bool none = bad >> now & 1;
@@ -1084,7 +1105,7 @@ Plan plan_attend(const AttendArgs& a) {
     p.units = (int64_t)a.n_seq * a.c.n_kv * p.n_rb;
     // Workgroups resident at once: each takes one share, more would only wait.
     // Fewer where full sequences have no more least shares.
-    p.per_cu = p.rt > 1 ? 1 : nb <= 4 && p.folded ? 3 : 2;
+    p.per_cu = nb <= 4 && p.folded ? 3 : 2;
     const int64_t tiles = ((int64_t)a.c.max_pages * a.c.page_tokens + kKvTile - 1) / kKvTile;
     p.abreast = 1;
     for (int d = 2; d <= 32 && d <= a.c.n_kv; ++d)
