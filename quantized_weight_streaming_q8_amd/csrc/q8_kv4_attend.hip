@@ -625,25 +625,27 @@ struct Room {
 };
 
 // The room cut into shares.  Even layout: kMinSteps each.  End to end: one for
-// each resident workgroup.  Where three share a CU, those dispatched first
-// (the first third) get ahead of the others in its issue slots, and the last
-// ones would run on alone: the thirds' shares are in the ratio 23 : 20 : 17, at
-// which they end about together (16 sessions up to 8192 tokens 31.5 -> 28.6 us,
-// near 32768 tokens 103.8 -> 99.0, against equal shares; at 26 : 20 : 14, 29.0
-// and 100.8).
+// each resident workgroup.  Where several share a CU, those dispatched first
+// get ahead of the others in its issue slots, and the last ones would run on
+// alone: shares are weighted by rank, 23 : 20 : 17 for three (16 sessions up to
+// 8192 tokens 31.5 -> 28.6 us, near 32768 tokens 103.8 -> 99.0, against equal
+// shares; at 26 : 20 : 14, 29.0 and 100.8) and 5 : 4 for two (drafts 39.1 -> 38.4).
 struct Shares {
     int64_t room;
-    double unit;  // room of a share of weight 1
-    int n, third;
-    bool even, equal;
+    double unit;   // room of a share of weight 1
+    int n, rank;   // shares in all, and of one rank
+    int w[3];      // weight of a share by its rank
+    bool even;
 
-    __device__ Shares(int64_t room_, int n_, bool even_, bool equal_)
-        : room(room_), n(n_), third(n_ / 3), even(even_), equal(equal_) {
+    __device__ Shares(int64_t room_, int n_, bool even_, int per_cu)
+        : room(room_), n(n_), rank(n_ / per_cu), even(even_) {
+        w[0] = per_cu == 3 ? 23 : per_cu == 2 ? 5 : 1;
+        w[1] = per_cu == 3 ? 20 : per_cu == 2 ? 4 : 1;
+        w[2] = per_cu == 3 ? 17 : w[1];
         unit = (double)room / weight(n);
     }
     __device__ int weight(int i) const {  // of the first i shares
-        if (equal) return i;
-        return 23 * min(i, third) + 20 * max(min(i - third, third), 0) + 17 * max(i - 2 * third, 0);
+        return w[0] * min(i, rank) + w[1] * max(min(i - rank, rank), 0) + w[2] * max(i - 2 * rank, 0);
     }
     __device__ int64_t start(int i) const {
         if (even) return min((int64_t)kMinSteps * i, room);
@@ -651,10 +653,8 @@ struct Shares {
     }
     __device__ int at(int64_t pos) const {  // the share that holds pos
         if (even) return (int)(pos / kMinSteps);
-        const int w = (int)((double)pos / unit);
-        int i = equal ? w
-                : w < 23 * third ? w / 23
-                : w < 43 * third ? third + (w - 23 * third) / 20 : 2 * third + (w - 43 * third) / 17;
+        const int v = (int)((double)pos / unit), v0 = w[0] * rank, v1 = v0 + w[1] * rank;
+        int i = v < v0 ? v / w[0] : v < v1 ? rank + (v - v0) / w[1] : 2 * rank + (v - v1) / w[2];
         i = min(i, n - 1);
         while (start(i) > pos) --i;
         while (start(i + 1) <= pos) ++i;
@@ -749,7 +749,7 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int per_cu, int rec_rows,
     }
     const Room lay = {room_even <= (int64_t)kMinSteps * n_shares};
     const int64_t room = lay.even ? room_even : room_to_end;
-    const Shares shares(room, n_shares, lay.even, per_cu != 3);
+    const Shares shares(room, n_shares, lay.even, per_cu);
     const auto upto_of = [&](int i) { return lay.even ? (int64_t)sh.seqs.even[i] : sh.seqs.upto[i]; };
     if (a.n_seq > 64) {
         __syncthreads();
@@ -1051,7 +1051,7 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int per_cu, int rec_rows,
             const int row = u / (D / 4), d = (u - row * (D / 4)) * 4;
             v4f x = {0.f, 0.f, 0.f, 0.f};
             float top = -__builtin_inff(), sum = 0.0f;
-            constexpr int kAtOnce = 4;  // parts whose loads travel together
+            constexpr int kAtOnce = RT > 1 ? 8 : 4;  // parts whose loads travel together
             for (int i0 = 0; i0 < parts; i0 += kAtOnce) {
                 float m[kAtOnce], l[kAtOnce];
                 uint64_t lo[kAtOnce], hi[kAtOnce];
