@@ -152,9 +152,6 @@ q8_status q8_kv4_read(const q8_kv4_cache* cache, const int32_t* batch_index, con
         !aligned(pos, 4) || (K == nullptr && V == nullptr) || (K != nullptr && !aligned(K, 4)) ||
         (V != nullptr && !aligned(V, 4)))
         return Q8_ERR_INVALID_ARG;
-    // one thread per 4 values, below 2^32 threads a launch
-    if ((int64_t)cache->n_kv_heads * cache->head_dim / 4 > (int64_t(1) << 31) / n_rows)
-        return Q8_ERR_INVALID_ARG;
     if (!q8_device_supported()) return Q8_ERR_UNSUPPORTED;
     return from_hip(q8::launch_kv4_read(view(cache), batch_index, pos, n_rows, K, V, stream));
 }

@@ -146,6 +146,47 @@ __device__ inline uint32_t encode2(uint32_t q, float a, float b, int s) {
                                                     __uint_as_float((uint32_t)s << 23), B);
 }
 
+// The 4 values x from d on of a head at src, rotated; d < 2 r.half.  V = 4:
+// the rotated part and its halves are whole units.
+template <int V>
+__device__ inline void turn_unit(float (&x)[4], const float* src, int d, const RotaryView& r,
+                                 const double2* cs) {
+    if (V == 4 && r.interleaved) {
+        turn(cs[d >> 1], x[0], x[1]);
+        turn(cs[(d >> 1) + 1], x[2], x[3]);
+    } else if (V == 4) {
+        const bool first = d < r.half;
+        const int i = first ? d : d - r.half;
+        float y[4];
+        load_v<4>(src + (first ? d + r.half : i), y);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (first) turn(cs[i + j], x[j], y[j]);
+            else turn(cs[i + j], y[j], x[j]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int e = d + j;
+            if (e >= 2 * r.half) continue;
+            const bool first = r.interleaved ? (e & 1) == 0 : e < r.half;
+            const int i = r.interleaved ? e >> 1 : first ? e : e - r.half;
+            float y = src[r.interleaved ? e ^ 1 : first ? e + r.half : i];
+            if (first) turn(cs[i], x[j], y);
+            else turn(cs[i], y, x[j]);
+        }
+    }
+}
+
+// The row of a workgroup: neighbouring rows, which write into the same lines
+// of the cache where they are neighbouring positions, go to one XCD (of 8,
+// which take workgroups in turn) and meet in its L2.
+__device__ inline int64_t row_of(unsigned block, unsigned n_rows) {
+    if (n_rows < 256) return block;
+    const unsigned per = n_rows / 8, tail = 8 * per;
+    return block < tail ? (block & 7) * per + (block >> 3) : block;
+}
+
 // One workgroup: one row and either a share of its query heads (blockIdx.y <
 // q_wgs) or a share of its keys and values.
 template <int V>
@@ -155,7 +196,7 @@ kv4_append_kernel(KvView c, const float* q, const float* __restrict__ k, const f
                   const int32_t* __restrict__ pos, RotaryView r, int q_units, int q_per_wg, int q_wgs,
                   float* q_out, int64_t q_out_stride, int kv_per_wg) {
     __shared__ double2 cs[Q8_KV4_MAX_HEAD_DIM / 2];
-    const int64_t t = blockIdx.x;
+    const int64_t t = row_of(blockIdx.x, gridDim.x);
     const int p = pos[t];
     const int D = c.nb * 32;
     if ((int)blockIdx.y < q_wgs) {
@@ -179,27 +220,7 @@ kv4_append_kernel(KvView c, const float* q, const float* __restrict__ k, const f
         const float* src = (is_v ? v : k) + t * row_stride + (int64_t)h * D;
         float x[4];
         load_v<4>(src + d, x);
-        if (!is_v && d < 2 * r.half) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int e = d + j;
-                if (e >= 2 * r.half) continue;
-                int i, mate;
-                bool first;
-                if (r.interleaved) {
-                    i = e >> 1;
-                    mate = e ^ 1;
-                    first = (e & 1) == 0;
-                } else {
-                    first = e < r.half;
-                    i = first ? e : e - r.half;
-                    mate = first ? e + r.half : i;
-                }
-                const double2 w = cs[i];
-                const double a = x[j], b = src[mate];
-                x[j] = first ? (float)(a * w.x - b * w.y) : (float)(b * w.y + a * w.x);
-            }
-        }
+        if (!is_v && d < 2 * r.half) turn_unit<V>(x, src, d, r, cs);
         const int s = block_scale(x);
         const int b = d >> 5, l = (d & 31) >> 2;  // block of the head, lane of the block
         uint8_t* head = c.pages + pg * c.page_bytes + h * c.head_bytes;
@@ -224,44 +245,54 @@ kv4_append_kernel(KvView c, const float* q, const float* __restrict__ k, const f
 
 // -------------------------------------------------------------------- read
 
-// One thread per 4 values; blockIdx.y 0: keys, 1: values (either may be null).
+// A workgroup per row and share of its units: 8 values of a block, first the
+// keys (the low and high nibbles of 4 bytes: values 4n .. and 16 + 4n ..), then
+// the values (4 bytes: values 8n ..).
 __global__ void __launch_bounds__(kThreads)
 kv4_read_kernel(KvView c, const int32_t* __restrict__ batch_index, const int32_t* __restrict__ pos,
-                int64_t units, float* k, float* v) {
-    const bool is_v = blockIdx.y == 1;
-    float* out = is_v ? v : k;
-    const int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (out == nullptr || u >= units) return;
-    const int D = c.nb * 32, per_row = c.n_kv * D / 4;
-    const int64_t t = u / per_row;
-    const int w = (int)(u - t * per_row), h = w / (D / 4), d = (w - h * (D / 4)) * 4;
+                int units, int per_wg, float* k, float* v) {
+    const int64_t t = row_of(blockIdx.x, gridDim.x);
     const int p = pos[t];
     const int64_t pg = kv_page(c, batch_index[t], p);
-    const float nan = __builtin_nanf("");
-    f4u y = {nan, nan, nan, nan};
-    if (pg >= 0) {
-            const uint8_t* head = c.pages + pg * c.page_bytes + h * c.head_bytes;
-        const int tok = p % c.page_tokens, b = d >> 5, l = (d & 31) >> 2;
-        uint32_t code;  // four nibbles
-        int s;
-        if (is_v) {
-            const uint8_t* o = head + v_code_offset(c.nb, tok, b, 2 * l);
-            code = o[0] | (uint32_t)o[8 * min(2, c.nb - (b & ~1))] << 8;
-            s = head[v_scale_offset(c.nb, tok, b)];
-        } else {
-            const uint32_t w =
-                *reinterpret_cast<const uint32_t*>(head + k_code_offset(c.nb, tok, b, l & 3)) >> (l & 4);
-            code = (w & 0xfu) | (w >> 4 & 0xf0u) | (w >> 8 & 0xf00u) | (w >> 12 & 0xf000u);
-            s = head[k_scale_offset(c.nb, tok, b)];
+    const int tok = pg < 0 ? 0 : p % c.page_tokens;
+    const uint8_t* page = c.pages + (pg < 0 ? 0 : pg) * c.page_bytes;
+    const int D = c.nb * 32, per_head = D / 8, heads_units = c.n_kv * per_head;
+    const int u0 = (int)blockIdx.y * per_wg, u1 = min(units, u0 + per_wg);
+    for (int u = u0 + (int)threadIdx.x; u < u1; u += kThreads) {
+        // units of keys come first where both are wanted
+        const bool is_v = k == nullptr || u >= heads_units;
+        const int uu = is_v && k != nullptr ? u - heads_units : u;
+        const int h = uu / per_head, in_head = uu - h * per_head, b = in_head >> 2, n = in_head & 3;
+        const uint8_t* head = page + h * c.head_bytes;
+        uint32_t lo = 0, hi = 0;  // codes of the two runs of 4 values, two a byte
+        int s = kNanByte;
+        if (pg >= 0) {
+            if (is_v) {
+                const uint8_t* o = head + v_code_offset(c.nb, tok, b, 4 * n);
+                const int w = 8 * min(2, c.nb - (b & ~1));  // bytes from c to c + 1
+                lo = o[0] | (uint32_t)o[w] << 8;
+                hi = o[2 * w] | (uint32_t)o[3 * w] << 8;
+                s = head[v_scale_offset(c.nb, tok, b)];
+            } else {
+                const uint32_t w = *reinterpret_cast<const uint32_t*>(head + k_code_offset(c.nb, tok, b, n));
+                const uint32_t even = w & 0x0f0f0f0fu, odd = w >> 4 & 0x0f0f0f0fu;
+                lo = (even | even >> 4) & 0x00ff00ffu;  // nibbles of two bytes side by side
+                hi = (odd | odd >> 4) & 0x00ff00ffu;
+                lo = (lo | lo >> 8) & 0xffffu;
+                hi = (hi | hi >> 8) & 0xffffu;
+                s = head[k_scale_offset(c.nb, tok, b)];
+            }
         }
-        if (s != kNanByte) {
-            const float unit = __uint_as_float((uint32_t)s << 23);
-            const f2 lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, unit, 0);
-            const f2 hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, unit, 1);
-            y = f4u{lo.x, lo.y, hi.x, hi.y};
-        }
+        const float nan = __builtin_nanf(""), unit = __uint_as_float((uint32_t)s << 23);
+        const f2 a0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(lo, unit, 0);
+        const f2 a1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(lo, unit, 1);
+        const f2 b0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(hi, unit, 0);
+        const f2 b1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(hi, unit, 1);
+        const bool bad = s == kNanByte;
+        float* o = (is_v ? v : k) + (t * c.n_kv + h) * D + 32 * b + (is_v ? 8 * n : 4 * n);
+        *reinterpret_cast<f4u*>(o) = bad ? f4u{nan, nan, nan, nan} : f4u{a0.x, a0.y, a1.x, a1.y};
+        *reinterpret_cast<f4u*>(o + (is_v ? 4 : 16)) = bad ? f4u{nan, nan, nan, nan} : f4u{b0.x, b0.y, b1.x, b1.y};
     }
-    *reinterpret_cast<f4u*>(out + u * 4) = y;
 }
 
 // Share of a row's units that one workgroup takes: a pass of its threads for
@@ -318,9 +349,10 @@ hipError_t launch_kv4_append(const KvView& c, const float* Q, const float* K, co
 
 hipError_t launch_kv4_read(const KvView& c, const int32_t* batch_index, const int32_t* pos,
                            int n_rows, float* K, float* V, hipStream_t st) {
-    const int64_t units = (int64_t)n_rows * c.n_kv * c.nb * 8;
-    const dim3 grid((unsigned)((units + kThreads - 1) / kThreads), 2);
-    hipLaunchKernelGGL(kv4_read_kernel, grid, dim3(kThreads), 0, st, c, batch_index, pos, units, K, V);
+    const int units = c.n_kv * c.nb * 4 * (K != nullptr && V != nullptr ? 2 : 1);
+    const int per = units_per_wg(units, n_rows);
+    const dim3 grid((unsigned)n_rows, (unsigned)((units + per - 1) / per));
+    hipLaunchKernelGGL(kv4_read_kernel, grid, dim3(kThreads), 0, st, c, batch_index, pos, units, per, K, V);
     return hipGetLastError();
 }
 

@@ -160,14 +160,12 @@ def test_read_refuses(q8):
     fn = q8.library().q8_kv4_read
     c = _cache(q8)
     bad_caches = [_cache(q8, **b) for b in BAD_CACHES]
-    wide = _cache(q8, n_kv_heads=1024, head_dim=256, n_pages=1)
     A = ctypes.addressof
     ok = [A(c), P, P, 16, P, P, None]
     _refuses(fn, ok, [(0, None), (1, None), (1, P + 2), (2, None), (2, P + 2), (3, 0),
                       (3, (1 << 20) + 1), (4, P + 2), (5, P + 1)])
     _refuses(fn, ok, [(0, A(b)) for b in bad_caches])
     assert fn(A(c), P, P, 16, None, None, None) == 1
-    assert fn(A(wide), P, P, 1 << 20, P, P, None) == 1   # more than 2^32 threads
 
 
 def test_attend_refuses(q8):
