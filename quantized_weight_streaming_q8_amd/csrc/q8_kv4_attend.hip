@@ -194,7 +194,7 @@ __device__ inline void read_keys(const uint8_t* slot, int lane, Keys<NB>& k) {
     for (int q = 0; q < Keys<NB>::kQuads; ++q) {
         // lanes of blocks that are not there take any codes, at scale 1: the
         // queries have zeros for them
-        const int b = 4 * q + (lane >> 4), here = min(b, NB - 1) * 16 + (lane & 15);
+        const int b = 4 * q + (lane >> 4), here = (lane & 15) * NB + min(b, NB - 1);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
             k.c[h][q] = *reinterpret_cast<const u4*>(slot + h * 256 * NB + here * 16);
@@ -727,8 +727,7 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int per_cu, int rec_rows,
             const int tiles = tiles_of(sh.seqs.lo[lane], sh.seqs.hi[lane]);
             int64_t upto = there ? (int64_t)Room{false}.unit(tiles) * units_per_seq : 0;
             int64_t even = there ? (int64_t)Room{true}.unit(tiles) * units_per_seq : 0;
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
+            for (int d = 1; d < min(a.n_seq, 64); d <<= 1) {
                 const int64_t o = __shfl_up(upto, d), e = __shfl_up(even, d);
                 if (lane >= d) {
                     upto += o;
@@ -744,8 +743,8 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int per_cu, int rec_rows,
     for (int s0 = 0; s0 < a.n_seq; s0 += 64) {
         if (s0 > 0) __syncthreads();  // everyone is done with those before
         measure(s0);
-        room_to_end += sh.seqs.upto[63];
-        room_even += sh.seqs.even[63];
+        room_to_end += sh.seqs.upto[min(63, a.n_seq - 1)];
+        room_even += sh.seqs.even[min(63, a.n_seq - 1)];
     }
     const Room lay = {room_even <= (int64_t)kMinSteps * n_shares};
     const int64_t room = lay.even ? room_even : room_to_end;

@@ -7,10 +7,10 @@
 //
 //   K codes, 512 NB bytes, in two tiles of 16 positions.  A tile is the A operand
 //     of v_mfma_scale_f32_16x16x128_f8f6f4 for four blocks at a time: lane (r =
-//     position & 15, g = 0..3) takes block 4q + g of a position, 16 bytes, at
-//     byte b*256 + 16r of the tile.  Byte i holds values i (low nibble) and
-//     16 + i: the order in which two 16-value registers are converted to the
-//     other operand.
+//     position & 15, g = 0..3) takes block b = 4q + g of a position, 16 bytes, at
+//     byte (r*NB + b)*16 of the tile: a position's codes lie side by side.  Byte
+//     i holds values i (low nibble) and 16 + i: the order in which two 16-value
+//     registers are converted to the other operand.
 //   V codes, 512 NB bytes: the A operand (V transposed) of NB pairs of the
 //     same instruction, with the 32 positions along k: lane (c = 0..15, g)
 //     takes values 2c and 2c+1 (the two nibbles of a byte) of each block at 8
@@ -19,7 +19,7 @@
 //     are the B operand as they stand.  Two blocks to a 16-byte read:
 //     byte  p*1024 + (16g + c)*W + 8*(b & 1) + j,  p = b / 2, W = 8 * (blocks
 //     of this pair, 2 but for the last).
-//   K scales, 32 NB bytes: byte (16b + r)*2 + h for tile h = 0, 1 (the two
+//   K scales, 32 NB bytes: byte (r*NB + b)*2 + h for tile h = 0, 1 (the two
 //     tiles' scales of a lane side by side).
 //   V scales, 32 NB bytes: byte g*8NB + 8b + j, j as above.
 #pragma once
@@ -47,8 +47,8 @@ __host__ __device__ constexpr int64_t head_bytes(int nb, int page_tokens) {
 // Offsets in a head's part of a page, t = position of the page.
 // The 4 bytes of K codes with values 4n .. 4n+3 and 16 + 4n .. of block b:
 __host__ __device__ constexpr int64_t k_code_offset(int nb, int t, int b, int n) {
-    return (int64_t)(t >> 5) * group_bytes(nb) + (t >> 4 & 1) * (256 * nb) + b * 256 + (t & 15) * 16 +
-           4 * n;
+    return (int64_t)(t >> 5) * group_bytes(nb) + (t >> 4 & 1) * (256 * nb) +
+           ((t & 15) * nb + b) * 16 + 4 * n;
 }
 // j (byte of a lane's 8) and g (lane quarter) of a position in its group
 __host__ __device__ constexpr int v_byte(int t) { return ((t >> 4 & 1) << 2) | (t & 3); }
@@ -60,7 +60,7 @@ __host__ __device__ constexpr int64_t v_code_offset(int nb, int t, int b, int c)
            (v_quarter(t) * 16 + c) * (8 * in_pair) + 8 * (b & 1) + v_byte(t);
 }
 __host__ __device__ constexpr int64_t k_scale_offset(int nb, int t, int b) {
-    return (int64_t)(t >> 5) * group_bytes(nb) + group_ks(nb) + (16 * b + (t & 15)) * 2 +
+    return (int64_t)(t >> 5) * group_bytes(nb) + group_ks(nb) + ((t & 15) * nb + b) * 2 +
            (t >> 4 & 1);
 }
 __host__ __device__ constexpr int64_t v_scale_offset(int nb, int t, int b) {

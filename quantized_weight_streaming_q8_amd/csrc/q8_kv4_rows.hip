@@ -47,7 +47,8 @@ __device__ inline void turn(const double2 cs, float& a, float& b) {
 template <int V>
 __device__ inline void load_v(const float* p, float (&v)[V]) {
     if constexpr (V == 4) {
-        const f4u t = *reinterpret_cast<const f4u*>(p);
+        // rows are read once (rotary of 4099 rows of 40 heads 39.2 -> 35.2 us with the hint)
+        const f4u t = __builtin_nontemporal_load(reinterpret_cast<const f4u*>(p));
         v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
     } else {
         for (int i = 0; i < V; ++i) v[i] = p[i];

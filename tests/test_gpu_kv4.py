@@ -549,3 +549,16 @@ def test_decode_step_in_a_graph(q8):
         torch.cuda.synchronize()
         assert torch.equal(bufs[0][2], bufs[1][2]), i
         assert torch.isfinite(bufs[0][2]).all()
+
+
+def test_decode_attention_example():
+    """The example runs, appends one position a step and stays finite."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "decode_attention.py")
+    spec = importlib.util.spec_from_file_location("decode_attention", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    out = mod.main(["--live", "3", "--context", "100", "--steps", "5"])
+    assert out["finite"] and out["position"] == 100 + 5 + 1   # one step before the capture
