@@ -683,7 +683,6 @@ struct Shared {
         QueryLds<F> query[RT][Keys<NB>::kQuads];  // a unit's, each made by one wave
     };
     float m[kWaves][kRows], l[kWaves][kRows];  // of the waves
-    float inv[kRows];
     int flag[kRows];
     Sequences seqs;                            // 64 at a time
     uint32_t last;
@@ -902,6 +901,10 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int per_cu, int rec_rows,
             for (int r = 0; r < RT; ++r)
 #pragma unroll
                 for (int k = 0; k < kQuads; ++k) read_query<F>(sh.query[r][k], lane, rows[r].q[k]);
+        if constexpr (RT == 1) {
+            wait_lds_reads();
+            __syncthreads();  // the join of a wave without steps may write over them
+        }
 #pragma unroll
         for (int d = 1; d < 16; d <<= 1) {
             all_lo = max(all_lo, __shfl_xor(all_lo, d));
@@ -956,6 +959,29 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int per_cu, int rec_rows,
                 sh.l[wave][r * kCols + col] = l;
             }
         }
+        // With one tile the accumulators go to LDS as they are, at once; with
+        // two, whose queries are still read there, after everyone's last step.
+        constexpr bool kAtOnceToLds = RT == 1;
+        const auto put = [&](int r) {
+            float* o = &sh.o[wave][col][8 * g];
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                v4f x = rows[r].o[b][0], y = rows[r].o[b][1];
+                if constexpr (F == kFolded) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        x[i] = add_ror8(x[i]);
+                        y[i] = add_ror8(y[i]);
+                    }
+                }
+                // folded: columns c and c + 8 hold the same; each writes half
+                if (F == kWide || (lane & 8) == 0)
+                    *reinterpret_cast<v4f*>(o + 32 * b) = v4f{x[0], y[0], x[1], y[1]};
+                if (F == kWide || (lane & 8) != 0)
+                    *reinterpret_cast<v4f*>(o + 32 * b + 4) = v4f{x[2], y[2], x[3], y[3]};
+            }
+        };
+        if constexpr (kAtOnceToLds) put(0);
         __syncthreads();
         // a share's records: of the unit it goes on with, of the one it leaves
         const auto record_of = [&](int share_no, bool goes_on) {
@@ -971,61 +997,36 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int per_cu, int rec_rows,
             *reinterpret_cast<f4u*>(a.O + ((int64_t)seq * a.tokens + j) * a.o_stride + (int64_t)qh * D +
                                     d) = f4u{y[0], y[1], y[2], y[3]};
         };
-        float wave_max[RT];
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            const int i = r * kCols + col;
-            float m = sh.m[0][i];
-            for (int w = 1; w < kWaves; ++w) m = fmaxf(m, sh.m[w][i]);
-            wave_max[r] = m;
-        }
-        if (thread < kRows) {
-            const int r = thread;
-            float m = sh.m[0][r], l = 0.0f;
-            for (int w = 1; w < kWaves; ++w) m = fmaxf(m, sh.m[w][r]);
-            for (int w = 0; w < kWaves; ++w) l += sh.l[w][r] * part_weight(sh.m[w][r], m, c);
-            sh.inv[r] = 1.0f / l;
-            if (!whole && r < rec_rows) {
-                publish(rec + 2 * half + r, m);
-                publish(rec + 2 * half + rec_rows + r, l);
-            }
-        }
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
             if (r > 0) __syncthreads();  // the tile before is read
-            const float f = part_weight(rows[r].m, wave_max[r], c);
-            float* o = &sh.o[wave][col][8 * g];
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                v4f x = rows[r].o[b][0] * f, y = rows[r].o[b][1] * f;
-                if constexpr (F == kFolded) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        x[i] = add_ror8(x[i]);
-                        y[i] = add_ror8(y[i]);
-                    }
-                }
-                // folded: columns c and c + 8 hold the same; each writes half
-                if (F == kWide || (lane & 8) == 0)
-                    *reinterpret_cast<v4f*>(o + 32 * b) = v4f{x[0], y[0], x[1], y[1]};
-                if (F == kWide || (lane & 8) != 0)
-                    *reinterpret_cast<v4f*>(o + 32 * b + 4) = v4f{x[2], y[2], x[3], y[3]};
+            if constexpr (!kAtOnceToLds) {
+                put(r);
+                __syncthreads();
             }
-            __syncthreads();
             const int here = min(kCols, n_rows - rb * kRows - r * kCols);  // rows of this tile
             for (int u = thread; u < here * (D / 4); u += kThreads) {
-                const int row = u / (D / 4), d = (u - row * (D / 4)) * 4;
-                v4f x = *reinterpret_cast<const v4f*>(&sh.o[0][row][d]);
+                const int row = u / (D / 4), d = (u - row * (D / 4)) * 4, i = r * kCols + row;
+                float m = sh.m[0][i], l = 0.0f;
 #pragma unroll
-                for (int w = 1; w < kWaves; ++w)
-                    x += *reinterpret_cast<const v4f*>(&sh.o[w][row][d]);
-                const int i = r * kCols + row;
+                for (int w = 1; w < kWaves; ++w) m = fmaxf(m, sh.m[w][i]);
+                v4f x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w) {
+                    const float f = part_weight(sh.m[w][i], m, c);
+                    l += sh.l[w][i] * f;
+                    x += *reinterpret_cast<const v4f*>(&sh.o[w][row][d]) * f;
+                }
                 if (whole) {
-                    store_out(i, d, x * sh.inv[i]);
+                    store_out(i, d, x * (1.0f / l));
                 } else {
                     float* o = rec + 2 * (i * (D / 4) + d / 4);
                     publish2(o, x[0], x[1]);
                     publish2(o + half, x[2], x[3]);
+                    if (d == 0) {
+                        publish(rec + 2 * half + i, m);
+                        publish(rec + 2 * half + rec_rows + i, l);
+                    }
                 }
             }
         }
