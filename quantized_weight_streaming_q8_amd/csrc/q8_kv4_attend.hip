@@ -13,9 +13,21 @@
 // value.  Values become exact bf16 (a code times its scale has two significant
 // bits; one instruction converts a pair); the weights 2^(c (s - m)) are fp32
 // numbers of 24 bits, three bf16 pieces of 8 bits exactly.  All sums are fp32.
-// The matrix cores have the room: at head_dim 128 and up to 8 query rows a
-// wave's 32 positions cost them 352 cycles of a SIMD whose share of HBM brings
-// those 4352 bytes in about 1650.
+//
+// What bounds it.  A wave's step of 32 positions at head_dim 128 takes about 240
+// vector instructions (96 of them make the values' operands, 44 the weights'),
+// with 16 rows or 8, about 1000 cycles of its SIMD; the matrix instructions
+// beside them take 576 with 16 rows and 350 with 8; its 4352 bytes come from HBM
+// in about 1500 cycles of the SIMD's share.  So 8 rows (a decode step of up to 8
+// grouped heads) are bound by HBM and the vector instructions alike, 16 by the
+// vector instructions.  About 16 us of a launch on the whole chip are round
+// trips one after the other: the positions 2, page ids and queries 2.5, the
+// queries' pieces 2 (the first groups come in meanwhile), a cut unit's parts
+// on their way 3, their join 3 to 6.  Measured on one MI355X, head_dim 128, 40 query
+// heads on 8: 16 sessions of 1 to 8192 positions 28.2 us (86 MB, 3.1 TB/s), of
+// about 32768 92 us (502 MB, 5.4 TB/s), with 4 tokens each up to 8192 33.7 us;
+// 64 tokens of one session behind 8192 positions 42.5 us (252 TFLOP/s of
+// 10.7 GFLOP counted once, times six for the scores and three for the outputs).
 //
 // Layout of the work.  S^T = K q^T puts positions in the rows of a 16x16 tile
 // and query rows in its columns: a lane holds one query row's scores at 4
@@ -23,28 +35,38 @@
 // O^T = V^T P^T over 32 positions, when V's 32 positions are ordered alike,
 // which the page layout does.  So the softmax needs no data exchange but the
 // maximum over the 4 lanes of a row, the accumulator's columns are query rows
-// (m, l and the rescaling are one number a lane), and nothing passes through
-// LDS until the end.  Keys, values and scales go from memory to the operand
-// registers in whole 16-byte loads.
+// (m, l and the rescaling are one number a lane), and no score or weight passes
+// through LDS.  Keys, values and scales go from memory to LDS past the registers, in
+// whole 16-byte loads, a group of 32 positions ahead, and from there to the operand
+// registers: a slot in registers instead cost a workgroup a CU (16 sessions
+// up to 8192 tokens 58 us against 49, with what else was there then).
 //
 // Query rows are the tokens x grouped heads of one key/value head, 16 to a
-// column tile, RT tiles to a workgroup.  4 waves of a workgroup take its 32-position
+// workgroup, or 8.  Two tiles of 16 to a workgroup (half the operands of the
+// values a row, but one workgroup with 245 registers less) took 40.1 us for 4 drafted
+// tokens of 16 sessions against 39.2, and 49.2 for 64 tokens against 47.6.  16
+// rows with their queries read from LDS at every step, for a third workgroup
+// a CU, took 44.0 and 51.7.  4 waves of a workgroup take its 32-position
 // steps in turn, each with its own m, l and O, joined in LDS at the end.
 //
 // Shares.  Where a share of kMinSteps steps each takes no more workgroups than
 // are resident at once, a unit (sequence, head, row block) is cut into such
 // shares.  Where it takes more, the steps of all units are laid end to end,
-// each unit with kUnitCost steps' worth of room before its own for what it costs
+// each unit with unit_cost steps' worth of room before its own for what it costs
 // to take up, and cut into as many equal shares as are resident: every
 // workgroup has the same to do however ragged the sequences are, and a unit
-// is cut only where a share ends.  A cut unit's parts go to the workspace, and
+// is cut only where a share ends.  (Shares of a fixed 1024 positions, one workgroup
+// each: 34 us for 16 sessions up to 8192, 134 near 32768, against 31.5 and 104
+// as this came in.)  A cut unit's parts go to the workspace, and
 // the last workgroup to leave one joins them, in their order.  The cut is made on
 // the GPU, from pos: the host need not know the lengths, and a launch captured
 // in a graph serves any.
 //
 // Heads abreast.  A page holds its positions for all key/value heads side by
 // side.  Workgroups that differ only in the head go through the same share of
-// the steps at the same time, so that what is read together lies together.
+// the steps at the same time, so that what is read together lies together (one
+// head after the other: 31.6 us for 16 sessions up to 8192 against 30.2, 51.6 for
+// 64 tokens against 49.2).
 
 #include "q8_kv4_internal.h"
 
@@ -53,12 +75,12 @@
 namespace q8 {
 namespace {
 
-// Waves of a workgroup (2 for the heads whose slots of 4 would pass 64 KB).
-__host__ __device__ constexpr int waves_of(int nb) { return nb <= 4 ? 4 : 2; }
+constexpr int kWaves = 4, kThreads = 64 * kWaves;  // of a workgroup, a wave a SIMD
 // The workspace starts with a counter for each unit, at the same place for
 // every shape: calls of other shapes find them at zero too.
 constexpr size_t kCounterBytes = kMaxRowBlocks * sizeof(uint32_t);
-constexpr int kUnitCost = 12;
+// Least share: two steps a wave.  With 4 or 16 steps, 7 sessions with a window of
+// 1000 take 12.8 or 13.3 us against 12.1, the larger cases the same.
 constexpr int kMinSteps = 8;
 constexpr int kNoVmem = 0x0f70;  // s_waitcnt vmcnt(0), no other count
 
@@ -94,29 +116,26 @@ __device__ inline uint32_t dequant2(uint32_t w, float scale) {
 __device__ inline uint32_t pack_hi(float a, float b) {
     return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
 }
-__device__ inline float trunc_bf16(float a) {
-    return __uint_as_float(__float_as_uint(a) & 0xffff0000u);
+// x less the low (high) bf16 of p, exactly where that is x's upper half; k: the
+// packed bf16 (-1, 0) ((0, -1)).
+__device__ inline float less(uint32_t p, uint32_t k, float x) {
+    typedef __bf16 pair __attribute__((ext_vector_type(2)));
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(pair, p), __builtin_bit_cast(pair, k), x,
+                                           false);
 }
-
-// 8 floats as three operands of 8 bf16, x = p[0] + p[1] + p[2] exactly.
-__device__ inline void split3(const float (&x)[8], u4 (&p)[3]) {
-    float r[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p[0][i] = pack_hi(x[2 * i], x[2 * i + 1]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = x[i] - trunc_bf16(x[i]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p[1][i] = pack_hi(r[2 * i], r[2 * i + 1]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = r[i] - trunc_bf16(r[i]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p[2][i] = pack_hi(r[2 * i], r[2 * i + 1]);
+constexpr uint32_t kLessHigh = 0xbf800000u;
+// (-1, 0) in a register: as a constant it would become the inline -1.0, which
+// the instruction reads as (0, -1).
+__device__ inline uint32_t less_low() {
+    uint32_t k;
+    asm("s_mov_b32 %0, 0xbf80" : "=s"(k));
+    return k;
 }
 
 // ---- memory to LDS.  A wave has kSlots slots of its own in LDS, one group of
 // 32 positions each, filled by loads that go past the registers and are
 // waited for by count (loads complete in order).  No other wave touches them.
-constexpr int kSlots = 2;
+constexpr int kSlots = 2;  // three leave two workgroups a CU instead of three
 
 // A group in LDS: its bytes, the scales' part rounded up to whole loads.
 __host__ __device__ constexpr int scale_loads(int nb) {
@@ -128,7 +147,9 @@ __device__ inline uint32_t lds_address(const void* p) {
     return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
 }
 
-// 64 lanes x 16 (4) bytes from base + voff to the LDS bytes from `lds` on.
+// 64 lanes x 16 (4) bytes from base + voff to the LDS bytes from `lds` on.  Read
+// once, past the caches' retention (16 sessions near 32768 positions, the loads
+// alone: 95 us against 109 without the hint).
 __device__ inline void lds_load16(uint32_t lds, const uint8_t* base, uint32_t voff) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt"
                  ::"s"(lds), "v"(voff), "s"(base) : "memory");
@@ -159,20 +180,13 @@ __device__ inline void load_group(uint32_t lds, const uint8_t* group, int lane) 
                   min(i * 256 + lane * 4, group_bytes(NB) - group_ks(NB) - 4));
 }
 
-// N (1..4) words from LDS.
+// N (2 or 4) words from LDS at once.
 template <int N>
 __device__ inline void read_words(const uint8_t* p, uint32_t* o) {
-    if constexpr (N == 4) {
-        const u4 t = *reinterpret_cast<const u4*>(p);
-        o[0] = t[0]; o[1] = t[1]; o[2] = t[2]; o[3] = t[3];
-    } else if constexpr (N == 2) {
-        typedef uint32_t u2 __attribute__((ext_vector_type(2)));
-        const u2 t = *reinterpret_cast<const u2*>(p);
-        o[0] = t[0]; o[1] = t[1];
-    } else {
+    typedef uint32_t words __attribute__((ext_vector_type(N)));
+    const words t = *reinterpret_cast<const words*>(p);
 #pragma unroll
-        for (int i = 0; i < N; ++i) o[i] = reinterpret_cast<const uint32_t*>(p)[i];
-    }
+    for (int i = 0; i < N; ++i) o[i] = t[i];
 }
 
 // One step's operands of one wave: 32 positions of a head.
@@ -232,41 +246,77 @@ __device__ inline float add_ror8(float v) {
     return v + __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), 0x128, 0xf,
                                                                  0xf, true));
 }
+// Maximum of a lane's 16: over neighbours, pairs, fours (mirrored halves) and
+// eights (mirrored rows).
+__device__ inline int max_of_16(int v) {
+    v = max(v, __builtin_amdgcn_mov_dpp(v, 0xb1, 0xf, 0xf, true));
+    v = max(v, __builtin_amdgcn_mov_dpp(v, 0x4e, 0xf, 0xf, true));
+    v = max(v, __builtin_amdgcn_mov_dpp(v, 0x141, 0xf, 0xf, true));
+    return max(v, __builtin_amdgcn_mov_dpp(v, 0x140, 0xf, 0xf, true));
+}
+
+// Maximum of two numbers that are no signalling NaN, which the compiler's own
+// makes sure of with an instruction an operand.  Not for results of matrix
+// instructions: the compiler does not see that this reads them.
+__device__ inline float max2(float a, float b) {
+    float m;
+    asm("v_max_f32 %0, %1, %2" : "=v"(m) : "v"(a), "v"(b));
+    return m;
+}
 // Maximum over lanes 16 and 32 apart.
 __device__ inline float max_over_quarters(float v) {
     const uint32_t u = __float_as_uint(v);
     const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-    const uint32_t m = __float_as_uint(fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1])));
+    const uint32_t m = __float_as_uint(max2(__uint_as_float(a[0]), __uint_as_float(a[1])));
     const auto b = __builtin_amdgcn_permlane16_swap(m, m, false, false);
-    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+    return max2(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 
 // How a column tile holds its rows.  kWide: 16 rows, an operand for each of the
 // pieces of a number.  kFolded, for at most 8 rows: columns c and c + 8 belong
 // to one row and hold two pieces, so that half the instructions do.  Scores
-// add up over the two columns; outputs do at the end.
+// add up over the two columns; outputs do at the end.  Fewer registers then
+// let a third workgroup onto a CU: 16 sessions of 5 rows near 32768 positions
+// took 104.7 us, and 114.9 wide.
 enum Fold { kWide, kFolded };
 
-// Weights as operands: N = 3 (wide) or 2 (folded: upper and middle piece, then
-// lower piece and nothing) of 8 bf16, exactly.  Folded, every lane is given
-// its row's x, keep = 0xffff0000 in columns 8..15 and 0 in 0..7.
+// Workgroups that a CU holds, by LDS and registers.  (At head_dim 160, 192 and 256
+// workgroups of 2 waves, two or three to a CU, took 43 to 55 us for 16 sessions of 1000
+// to 16000 positions and 5 rows, these 36 to 46; of 20 rows 78 to 94 against 71 to 84.)
+__host__ __device__ constexpr int per_cu(int nb, Fold f) {
+    return nb <= 4 ? (f == kFolded ? 3 : 2) : nb <= 6 && f == kFolded ? 2 : 1;
+}
+
+// The upper halves of 8 floats as an operand, and the floats less those (less
+// nothing where on is 0).
+__device__ inline u4 upper(float (&x)[8], uint32_t on = ~0u) {
+    u4 p;
+    const uint32_t low = less_low();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        p[i] = pack_hi(x[2 * i], x[2 * i + 1]);
+        x[2 * i] = less(p[i], low & on, x[2 * i]);
+        x[2 * i + 1] = less(p[i], kLessHigh & on, x[2 * i + 1]);
+    }
+    return p;
+}
+
+// Weights as operands of 8 bf16, exactly: upper, middle and lower piece.
+// Folded, two operands, of upper and middle piece and of the lower piece and
+// nothing: every lane is given its row's x, high = ~0 in columns 8..15, else 0.
 template <Fold F>
-__device__ inline void split(const float (&x)[8], uint32_t keep, u4 (&p)[F == kWide ? 3 : 2]) {
+__device__ inline void split(float (&x)[8], uint32_t high, u4 (&p)[F == kWide ? 3 : 2]) {
     if constexpr (F == kWide) {
-        split3(x, p);
+        p[0] = upper(x);
+        p[1] = upper(x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[2][i] = pack_hi(x[2 * i], x[2 * i + 1]);
     } else {
-        float y[8];
+        upper(x, high);
+        p[0] = upper(x);
+        // columns 8..15: what is below the middle piece is the lower piece
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = x[i] - __uint_as_float(__float_as_uint(x[i]) & keep);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p[0][i] = pack_hi(y[2 * i], y[2 * i + 1]);
-        // columns 8..15: y is the part below the upper piece, and what is below
-        // its own upper half is the lower piece
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = y[i] - trunc_bf16(y[i]);
-        const uint32_t low = keep | keep >> 16;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p[1][i] = pack_hi(y[2 * i], y[2 * i + 1]) & low;
+        for (int i = 0; i < 4; ++i) p[1][i] = pack_hi(x[2 * i], x[2 * i + 1]) & high;
     }
 }
 
@@ -352,13 +402,9 @@ __device__ inline void read_query(const QueryLds<F>& in, int lane, Query<F>& q) 
 }
 
 // Carried state of one column tile.
-template <int NB, int RT, Fold F>
+template <int NB, Fold F>
 struct Rows {
-    // Two tiles' queries stay in LDS and are read at each step: their registers
-    // let two workgroups share a CU instead of one.
-    static constexpr bool kInLds = RT > 1;
-    static constexpr int kQuads = (NB + 3) / 4;
-    Query<F> q[kInLds ? 1 : kQuads];
+    Query<F> q[(NB + 3) / 4];
     v4f o[NB][2];        // O^T: dim 32b + 2(4g + i) + e in o[b][e][i]
     float m, l;          // running maximum (of the scores) and this lane's share of the sum
     int lo, hi;          // positions this column sees
@@ -372,61 +418,42 @@ __device__ inline v4f mfma_scaled(u4 k, uint32_t ks, v6u q, uint32_t qs, v4f c) 
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 2, H, (int)ks, I, (int)qs);
 }
 
-template <int NB, int RT, Fold F, int I>
-__device__ inline void score_piece(const Keys<NB>& k, const Rows<NB, RT, F> (&rows)[RT],
-                                   const QueryLds<F> (&query)[RT][Keys<NB>::kQuads], int lane, int q,
-                                   v4f (&S)[RT][2]) {
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-        v6u y;
-        uint32_t ys;
-        if constexpr (Rows<NB, RT, F>::kInLds) {
-#pragma unroll
-            for (int v = 0; v < 3; ++v) {
-                const uint2 w = query[r][q].p[3 * I + v][lane];
-                y[2 * v] = w.x;
-                y[2 * v + 1] = w.y;
-            }
-            ys = query[r][q].s[I >> 2][lane];
-        } else {
-            y = rows[r].q[q].p[I];
-            ys = rows[r].q[q].s[I >> 2];
-        }
-        S[r][0] = mfma_scaled<0, (I & 3)>(k.c[0][q], k.s[q], y, ys, S[r][0]);
-        S[r][1] = mfma_scaled<1, (I & 3)>(k.c[1][q], k.s[q], y, ys, S[r][1]);
-    }
+template <int NB, Fold F, int I>
+__device__ inline void score_piece(const Keys<NB>& k, const Rows<NB, F>& rows, int q, v4f (&S)[2]) {
+    const v6u y = rows.q[q].p[I];
+    const uint32_t ys = rows.q[q].s[I >> 2];
+    S[0] = mfma_scaled<0, (I & 3)>(k.c[0][q], k.s[q], y, ys, S[0]);
+    S[1] = mfma_scaled<1, (I & 3)>(k.c[1][q], k.s[q], y, ys, S[1]);
 }
 
-template <int NB, int RT, Fold F>
-__device__ inline void scores(const Keys<NB>& k, const Rows<NB, RT, F> (&rows)[RT],
-                              const QueryLds<F> (&query)[RT][Keys<NB>::kQuads], int lane,
-                              v4f (&S)[RT][2]) {
-    const v4f zero = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int r = 0; r < RT; ++r) S[r][0] = S[r][1] = zero;
+template <int NB, Fold F>
+__device__ inline void scores(const Keys<NB>& k, const Rows<NB, F>& rows, v4f (&S)[2]) {
+    S[0] = S[1] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int q = 0; q < Keys<NB>::kQuads; ++q) {  // small pieces first
         if constexpr (F == kWide) {
-            score_piece<NB, RT, F, 5>(k, rows, query, lane, q, S);
-            score_piece<NB, RT, F, 4>(k, rows, query, lane, q, S);
-            score_piece<NB, RT, F, 3>(k, rows, query, lane, q, S);
+            score_piece<NB, F, 5>(k, rows, q, S);
+            score_piece<NB, F, 4>(k, rows, q, S);
+            score_piece<NB, F, 3>(k, rows, q, S);
         }
-        score_piece<NB, RT, F, 2>(k, rows, query, lane, q, S);
-        score_piece<NB, RT, F, 1>(k, rows, query, lane, q, S);
-        score_piece<NB, RT, F, 0>(k, rows, query, lane, q, S);
+        score_piece<NB, F, 2>(k, rows, q, S);
+        score_piece<NB, F, 1>(k, rows, q, S);
+        score_piece<NB, F, 0>(k, rows, q, S);
     }
     if constexpr (F == kFolded) {
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) S[r][i >> 2][i & 3] = add_ror8(S[r][i >> 2][i & 3]);
+        for (int i = 0; i < 8; ++i) {
+            S[i >> 2][i & 3] = add_ror8(S[i >> 2][i & 3]);
+            // here, as one instruction: moved behind a branch they would be two
+            asm volatile("" : "+v"(S[i >> 2][i & 3]));
+        }
     }
 }
 
 // A step that some row does not see whole, or whose page is not there (bad).
-template <int NB, int RT, Fold F>
-__device__ inline void mask_step(Values<NB>& v, Rows<NB, RT, F> (&rows)[RT], v4f (&S)[RT][2], int tok, int g,
-                                 bool bad, int lo, int hi) {
+template <int NB, Fold F>
+__device__ inline void mask_step(Values<NB>& v, Rows<NB, F>& rows, v4f (&S)[2], int tok, int g, bool bad,
+                                 int lo, int hi) {
     // Positions outside [lo, hi), which no row sees, may hold anything:
     // their values and scales become zeros, so that 0 * NaN cannot arise.
     const uint32_t m0 = bad ? 0u : byte_mask(tok + 4 * g, lo, hi);
@@ -440,15 +467,13 @@ __device__ inline void mask_step(Values<NB>& v, Rows<NB, RT, F> (&rows)[RT], v4f
         nan_here |= any_ff(v.s[b]);
     }
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = tok + 16 * h + 4 * g + i;
-                const bool seen = t >= rows[r].lo && t < rows[r].hi;
-                S[r][h][i] = seen ? (bad ? __builtin_nanf("") : S[r][h][i]) : -__builtin_inff();
-            }
+        for (int i = 0; i < 4; ++i) {
+            const int t = tok + 16 * h + 4 * g + i;
+            const bool seen = t >= rows.lo && t < rows.hi;
+            S[h][i] = seen ? (bad ? __builtin_nanf("") : S[h][i]) : -__builtin_inff();
+        }
     // A NaN value block at a position that some rows see and others do not:
     // 0 * NaN would reach the others.  The block becomes zeros, and the rows
     // that see it get their NaN here.
@@ -461,60 +486,55 @@ __device__ inline void mask_step(Values<NB>& v, Rows<NB, RT, F> (&rows)[RT], v4f
             const uint32_t w = __builtin_amdgcn_readlane(v.s[b], 16 * (n >> 2));
             if ((w >> (8 * (n & 3)) & 0xffu) != 0xffu) continue;
             const int t = tok + 16 * (b & 1) + n;
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                const float add = t >= rows[r].lo && t < rows[r].hi ? __builtin_nanf("") : 0.0f;
-                rows[r].o[b >> 1][0] += add;
-                rows[r].o[b >> 1][1] += add;
-            }
+            const float add = t >= rows.lo && t < rows.hi ? __builtin_nanf("") : 0.0f;
+            rows.o[b >> 1][0] += add;
+            rows.o[b >> 1][1] += add;
         }
         v.s[b] &= ~((any_ff(v.s[b]) >> 7) * 0xffu);
     }
 }
 
-template <int NB, int RT, Fold F>
-__device__ inline void softmax_and_values(const Values<NB>& v, Rows<NB, RT, F> (&rows)[RT], v4f (&S)[RT][2],
-                                          float c, float lag, uint32_t keep) {
+template <int NB, Fold F>
+__device__ inline void softmax_and_values(const Values<NB>& v, Rows<NB, F>& rows, v4f (&S)[2], float c,
+                                          float lag, uint32_t high) {
     constexpr int P = F == kWide ? 3 : 2;
-    u4 p[RT][P];
+    u4 p[P];
+    const float inf = __builtin_inff();  // the median of two and infinity: their maximum
+    float t = max2(max2(__builtin_amdgcn_fmed3f(S[0][0], S[0][1], inf),
+                        __builtin_amdgcn_fmed3f(S[0][2], S[0][3], inf)),
+                   max2(__builtin_amdgcn_fmed3f(S[1][0], S[1][1], inf),
+                        __builtin_amdgcn_fmed3f(S[1][2], S[1][3], inf)));
+    t = max_over_quarters(t);
+    // The maximum is raised only when it grew by more than 2^8: weights
+    // up to 256 lose nothing in floating point, and most steps skip the rescaling.
+    const bool grow = t > rows.m + lag;
+    if (__any(grow)) {
+        // scores beyond fp32's range without the shift are infinities
+        const float huge = __uint_as_float((uint32_t)(127 + 128 - kScoreShift) << 23);
+        if (__any(fabsf(t) >= huge)) {
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-        const v4f x0 = S[r][0], x1 = S[r][1];
-        float t = fmaxf(fmaxf(fmaxf(x0[0], x0[1]), fmaxf(x0[2], x0[3])),
-                        fmaxf(fmaxf(x1[0], x1[1]), fmaxf(x1[2], x1[3])));
-        t = max_over_quarters(t);
-        // The maximum is raised only when it grew by more than 2^8: weights
-        // up to 256 lose nothing in floating point, and most steps skip the rescaling.
-        bool grow = t > rows[r].m + lag;
-        if (__any(grow)) {
-            // scores beyond fp32's range without the shift are infinities
-            const float huge = __uint_as_float((uint32_t)(127 + 128 - kScoreShift) << 23);
-            if (__any(fabsf(t) >= huge)) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float y = S[r][i >> 2][i & 3];
-                    S[r][i >> 2][i & 3] = y >= huge ? __builtin_inff() : y <= -huge ? -__builtin_inff() : y;
-                }
-                t = t >= huge ? __builtin_inff() : t <= -huge ? -__builtin_inff() : t;
+            for (int i = 0; i < 8; ++i) {
+                const float y = S[i >> 2][i & 3];
+                S[i >> 2][i & 3] = y >= huge ? __builtin_inff() : y <= -huge ? -__builtin_inff() : y;
             }
-            const float m = grow ? t : rows[r].m;
-            const float f = grow ? __builtin_amdgcn_exp2f((rows[r].m - m) * c) : 1.0f;
-            rows[r].m = m;
-            rows[r].l *= f;
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                rows[r].o[b][0] *= f;
-                rows[r].o[b][1] *= f;
-            }
+            t = t >= huge ? __builtin_inff() : t <= -huge ? -__builtin_inff() : t;
         }
-        const float m = rows[r].m == -__builtin_inff() ? 0.0f : rows[r].m;
-        float e[8];
+        const float m = grow ? t : rows.m;
+        const float f = grow ? __builtin_amdgcn_exp2f((rows.m - m) * c) : 1.0f;
+        rows.m = m;
+        rows.l *= f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            e[i] = __builtin_amdgcn_exp2f((S[r][i >> 2][i & 3] - m) * c);
-        rows[r].l += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-        split<F>(e, keep, p[r]);
+        for (int b = 0; b < NB; ++b) {
+            rows.o[b][0] *= f;
+            rows.o[b][1] *= f;
+        }
     }
+    const float m = rows.m == -__builtin_inff() ? 0.0f : rows.m;
+    float e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = __builtin_amdgcn_exp2f((S[i >> 2][i & 3] - m) * c);
+    rows.l += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+    split<F>(e, high, p);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
         const uint32_t w0 = v.c[2 * b], w1 = v.c[2 * b + 1], s0 = v.s[2 * b], s1 = v.s[2 * b + 1];
@@ -529,12 +549,10 @@ __device__ inline void softmax_and_values(const Values<NB>& v, Rows<NB, RT, F> (
             odd[i] = __builtin_amdgcn_perm(d[2 * i + 1], d[2 * i], 0x07060302u);
         }
 #pragma unroll
-        for (int k = P - 1; k >= 0; --k)
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                rows[r].o[b][0] = mfma(even, p[r][k], rows[r].o[b][0]);
-                rows[r].o[b][1] = mfma(odd, p[r][k], rows[r].o[b][1]);
-            }
+        for (int k = P - 1; k >= 0; --k) {
+            rows.o[b][0] = mfma(even, p[k], rows.o[b][0]);
+            rows.o[b][1] = mfma(odd, p[k], rows.o[b][1]);
+        }
     }
 }
 
@@ -612,15 +630,23 @@ __device__ inline uint64_t fetch2(const float* p) {
                              __HIP_MEMORY_SCOPE_AGENT);
 }
 
+// What taking up a unit costs in steps: its queries, and the join of what other
+// workgroups have of it.  Measured with 4 / 8 / 12 / 16 / 20: 16 sessions up to
+// 8192 tokens, folded, 33 / 31.8 / 30.0 / 30.7 / 31.0 us; 64 tokens of a prompt
+// behind 8192, wide, - / 47.3 / 46.1 / 45.1 / 44.2, 4 drafted tokens of 16
+// sessions, wide, - / 40.5 / 35.9 / 35.9 / 36.3.
+constexpr int unit_cost(Fold f) { return f == kFolded ? 12 : 16; }
+
 // How units are laid out: each starts on a share (even), or end to end.
+template <Fold F>
 struct Room {
     bool even;
     // Before a unit's steps, and of a unit in all (at least one step: someone
     // has to write its rows).
-    __device__ int cost() const { return even ? 0 : kUnitCost; }
+    __device__ int cost() const { return even ? 0 : unit_cost(F); }
     __device__ int unit(int tiles) const {
         const int t = max(tiles, 1);
-        return even ? (t + kMinSteps - 1) / kMinSteps * kMinSteps : kUnitCost + t;
+        return even ? (t + kMinSteps - 1) / kMinSteps * kMinSteps : unit_cost(F) + t;
     }
 };
 
@@ -629,7 +655,8 @@ struct Room {
 // get ahead of the others in its issue slots, and the last ones would run on
 // alone: shares are weighted by rank, 23 : 20 : 17 for three (16 sessions up to
 // 8192 tokens 31.5 -> 28.6 us, near 32768 tokens 103.8 -> 99.0, against equal
-// shares; at 26 : 20 : 14, 29.0 and 100.8) and 5 : 4 for two (drafts 39.1 -> 38.4).
+// shares; at 26 : 20 : 14, 29.0 and 100.8) and 5 : 4 for two (4 drafted tokens of
+// 16 sessions 35.9 us; equal shares 38.2, 4 : 3 39.5).
 struct Shares {
     int64_t room;
     double unit;   // room of a share of weight 1
@@ -637,11 +664,11 @@ struct Shares {
     int w[3];      // weight of a share by its rank
     bool even;
 
-    __device__ Shares(int64_t room_, int n_, bool even_, int per_cu)
-        : room(room_), n(n_), rank(n_ / per_cu), even(even_) {
-        w[0] = per_cu == 3 ? 23 : per_cu == 2 ? 5 : 1;
-        w[1] = per_cu == 3 ? 20 : per_cu == 2 ? 4 : 1;
-        w[2] = per_cu == 3 ? 17 : w[1];
+    __device__ Shares(int64_t room_, int n_, bool even_, int on_cu)
+        : room(room_), n(n_), rank(n_ / on_cu), even(even_) {
+        w[0] = on_cu == 3 ? 23 : on_cu == 2 ? 5 : 1;
+        w[1] = on_cu == 3 ? 20 : on_cu == 2 ? 4 : 1;
+        w[2] = on_cu == 3 ? 17 : w[1];
         unit = (double)room / weight(n);
     }
     __device__ int weight(int i) const {  // of the first i shares
@@ -671,30 +698,29 @@ struct Sequences {
 
 // LDS of a workgroup: the waves' slots, what the join of the waves needs
 // (apart from them: the next steps are on their way meanwhile), the counts.
-template <int NB, int RT, Fold F>
+template <int NB, Fold F>
 struct Shared {
-    static constexpr int kWaves = waves_of(NB);
-    static constexpr int kCols = F == kFolded ? 8 : 16;  // rows of a column tile
-    static constexpr int kRows = kCols * RT;
-    static constexpr int kPitch = NB * 32 + 4;           // floats of a row's accumulator
+    static constexpr int kRows = F == kFolded ? 8 : 16;
     uint8_t slots[kWaves][kSlots][slot_bytes(NB)];
     union {
-        float o[kWaves][kCols][kPitch];
-        QueryLds<F> query[RT][Keys<NB>::kQuads];  // a unit's, each made by one wave
+        // accumulators: the float4 i of row r is at i ^ (r & 7), so that a
+        // wave's writes, a row in each 4 lanes, spread over the banks
+        float o[kWaves][kRows][NB * 32];
+        QueryLds<F> query[Keys<NB>::kQuads];  // a unit's, each made by one wave
     };
     float m[kWaves][kRows], l[kWaves][kRows];  // of the waves
-    int flag[kRows];
-    Sequences seqs;                            // 64 at a time
+    uint8_t flag[kRows];
+    Sequences seqs;  // 64 at a time
     uint32_t last;
 };
 
-template <int NB, int RT, Fold F>
-__global__ void __launch_bounds__(64 * waves_of(NB), NB <= 4 ? (F == kFolded ? 3 : 2) : 1)
-kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int per_cu, int rec_rows, float* records) {
-    using Sh = Shared<NB, RT, F>;
+template <int NB, Fold F>
+__global__ void __launch_bounds__(kThreads, per_cu(NB, F))
+kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int rec_rows, float* records) {
+    using Sh = Shared<NB, F>;
     constexpr int D = NB * 32;
-    constexpr int kWaves = Sh::kWaves, kThreads = 64 * kWaves;
-    constexpr int kCols = Sh::kCols, kRows = Sh::kRows, kQuads = Keys<NB>::kQuads;
+    constexpr int kRows = Sh::kRows, kQuads = Keys<NB>::kQuads;
+    static_assert(per_cu(NB, F) * sizeof(Sh) <= 160 * 1024, "LDS of a CU");
     __shared__ __align__(16) Sh sh;
 
     int lane = threadIdx.x & 63;
@@ -724,8 +750,8 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int per_cu, int rec_rows,
         if (wave == 0) {
             const bool there = s0 + lane < a.n_seq;
             const int tiles = tiles_of(sh.seqs.lo[lane], sh.seqs.hi[lane]);
-            int64_t upto = there ? (int64_t)Room{false}.unit(tiles) * units_per_seq : 0;
-            int64_t even = there ? (int64_t)Room{true}.unit(tiles) * units_per_seq : 0;
+            int64_t upto = there ? (int64_t)Room<F>{false}.unit(tiles) * units_per_seq : 0;
+            int64_t even = there ? (int64_t)Room<F>{true}.unit(tiles) * units_per_seq : 0;
             for (int d = 1; d < min(a.n_seq, 64); d <<= 1) {
                 const int64_t o = __shfl_up(upto, d), e = __shfl_up(even, d);
                 if (lane >= d) {
@@ -745,9 +771,9 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int per_cu, int rec_rows,
         room_to_end += sh.seqs.upto[min(63, a.n_seq - 1)];
         room_even += sh.seqs.even[min(63, a.n_seq - 1)];
     }
-    const Room lay = {room_even <= (int64_t)kMinSteps * n_shares};
+    const Room<F> lay = {room_even <= (int64_t)kMinSteps * n_shares};
     const int64_t room = lay.even ? room_even : room_to_end;
-    const Shares shares(room, n_shares, lay.even, per_cu);
+    const Shares shares(room, n_shares, lay.even, per_cu(NB, F));
     const auto upto_of = [&](int i) { return lay.even ? (int64_t)sh.seqs.even[i] : sh.seqs.upto[i]; };
     if (a.n_seq > 64) {
         __syncthreads();
@@ -766,7 +792,7 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int per_cu, int rec_rows,
         asm volatile("" : "+v"(lane));
         const int col = F == kFolded ? lane & 7 : lane & 15, g = lane >> 4;
         const bool owner = F == kFolded ? (lane & 15) < 8 && g == 0 : g == 0;  // one lane of a row
-        const uint32_t keep = lane & 8 ? 0xffff0000u : 0u;
+        const uint32_t high = lane & 8 ? ~0u : 0u;
 
         // ---- the unit (sequence, head, row block) at `at`, and its steps here
         uint64_t past;
@@ -809,27 +835,22 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int per_cu, int rec_rows,
         };
         int ids = 0;
         if (slot >= 0) ids = load_ids(page0);
-        Rows<NB, RT, F> rows[RT];
-        int row_pos[RT], row_slot[RT];
-        // Operand (r, k) of the queries is made by one wave, not the same one
-        // for the workgroups that share a CU.
-        constexpr int kMine = (RT * kQuads + kWaves - 1) / kWaves;
+        Rows<NB, F> rows;
+        const int row = min(rb * kRows + col, n_rows - 1);  // past the last: that again
+        const int token = row / a.group;
+        const int64_t t_row = (int64_t)seq * a.tokens + token;
+        const int row_pos = a.pos[t_row], row_slot = a.batch_index[t_row];
+        // Operand k of the queries is made by one wave, not the same one for the
+        // workgroups that share a CU.
+        constexpr int kMine = (kQuads + kWaves - 1) / kWaves;
         const int turn = (wave + kWaves - blockIdx.x / 256 % kWaves) % kWaves;
         v16f q_in[kMine][2];
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            const int row = min(rb * kRows + r * kCols + col, n_rows - 1);  // past the last: that again
-            const int64_t t = (int64_t)seq * a.tokens + row / a.group;
-            row_pos[r] = a.pos[t];
-            row_slot[r] = a.batch_index[t];
-        }
-#pragma unroll
         for (int i = 0; i < kMine; ++i) {
-            const int n = turn + i * kWaves, r = n / kQuads, k = n - r * kQuads;
-            if (n >= RT * kQuads) break;
-            const int row = min(rb * kRows + r * kCols + col, n_rows - 1);
-            const int j = row / a.group, qh = head * a.group + row - j * a.group;
-            const float* q = a.Q + ((int64_t)seq * a.tokens + j) * a.q_stride + (int64_t)qh * D +
+            const int k = turn + i * kWaves;
+            if (k >= kQuads) break;
+            const float* q = a.Q + t_row * a.q_stride +
+                             (int64_t)(head * a.group + row - token * a.group) * D +
                              32 * min(4 * k + g, NB - 1);  // block 4k + g
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -848,6 +869,9 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int per_cu, int rec_rows,
             if (page - page0 >= 64) {
                 page0 = page;
                 ids = load_ids(page0);
+                // here, or the compiler waits at every use, also for the groups
+                // that are on their way
+                __builtin_amdgcn_s_waitcnt(kNoVmem);
             }
             const int id = __builtin_amdgcn_readlane(ids, page - page0);
             const bool none = id < 0 || id >= a.c.n_pages;
@@ -866,26 +890,21 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int per_cu, int rec_rows,
 #pragma unroll
         for (int i = 0; i < kSlots; ++i) load_next(i);
 
-        int all_lo = 0, all_hi = INT32_MAX;  // seen by every row of the workgroup
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            const int flag = row_flag(row_pos[r], row_slot[r], slot, a.c.n_slots, cap);
-            // rows that are not computed see what their neighbours see, of a
-            // query of zeros
-            rows[r].lo = flag == 0 && a.window > 0 ? max(0, row_pos[r] + 1 - a.window) : 0;
-            rows[r].hi = flag == 0 ? row_pos[r] + 1 : INT32_MAX;
-            all_lo = max(all_lo, rows[r].lo);
-            all_hi = min(all_hi, rows[r].hi);
-            if (wave == 0 && owner) sh.flag[r * kCols + col] = flag;
-        }
+        // rows that are not computed see what their neighbours see, of a query
+        // of zeros
+        const int flag = row_flag(row_pos, row_slot, slot, a.c.n_slots, cap);
+        rows.lo = flag == 0 && a.window > 0 ? max(0, row_pos + 1 - a.window) : 0;
+        rows.hi = flag == 0 ? row_pos + 1 : INT32_MAX;
+        if (wave == 0 && owner) sh.flag[col] = (uint8_t)flag;
+        // seen by every row of the workgroup
+        const int all_lo = max(__builtin_amdgcn_readfirstlane(max_of_16(rows.lo)), ex.lo);
+        const int all_hi = min(__builtin_amdgcn_readfirstlane(-max_of_16(-rows.hi)), ex.hi);
+        // steps that every row sees whole: [whole_lo, whole_hi)
+        const int whole_lo = (all_lo + kKvTile - 1) / kKvTile, whole_hi = all_hi / kKvTile;
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
-            const int n = turn + i * kWaves, r = n / kQuads, k = n - r * kQuads;
-            if (n >= RT * kQuads) break;
-            int flag = row_flag(row_pos[0], row_slot[0], slot, a.c.n_slots, cap);
-#pragma unroll
-            for (int o = 1; o < RT; ++o)
-                if (r == o) flag = row_flag(row_pos[o], row_slot[o], slot, a.c.n_slots, cap);
+            const int k = turn + i * kWaves;
+            if (k >= kQuads) break;
             const bool there = flag == 0 && 4 * k + g < NB;
             v16f &x = q_in[i][0], &y = q_in[i][1];
 #pragma unroll
@@ -893,36 +912,18 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int per_cu, int rec_rows,
                 x[v] = there ? x[v] : 0.0f;
                 y[v] = there ? y[v] : 0.0f;
             }
-            make_query<F>(x, y, lane, sh.query[r][k]);
+            make_query<F>(x, y, lane, sh.query[k]);
         }
         __syncthreads();
-        if constexpr (!Rows<NB, RT, F>::kInLds)
 #pragma unroll
-            for (int r = 0; r < RT; ++r)
-#pragma unroll
-                for (int k = 0; k < kQuads; ++k) read_query<F>(sh.query[r][k], lane, rows[r].q[k]);
-        if constexpr (RT == 1) {
-            wait_lds_reads();
-            __syncthreads();  // the join of a wave without steps may write over them
-        }
-#pragma unroll
-        for (int d = 1; d < 16; d <<= 1) {
-            all_lo = max(all_lo, __shfl_xor(all_lo, d));
-            all_hi = min(all_hi, __shfl_xor(all_hi, d));
-        }
-        // steps that every row sees whole: [whole_lo, whole_hi)
-        all_lo = max(__builtin_amdgcn_readfirstlane(all_lo), ex.lo);
-        all_hi = min(__builtin_amdgcn_readfirstlane(all_hi), ex.hi);
-        const int whole_lo = (all_lo + kKvTile - 1) / kKvTile, whole_hi = all_hi / kKvTile;
-
+        for (int k = 0; k < kQuads; ++k) read_query<F>(sh.query[k], lane, rows.q[k]);
+        wait_lds_reads();
+        __syncthreads();  // the join of a wave without steps may write over them
         int now = 0;  // slot of the next step
+        rows.m = -__builtin_inff();
+        rows.l = 0.0f;
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            rows[r].m = -__builtin_inff();
-            rows[r].l = 0.0f;
-#pragma unroll
-            for (int b = 0; b < NB; ++b) rows[r].o[b][0] = rows[r].o[b][1] = v4f{0.f, 0.f, 0.f, 0.f};
-        }
+        for (int b = 0; b < NB; ++b) rows.o[b][0] = rows.o[b][1] = v4f{0.f, 0.f, 0.f, 0.f};
         for (int t = first; t < t1; t += kWaves) {
             // A step.  Its slot is free for the step after next as soon as
             // the values are in registers.
@@ -933,55 +934,47 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int per_cu, int rec_rows,
             --in_flight;
             Keys<NB> keys;
             Values<NB> vals;
-            v4f S[RT][2];
+            v4f S[2];
             read_keys<NB>(in, lane, keys);
-            scores<NB, RT, F>(keys, rows, sh.query, lane, S);
+            scores<NB, F>(keys, rows, S);
             read_values<NB>(in, lane, vals);
             wait_lds_reads();
             const bool none = bad >> now & 1;
             load_next(now);
             now ^= 1;
             if (none || t < whole_lo || t >= whole_hi)
-                mask_step<NB, RT, F>(vals, rows, S, t * kKvTile, g, none, ex.lo, ex.hi);
-            softmax_and_values<NB, RT, F>(vals, rows, S, c, lag, keep);
+                mask_step<NB, F>(vals, rows, S, t * kKvTile, g, none, ex.lo, ex.hi);
+            softmax_and_values<NB, F>(vals, rows, S, c, lag, high);
         }
 
         // ---- join the waves
         asm volatile("" : "+v"(lane));  // as above
         const int thread = wave * 64 + lane;
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            float l = rows[r].l;
-            l += __shfl_xor(l, 16);
-            l += __shfl_xor(l, 32);
-            if (owner) {
-                sh.m[wave][r * kCols + col] = rows[r].m;
-                sh.l[wave][r * kCols + col] = l;
-            }
+        float l_row = rows.l;
+        l_row += __shfl_xor(l_row, 16);
+        l_row += __shfl_xor(l_row, 32);
+        if (owner) {
+            sh.m[wave][col] = rows.m;
+            sh.l[wave][col] = l_row;
         }
-        // With one tile the accumulators go to LDS as they are, at once; with
-        // two, whose queries are still read there, after everyone's last step.
-        constexpr bool kAtOnceToLds = RT == 1;
-        const auto put = [&](int r) {
-            float* o = &sh.o[wave][col][8 * g];
+        float* const o_row = sh.o[wave][col];
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                v4f x = rows[r].o[b][0], y = rows[r].o[b][1];
-                if constexpr (F == kFolded) {
+        for (int b = 0; b < NB; ++b) {
+            v4f x = rows.o[b][0], y = rows.o[b][1];
+            if constexpr (F == kFolded) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        x[i] = add_ror8(x[i]);
-                        y[i] = add_ror8(y[i]);
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    x[i] = add_ror8(x[i]);
+                    y[i] = add_ror8(y[i]);
                 }
-                // folded: columns c and c + 8 hold the same; each writes half
-                if (F == kWide || (lane & 8) == 0)
-                    *reinterpret_cast<v4f*>(o + 32 * b) = v4f{x[0], y[0], x[1], y[1]};
-                if (F == kWide || (lane & 8) != 0)
-                    *reinterpret_cast<v4f*>(o + 32 * b + 4) = v4f{x[2], y[2], x[3], y[3]};
             }
-        };
-        if constexpr (kAtOnceToLds) put(0);
+            // folded: columns c and c + 8 hold the same; each writes half
+            const int i4 = 8 * b + ((2 * g) ^ (col & 7));
+            if (F == kWide || (lane & 8) == 0)
+                *reinterpret_cast<v4f*>(o_row + 4 * i4) = v4f{x[0], y[0], x[1], y[1]};
+            if (F == kWide || (lane & 8) != 0)
+                *reinterpret_cast<v4f*>(o_row + 4 * (i4 ^ 1)) = v4f{x[2], y[2], x[3], y[3]};
+        }
         __syncthreads();
         // a share's records: of the unit it goes on with, of the one it leaves
         const auto record_of = [&](int share_no, bool goes_on) {
@@ -997,36 +990,27 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int per_cu, int rec_rows,
             *reinterpret_cast<f4u*>(a.O + ((int64_t)seq * a.tokens + j) * a.o_stride + (int64_t)qh * D +
                                     d) = f4u{y[0], y[1], y[2], y[3]};
         };
+        const int live = min(kRows, n_rows - rb * kRows);
+        for (int u = thread; u < live * (D / 4); u += kThreads) {
+            const int row = u / (D / 4), d = (u - row * (D / 4)) * 4;
+            float m = sh.m[0][row], l = 0.0f;
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            if (r > 0) __syncthreads();  // the tile before is read
-            if constexpr (!kAtOnceToLds) {
-                put(r);
-                __syncthreads();
+            for (int w = 1; w < kWaves; ++w) m = fmaxf(m, sh.m[w][row]);
+            v4f x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                const float f = part_weight(sh.m[w][row], m, c);
+                l += sh.l[w][row] * f;
+                x += *reinterpret_cast<const v4f*>(&sh.o[w][row][d ^ 4 * (row & 7)]) * f;
             }
-            const int here = min(kCols, n_rows - rb * kRows - r * kCols);  // rows of this tile
-            for (int u = thread; u < here * (D / 4); u += kThreads) {
-                const int row = u / (D / 4), d = (u - row * (D / 4)) * 4, i = r * kCols + row;
-                float m = sh.m[0][i], l = 0.0f;
-#pragma unroll
-                for (int w = 1; w < kWaves; ++w) m = fmaxf(m, sh.m[w][i]);
-                v4f x = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int w = 0; w < kWaves; ++w) {
-                    const float f = part_weight(sh.m[w][i], m, c);
-                    l += sh.l[w][i] * f;
-                    x += *reinterpret_cast<const v4f*>(&sh.o[w][row][d]) * f;
-                }
-                if (whole) {
-                    store_out(i, d, x * (1.0f / l));
-                } else {
-                    float* o = rec + 2 * (i * (D / 4) + d / 4);
-                    publish2(o, x[0], x[1]);
-                    publish2(o + half, x[2], x[3]);
-                    if (d == 0) {
-                        publish(rec + 2 * half + i, m);
-                        publish(rec + 2 * half + rec_rows + i, l);
-                    }
+            if (whole) {
+                store_out(row, d, x * (1.0f / l));
+            } else {
+                publish2(rec + 2 * u, x[0], x[1]);
+                publish2(rec + half + 2 * u, x[2], x[3]);
+                if (d == 0) {
+                    publish(rec + 2 * half + row, m);
+                    publish(rec + 2 * half + rec_rows + row, l);
                 }
             }
         }
@@ -1045,13 +1029,11 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int per_cu, int rec_rows,
         __syncthreads();
         if (!sh.last) continue;
         if (thread == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        const int live = min(kRows, n_rows - rb * kRows);
-#pragma unroll RT
         for (int u = thread; u < live * (D / 4); u += kThreads) {
             const int row = u / (D / 4), d = (u - row * (D / 4)) * 4;
             v4f x = {0.f, 0.f, 0.f, 0.f};
             float top = -__builtin_inff(), sum = 0.0f;
-            constexpr int kAtOnce = RT > 1 ? 8 : 4;  // parts whose loads travel together
+            constexpr int kAtOnce = 4;  // parts whose loads travel together; 8 gain nothing
             for (int i0 = 0; i0 < parts; i0 += kAtOnce) {
                 float m[kAtOnce], l[kAtOnce];
                 uint64_t lo[kAtOnce], hi[kAtOnce];
@@ -1086,32 +1068,30 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int per_cu, int rec_rows,
 }
 
 struct Plan {
-    int rt, per_wg, per_cu, n_rb, abreast, rec_rows;
+    int per_wg, n_rb, abreast, rec_rows;
     bool folded;
     unsigned wgs;
     int64_t units;
 };
 
-// Up to 8 rows: folded.  More than 16: two column tiles a workgroup where the
-// registers hold them (head_dim <= 128).
+// Up to 8 rows: folded (both ways measured at the definition).
 Plan plan_attend(const AttendArgs& a) {
     Plan p;
     const int nb = a.c.nb, rows = a.tokens * a.group;
     p.folded = rows <= 8;
-    p.rt = rows > 16 && nb <= 4 ? 2 : 1;
-    p.per_wg = (p.folded ? 8 : 16) * p.rt;
+    p.per_wg = p.folded ? 8 : 16;
     p.n_rb = (rows + p.per_wg - 1) / p.per_wg;
     p.rec_rows = rows < p.per_wg ? rows : p.per_wg;
     p.units = (int64_t)a.n_seq * a.c.n_kv * p.n_rb;
     // Workgroups resident at once: each takes one share, more would only wait.
     // Fewer where full sequences have no more least shares.
-    p.per_cu = nb <= 4 && p.folded ? 3 : 2;
+    const int resident = 256 * per_cu(nb, p.folded ? kFolded : kWide);
     const int64_t tiles = ((int64_t)a.c.max_pages * a.c.page_tokens + kKvTile - 1) / kKvTile;
     p.abreast = 1;
     for (int d = 2; d <= 32 && d <= a.c.n_kv; ++d)
         if (a.c.n_kv % d == 0) p.abreast = d;
     const int64_t most = p.units / p.abreast * ((tiles + kMinSteps - 1) / kMinSteps);
-    const int64_t shares = std::min<int64_t>(256 * p.per_cu / p.abreast, most);
+    const int64_t shares = std::min<int64_t>(resident / p.abreast, most);
     p.wgs = (unsigned)(shares * p.abreast);
     return p;
 }
@@ -1120,19 +1100,16 @@ size_t records_bytes(const Plan& p, int nb) {
     return 2 * (size_t)p.wgs * record_floats(p.rec_rows, nb) * sizeof(float);
 }
 
-template <int NB, int RT, Fold F>
+template <int NB, Fold F>
 hipError_t launch_one(const Plan& p, const AttendArgs& a, float* records, hipStream_t st) {
-    hipLaunchKernelGGL((kv4_attend_kernel<NB, RT, F>), dim3(p.wgs), dim3(64 * waves_of(NB)), 0, st, a,
-                       p.n_rb, p.abreast, p.per_cu, p.rec_rows, records);
+    hipLaunchKernelGGL((kv4_attend_kernel<NB, F>), dim3(p.wgs), dim3(kThreads), 0, st, a,
+                       p.n_rb, p.abreast, p.rec_rows, records);
     return hipGetLastError();
 }
 
 template <int NB>
 hipError_t launch(const Plan& p, const AttendArgs& a, float* records, hipStream_t st) {
-    if constexpr (NB <= 4)
-        if (p.rt == 2) return launch_one<NB, 2, kWide>(p, a, records, st);
-    return p.folded ? launch_one<NB, 1, kFolded>(p, a, records, st)
-                    : launch_one<NB, 1, kWide>(p, a, records, st);
+    return p.folded ? launch_one<NB, kFolded>(p, a, records, st) : launch_one<NB, kWide>(p, a, records, st);
 }
 
 }  // namespace
