@@ -827,8 +827,8 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int rec_rows, float* reco
 
         // ---- the first page ids and the query rows, loaded together
         const int first = t0 + wave;
-        int page = first / groups_per_page, in_page = first - page * groups_per_page;
-        int page0 = page;  // lane i holds the page id of page page0 + i
+        int page0 = first / groups_per_page, in_page = first - page0 * groups_per_page;
+        int page = 0;  // of the next group to load, from page0; lane i holds the id of page0 + i
         const auto load_ids = [&](int p0) {
             const int p = p0 + lane;
             return p < a.c.max_pages ? a.c.table[(int64_t)slot * a.c.max_pages + p] : -1;
@@ -864,20 +864,22 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int rec_rows, float* reco
         int ahead = first;  // next step to load
         int in_flight = 0;
         uint32_t bad = 0;  // bit i: the page of slot i's step is not there
+        const uint8_t* const head_pages = a.c.pages + head * a.c.head_bytes;
+        const uint32_t n_pages = (uint32_t)min(a.c.n_pages, (int64_t)1 << 31);
         const auto load_next = [&](int i) {
             if (ahead >= t1) return;
-            if (page - page0 >= 64) {
-                page0 = page;
+            if (page >= 64) {
+                page0 += page;
+                page = 0;
                 ids = load_ids(page0);
                 // here, or the compiler waits at every use, also for the groups
                 // that are on their way
                 __builtin_amdgcn_s_waitcnt(kNoVmem);
             }
-            const int id = __builtin_amdgcn_readlane(ids, page - page0);
-            const bool none = id < 0 || id >= a.c.n_pages;
+            const uint32_t id = (uint32_t)__builtin_amdgcn_readlane(ids, page);
+            const bool none = id >= n_pages;  // -1 and its like too
             bad = none ? bad | 1u << i : bad & ~(1u << i);
-            const uint8_t* p = a.c.pages + (none ? 0 : id) * a.c.page_bytes + head * a.c.head_bytes +
-                               in_page * group_bytes(NB);
+            const uint8_t* p = head_pages + (none ? 0u : id) * a.c.page_bytes + in_page * group_bytes(NB);
             load_group<NB>(lds_address(sh.slots[wave][i]), p, lane);
             ++in_flight;
             ahead += kWaves;
