@@ -14,20 +14,21 @@
 // bits; one instruction converts a pair); the weights 2^(c (s - m)) are fp32
 // numbers of 24 bits, three bf16 pieces of 8 bits exactly.  All sums are fp32.
 //
-// What bounds it.  A wave's step of 32 positions at head_dim 128 takes about 240
-// vector instructions (96 of them make the values' operands, 44 the weights'),
-// with 16 rows or 8, about 1000 cycles of its SIMD; the matrix instructions
+// What bounds it.  A wave's step of 32 positions at head_dim 128 takes about 250
+// vector instructions (96 of them make the values' operands, 32 or 36 the
+// weights'), with 16 rows or 8, about 1000 cycles of its SIMD; the matrix instructions
 // beside them take 576 with 16 rows and 350 with 8; its 4352 bytes come from HBM
 // in about 1500 cycles of the SIMD's share.  So 8 rows (a decode step of up to 8
-// grouped heads) are bound by HBM and the vector instructions alike, 16 by the
-// vector instructions.  About 16 us of a launch on the whole chip are round
-// trips one after the other: the positions 2, page ids and queries 2.5, the
-// queries' pieces 2 (the first groups come in meanwhile), a cut unit's parts
-// on their way 3, their join 3 to 6.  Measured on one MI355X, head_dim 128, 40 query
-// heads on 8: 16 sessions of 1 to 8192 positions 28.2 us (86 MB, 3.1 TB/s), of
-// about 32768 92 us (502 MB, 5.4 TB/s), with 4 tokens each up to 8192 33.7 us;
-// 64 tokens of one session behind 8192 positions 42.5 us (252 TFLOP/s of
-// 10.7 GFLOP counted once, times six for the scores and three for the outputs).
+// grouped heads) are bound by HBM, with the vector units busy 65% of the time, 16
+// by the vector instructions and what they wait for (52%).  About 16 us of a launch on
+// the whole chip are round trips one after the other: the positions 2 us, page
+// ids and queries 2.5, the queries' pieces 2 (the first groups come in meanwhile), a
+// cut unit's parts on their way 3, their join 3 to 6.  Measured on one MI355X,
+// head_dim 128, 40 query heads on 8: 16 sessions of 1 to 8192 positions 27.9 us
+// (86 MB, 3.1 TB/s), of 24000 to 32768 92 us (502 MB, 5.5 TB/s), with 4 tokens
+// each of 1000 to 6000 positions 32.8 us (57 MB); 64 tokens of one session
+// behind 8192 positions 42.4 us (10.7 GFLOP, 252 TFLOP/s; with six pieces for the
+// scores and three for the outputs 4.5 times that in the matrix cores).
 //
 // Layout of the work.  S^T = K q^T puts positions in the rows of a 16x16 tile
 // and query rows in its columns: a lane holds one query row's scores at 4
