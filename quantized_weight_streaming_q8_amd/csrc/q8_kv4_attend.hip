@@ -562,8 +562,9 @@ __device__ inline void softmax_and_values(const Values<NB>& v, Rows<NB, F>& rows
     }
 }
 
-// What one sequence needs: its slot (that of its first row that is not
-// idle), positions [lo, hi) and the steps that hold them.
+// What one sequence needs: its slot (that of its first row that is not idle, as
+// the caller has it: it may lie outside the table), positions [lo, hi) and the
+// steps that hold them.
 struct Extent {
     int lo, hi, tiles, slot;
 };
@@ -835,12 +836,9 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int rec_rows, float* reco
         const int first = t0 + wave;
         int page0 = first / groups_per_page, in_page = first - page0 * groups_per_page;
         int page = 0;  // of the next group to load, from page0; lane i holds the id of page0 + i
-        const auto load_ids = [&](int p0) {
-            const int p = p0 + lane;
-            return p < a.c.max_pages ? a.c.table[(int64_t)slot * a.c.max_pages + p] : -1;
-        };
-        int ids = 0;
-        if (slot >= 0) ids = load_ids(page0);
+        // (a slot that the table does not have gives -1)
+        const auto load_ids = [&](int p0) { return table_entry(a.c, slot, p0 + lane); };
+        int ids = load_ids(page0);
         Rows<NB, F> rows;
         const int row = min(rb * kRows + col, n_rows - 1);  // past the last: that again
         const int token = row / a.group;

@@ -76,11 +76,19 @@ struct KvView {
     int32_t n_slots, max_pages, page_tokens, n_kv, nb;
 };
 
+// Entry i of slot s in the block table, -1 where the table has no such entry.
+// Slots and positions come from device arrays that the host cannot check, so
+// the table is read here and nowhere else.
+__host__ __device__ inline int32_t table_entry(const KvView& c, int s, int i) {
+    if ((uint32_t)s >= (uint32_t)c.n_slots || (uint32_t)i >= (uint32_t)c.max_pages) return -1;
+    return c.table[(int64_t)s * c.max_pages + i];
+}
+
 // Page of position p of slot s, or -1 where slot, position or page lies
 // outside the cache.
-__device__ inline int64_t kv_page(const KvView& c, int s, int p) {
+__host__ __device__ inline int64_t kv_page(const KvView& c, int s, int p) {
     if (s < 0 || s >= c.n_slots || p < 0 || p >= c.max_pages * c.page_tokens) return -1;
-    const int64_t pg = c.table[(int64_t)s * c.max_pages + p / c.page_tokens];
+    const int64_t pg = table_entry(c, s, p / c.page_tokens);
     return pg >= 0 && pg < c.n_pages ? pg : -1;
 }
 
