@@ -523,7 +523,8 @@ __device__ inline void softmax_and_values(const Values<NB>& v, Rows<NB, F>& rows
                 const float y = S[i >> 2][i & 3];
                 S[i >> 2][i & 3] = y >= huge ? __builtin_inff() : y <= -huge ? -__builtin_inff() : y;
             }
-            t = t >= huge ? __builtin_inff() : t <= -huge ? -__builtin_inff() : t;
+            // a maximum of -infinity stays finite: less itself it would be NaN
+            t = t >= huge ? __builtin_inff() : t <= -huge ? -__FLT_MAX__ : t;
         }
         const float m = grow ? t : rows.m;
         const float f = grow ? __builtin_amdgcn_exp2f((rows.m - m) * c) : 1.0f;

@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 import torch
 
+import kv4_ref as ref
 from gpu_util import q8 as _q8
 from test_gpu_kv4 import Step
 
@@ -46,3 +47,34 @@ def test_slots_outside_the_table(q8, tokens, group, slot):
         assert (np.abs(got[rows] - want[rows]) <= tol[rows]).all()
     assert not s.ws[:1 << 20].any()
     assert np.array_equal(s.run(), got, equal_nan=True)
+
+
+# positions whose score overflows to -inf, of how many, window, query heads
+LOST = [
+    (np.arange(32), 200, 0, 1),               # the first step of one wave
+    (np.arange(32), 200, 0, 9),               # the same with 16 rows a tile
+    (np.r_[0:32, 128:160], 200, 0, 3),        # all that one wave sees
+    (np.array([31]), 190, 159, 2),            # the one position a window leaves of its first step
+    (np.arange(1300), 3000, 0, 2),            # whole parts of a cut sequence
+    (np.r_[0:700, 1500:3000], 3000, 0, 12),
+    (np.arange(1, 90), 90, 0, 4),             # all but the first position
+]
+
+
+@pytest.mark.parametrize("lost,length,window,group", LOST)
+def test_scores_of_minus_infinity_only_lose_their_positions(q8, lost, length, window, group):
+    """A row with positions whose scores overflow to -inf is the attention
+    over its other positions, wherever a wave's steps and a sequence's parts
+    begin.  Those have score zero here: their weights are equal."""
+    s = Step(q8, 32, 1, group, 1, 32, [length], window=window)
+    k = np.zeros((length, 1, 32), np.float32)
+    k[lost, 0, 0] = 3e38
+    s.put(0, np.arange(length), k, s.v[0])
+    s.q[:] = 0
+    s.q[0, ::32] = -1e10
+    seen = np.setdiff1d(np.arange(max(0, length - window) if window else 0, length), lost)
+    v = ref.hold(s.v[0])[seen, 0]
+    want, tol = ref.attend(np.zeros((1, 32)), np.zeros_like(v), v, [len(seen) - 1], s.scale)
+    got = s.run()[0]
+    assert np.isfinite(got).all()
+    assert (np.abs(got - want) <= tol).all()
