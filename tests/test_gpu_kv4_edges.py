@@ -78,3 +78,34 @@ def test_scores_of_minus_infinity_only_lose_their_positions(q8, lost, length, wi
     got = s.run()[0]
     assert np.isfinite(got).all()
     assert (np.abs(got - want) <= tol).all()
+
+
+# sequences, tokens, kv heads, group, longest; with workgroups that share a
+# compute unit: 3 with up to 8 rows a head, else 2
+MANY = [(150, 1, 4, 4, 1200, 3), (70, 5, 2, 4, 1300, 2), (300, 1, 4, 2, 600, 3), (129, 3, 1, 2, 4000, 3)]
+
+
+@pytest.mark.parametrize("n,tokens,kv,group,longest,on_cu", MANY)
+def test_many_sequences_end_to_end(q8, n, tokens, kv, group, longest, on_cu):
+    """More sequences than a wave has lanes, and more steps than shares run at
+    once: they are measured 64 at a time while the shares are walked.  Some
+    are idle, one has no slot."""
+    rng = np.random.default_rng(n)
+    lens = rng.integers(tokens, longest, n).tolist()
+    lens[64] = tokens
+    row_blocks = 1 if on_cu == 3 else -(-tokens * group // 16)
+    least = sum(-(-L // 256) * 8 for L in lens) * row_blocks   # steps, a unit's rounded up to 8
+    assert least > 8 * (256 * on_cu // kv)
+    s = Step(q8, 64, kv, group, tokens, 32, lens, slots=n)
+    s.pos[[1, 63, 65]] = -1
+    s.seq[66 * tokens:67 * tokens] = n
+    got = s.run()
+    want, tol = s.want()
+    off = slice(66 * tokens, 67 * tokens)
+    assert np.isnan(got[off]).all()
+    got[off] = want[off]
+    assert (np.abs(got - want) <= tol).all()
+    again = s.run()
+    again[off] = want[off]
+    assert np.array_equal(again, got)
+    assert not s.ws[:1 << 20].any()
