@@ -158,11 +158,11 @@ __device__ inline uint32_t lds_address(const void* p) {
 // alone: 95 us against 109 without the hint).
 __device__ inline void lds_load16(uint32_t lds, const uint8_t* base, uint32_t voff) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt"
-                 ::"s"(lds), "v"(voff), "s"(base) : "memory");
+                 ::"s"(lds), "v"(voff), "s"(base) : "memory", "m0");
 }
 __device__ inline void lds_load4(uint32_t lds, const uint8_t* base, uint32_t voff) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
-                 ::"s"(lds), "v"(voff), "s"(base) : "memory");
+                 ::"s"(lds), "v"(voff), "s"(base) : "memory", "m0");
 }
 // At most N loads (and stores) still on their way.
 template <int N>
