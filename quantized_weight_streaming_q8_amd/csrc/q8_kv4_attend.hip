@@ -157,12 +157,12 @@ __device__ inline uint32_t lds_address(const void* p) {
 // once, past the caches' retention (16 sessions near 32768 positions, the loads
 // alone: 95 us against 109 without the hint).
 __device__ inline void lds_load16(uint32_t lds, const uint8_t* base, uint32_t voff) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt"
-                 ::"s"(lds), "v"(voff), "s"(base) : "memory", "m0");
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt" ::"v"(voff), "s"(base), "{m0}"(lds)
+                 : "memory");
 }
 __device__ inline void lds_load4(uint32_t lds, const uint8_t* base, uint32_t voff) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
-                 ::"s"(lds), "v"(voff), "s"(base) : "memory", "m0");
+    asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(base), "{m0}"(lds)
+                 : "memory");
 }
 // At most N loads (and stores) still on their way.
 template <int N>
