@@ -620,8 +620,16 @@ __device__ inline float part_weight(float m_part, float m, float c) {
 // at once is contiguous), then maxima and sums.
 __host__ __device__ constexpr int record_floats(int rows, int nb) { return rows * (nb * 32 + 2); }
 
-// Records pass from one CU to another within the launch: device-coherent
-// accesses.
+// Records pass from one CU to another within the launch, without a fence that
+// would write back and drop whole caches.  What orders them is this chip, not
+// the language's memory model: the stores go past the caches that other CUs do not
+// see (they are of device scope), each wave waits until its own have completed
+// (s_waitcnt vmcnt(0)), a barrier holds the workgroup's count back until all its
+// waves have, and the joining workgroup's loads, of device scope too, are issued
+// behind the barrier that follows its own count.  With the count itself as release
+// and acquire, which writes back an XCD's L2 at every part, 16 sessions up to 8192
+// positions take 53.4 us against 29.8, near 32768 122 against 102, 64 tokens of a
+// prompt 52.7 against 44.6.
 __device__ inline void publish(float* p, float v) {
     __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
