@@ -62,7 +62,13 @@ extern "C" {
  *           f / factor for r <= low, f for r >= high, and between them
  *           (1 - g) f / factor + g f with g = (r - low) / (high - low)
  *   YARN    the same with low and high as given, and the rotated values
- *           multiplied by the amplitude 0.1 ln(factor) + 1 */
+ *           multiplied by the amplitude 0.1 ln(factor) + 1
+ * Between low and high BANDS and YARN go linearly in the turns r, which for YARN is
+ * its published equation.  Models are also run with a YaRN whose ramp is linear
+ * in the pair's index i, between the indices (rounded outwards) where r = high
+ * and r = low.  Its frequencies between them are others, by up to 1.7 times for rot_dim
+ * 128, base 1e6, factor 4 and original_context 32768: for such a model fill the
+ * plan's inv_freq and amplitude with the model's own. */
 typedef enum q8_rotary_scaling {
     Q8_ROTARY_NONE = 0,
     Q8_ROTARY_LINEAR = 1,

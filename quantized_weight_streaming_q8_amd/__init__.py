@@ -430,7 +430,9 @@ def rotary_frequencies(rot_dim: int, base: float = 1e4, scaling: str = "none",
                        low: float = 1.0, high: float | None = None):
     """(frequencies float64 on the host, amplitude) of q8_rotary_frequencies.
     ``low`` and ``high`` bound the ramp of "bands" (default 1..4 turns) and
-    "yarn" (1..32)."""
+    "yarn" (1..32).  Both ramps are linear in the turns; a model whose YaRN ramp is
+    linear in the pair's index has other frequencies: make its plan from them,
+    ``Rotary(frequencies on the device, amplitude=...)``."""
     if scaling not in Q8_ROTARY_SCALINGS:
         raise ValueError(f"scaling: expected one of {sorted(Q8_ROTARY_SCALINGS)}, got {scaling!r}")
     if high is None:

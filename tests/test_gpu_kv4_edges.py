@@ -7,8 +7,8 @@ import pytest
 import torch
 
 import kv4_ref as ref
-from gpu_util import q8 as _q8
-from test_gpu_kv4 import Step
+from gpu_util import q8 as _q8, to_dev
+from test_gpu_kv4 import Step, host, i32, rotated_within
 
 pytestmark = pytest.mark.gpu
 
@@ -109,3 +109,27 @@ def test_many_sequences_end_to_end(q8, n, tokens, kv, group, longest, on_cu):
     again[off] = want[off]
     assert np.array_equal(again, got)
     assert not s.ws[:1 << 20].any()
+
+
+def test_plan_of_a_models_own_frequencies(q8):
+    """A YaRN whose ramp is linear in the pair's index, which is not "yarn":
+    its frequencies and amplitude make a plan of their own."""
+    rot, base, factor, context = 128, 1e6, 4.0, 32768.0
+    i = np.arange(rot // 2)
+    f = base ** (-2.0 * i / rot)
+
+    def index(turns):
+        return rot * np.log(context / (2 * np.pi * turns)) / (2 * np.log(base))
+    first, last = np.floor(index(32.0)), np.ceil(index(1.0))
+    kept = 1 - np.clip((i - first) / (last - first), 0, 1)
+    own = (1 - kept) * f / factor + kept * f
+    by_turns, amplitude = q8.rotary_frequencies(rot, base, "yarn", factor, context)
+    ratio = own / by_turns.numpy()
+    assert 1.7 < ratio.max() < 1.72 and (np.abs(ratio[np.r_[0:24, 40:64]] - 1) < 1e-12).all()
+    rng = np.random.default_rng(9)
+    x = rng.standard_normal((17, 3, rot), dtype=np.float32)
+    pos = rng.integers(0, 131072, 17)
+    plan = q8.Rotary(to_dev(own), amplitude=amplitude)
+    y = torch.empty(17, 3 * rot, device="cuda")
+    q8.q8_rotary(to_dev(x.reshape(17, -1)), y, 17, 3 * rot, i32(pos), 3, rot, plan)
+    assert rotated_within(host(y).reshape(17, 3, rot), x, pos, own, False, amplitude)
