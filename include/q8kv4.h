@@ -194,7 +194,9 @@ size_t q8_kv4_attend_workspace_bytes(const q8_kv4_cache* cache, int n_seq, int t
  * Arithmetic: the cache's values, Q (to 2^-29 of the largest of each 32
  * values of a head, and no finer than 2^-78) and the softmax weights enter the
  * matrix instructions as sums of short pieces, so that products have no
- * error; all sums, maxima and weights are fp32.  A NaN or an infinity in Q
+ * error; all sums, maxima and weights are fp32.  Weights are taken from a
+ * maximum that may lag behind by a factor of 2^8, so the outputs of values
+ * beyond 2^119 over their number may be infinite.  A NaN or an infinity in Q
  * gives a NaN row.  The positions of a sequence are divided by the lengths of
  * the whole batch and the parts added in a fixed order: a call gives the same
  * bits every time.
