@@ -24,11 +24,12 @@
 // the whole chip are round trips one after the other: the positions 2 us, page
 // ids and queries 2.5, the queries' pieces 2 (the first groups come in meanwhile), a
 // cut unit's parts on their way 3, their join 3 to 6.  Measured on one MI355X,
-// head_dim 128, 40 query heads on 8: 16 sessions of 1 to 8192 positions 27.9 us
-// (86 MB, 3.1 TB/s), of 24000 to 32768 92 us (502 MB, 5.5 TB/s), with 4 tokens
-// each of 1000 to 6000 positions 32.8 us (57 MB); 64 tokens of one session
-// behind 8192 positions 42.4 us (10.7 GFLOP, 252 TFLOP/s; with six pieces for the
-// scores and three for the outputs 4.5 times that in the matrix cores).
+// head_dim 128, 40 query heads on 8: 16 sessions of 5 to 8192 positions 28.5 us
+// (86 MB, 3.0 TB/s), of 24000 to 32768 94 us (502 MB, 5.4 TB/s; 40 launches on
+// end go from 91 to 120), with 4 tokens each of 1000 to 6000 positions 33.8 us
+// (57 MB); 64 tokens of one session behind 8192 positions 42.5 us (10.7 GFLOP, 252
+// TFLOP/s; with six pieces for the scores and three for the outputs 4.5 times
+// that in the matrix cores).
 //
 // Layout of the work.  S^T = K q^T puts positions in the rows of a 16x16 tile
 // and query rows in its columns: a lane holds one query row's scores at 4
@@ -86,7 +87,10 @@ constexpr int kMinSteps = 8;
 // Most parts of a unit, on average: one workgroup joins them, a few at a time, and
 // where there are few units that takes longer than their steps.  One session of
 // 32768 positions, 40 heads on 8: 43.6 us without the limit (96 parts), 34.2 with
-// 64, 26.6 with 32; of 100000 positions, 8 heads on 1: 105 (768 parts), 37.7, 42.1.
+// 64, 26.6 with 32; of 100000 positions, 8 heads on 1: 105 (391 parts), 37.7, 42.1.
+// The average is all that the host knows: short companions lift the limit for one
+// long unit.  With two sessions of 20 positions beside them these sessions take
+// 43.5 us (93 parts), and with 15 beside the second 106.
 constexpr int64_t kMostParts = 32;
 constexpr int kNoVmem = 0x0f70;  // s_waitcnt vmcnt(0), no other count
 
@@ -672,7 +676,9 @@ struct Room {
 // alone: shares are weighted by rank, 23 : 20 : 17 for three (16 sessions up to
 // 8192 tokens 31.5 -> 28.6 us, near 32768 tokens 103.8 -> 99.0, against equal
 // shares; at 26 : 20 : 14, 29.0 and 100.8) and 5 : 4 for two (4 drafted tokens of
-// 16 sessions 35.9 us; equal shares 38.2, 4 : 3 39.5).
+// 16 sessions 35.9 us; equal shares 38.2, 4 : 3 39.5).  Those are full grids.  One
+// that the context or kMostParts keeps smaller, with fewer workgroups to a CU or
+// one, is cut by the same weights, and its longest share is 15% (11%) above the mean.
 struct Shares {
     int64_t room;
     double unit;   // room of a share of weight 1

@@ -9,17 +9,19 @@
 // kernels are bound by memory, and for a step's few rows by the latency of
 // one load, one sincos and one store.  Measured on one MI355X, in a graph: 4099
 // rows of 40 heads of 128 rotated in 35.3 us (168 MB, 4.75 TB/s; a copy reaches
-// 5.1), 16 rows in 3.0 us, one row in 2.6 (a launch that does nothing
-// takes 1.7).
+// 5.1), 16 rows of 48 heads in 3.0 us, one row of 24 heads of 64 in 3.1 (a
+// launch that does nothing takes 1.7).
 //
 // Rotation alone: a thread takes V pairs at a time and writes both halves, so
 // in place is safe.  Append: a thread takes 4 consecutive values of a key or
 // value head; 8 lanes hold a block of 32 and agree on its scale with three
 // lane exchanges; a thread reads its rotation partners itself.  4099 rows of 40
-// query and 8 + 8 key and value heads: 47 us (115 MB read, 88 MB to write and 99
+// query and 8 + 8 key and value heads: 47 us (118 MB read, 88 MB to write and 99
 // written, as rows that follow one another in a head's group of 32 positions
-// write parts of the same lines; 4.3 TB/s), 16 rows 3.8 us.  Read: 4099 rows of 8 +
-// 8 heads 10.6 us (34 MB written), 16 rows 2.7.
+// write parts of the same lines; 4.4 TB/s).  Read: 4099 rows of 8 + 8 heads 10.5
+// us (34 MB written; 18.6 MB fetched where 4.5 are needed, as a row's value codes are
+// gathered byte by byte out of runs of 8 positions); at a copy's rate 7.4.
+// Append and read of 16 rows, in a graph: 6.1 us.
 
 #include "q8_kv4_internal.h"
 
