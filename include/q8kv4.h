@@ -33,7 +33,8 @@
  * them are device pointers), nothing allocated, work enqueued on `stream`,
  * arguments checked on the host before any HIP call.  Device arrays that the
  * host cannot check (batch_index, pos, block_table) are never read through
- * out of range: the entry points say what such a row gives.
+ * out of range: the entry points say what such a row gives.  They must not be
+ * written to while a call that reads them runs (every kernel ends all the same).
  */
 #ifndef Q8KV4_H
 #define Q8KV4_H

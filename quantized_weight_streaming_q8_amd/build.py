@@ -22,7 +22,7 @@ TIMELINE_LIB_PATH = os.path.join(HERE, "libq8narrow_timeline.so")
 
 SOURCES = ["q8_pack.hip", "q8_matmul.hip", "q8_rope.hip", "q8_measure.hip", "q8_abi.hip",
            "q8_noalloc.hip", "q8_kv4_rows.hip", "q8_kv4_attend.hip", "q8_kv4_abi.hip"]
-HEADERS = ["q8_internal.h", "q8_measure.h", "q8_kv4_internal.h"]
+HEADERS = ["q8_internal.h", "q8_measure.h", "q8_kv4_internal.h", "q8_kv4_shares.h"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -71,6 +71,7 @@
 // 64 tokens against 49.2).
 
 #include "q8_kv4_internal.h"
+#include "q8_kv4_shares.h"
 
 #include <algorithm>
 
@@ -81,9 +82,6 @@ constexpr int kWaves = 4, kThreads = 64 * kWaves;  // of a workgroup, a wave a S
 // The workspace starts with a counter for each unit, at the same place for
 // every shape: calls of other shapes find them at zero too.
 constexpr size_t kCounterBytes = kMaxRowBlocks * sizeof(uint32_t);
-// Least share: two steps a wave.  With 4 or 16 steps, 7 sessions with a window of
-// 1000 take 12.8 or 13.3 us against 12.1, the larger cases the same.
-constexpr int kMinSteps = 8;
 // Most parts of a unit, on average: one workgroup joins them, a few at a time, and
 // where there are few units that takes longer than their steps.  One session of
 // 32768 positions, 40 heads on 8: 43.6 us without the limit (96 parts), 34.2 with
@@ -670,47 +668,6 @@ struct Room {
     }
 };
 
-// The room cut into shares.  Even layout: kMinSteps each.  End to end: one for
-// each resident workgroup.  Where several share a CU, those dispatched first
-// get ahead of the others in its issue slots, and the last ones would run on
-// alone: shares are weighted by rank, 23 : 20 : 17 for three (16 sessions up to
-// 8192 tokens 31.5 -> 28.6 us, near 32768 tokens 103.8 -> 99.0, against equal
-// shares; at 26 : 20 : 14, 29.0 and 100.8) and 5 : 4 for two (4 drafted tokens of
-// 16 sessions 35.9 us; equal shares 38.2, 4 : 3 39.5).  Those are full grids.  One
-// that the context or kMostParts keeps smaller, with fewer workgroups to a CU or
-// one, is cut by the same weights, and its longest share is 15% (11%) above the mean.
-struct Shares {
-    int64_t room;
-    double unit;   // room of a share of weight 1
-    int n, rank;   // shares in all, and of one rank
-    int w[3];      // weight of a share by its rank
-    bool even;
-
-    __device__ Shares(int64_t room_, int n_, bool even_, int on_cu)
-        : room(room_), n(n_), rank(n_ / on_cu), even(even_) {
-        w[0] = on_cu == 3 ? 23 : on_cu == 2 ? 5 : 1;
-        w[1] = on_cu == 3 ? 20 : on_cu == 2 ? 4 : 1;
-        w[2] = on_cu == 3 ? 17 : w[1];
-        unit = (double)room / weight(n);
-    }
-    __device__ int weight(int i) const {  // of the first i shares
-        return w[0] * min(i, rank) + w[1] * max(min(i - rank, rank), 0) + w[2] * max(i - 2 * rank, 0);
-    }
-    __device__ int64_t start(int i) const {
-        if (even) return min((int64_t)kMinSteps * i, room);
-        return i >= n ? room : (int64_t)(unit * weight(i));
-    }
-    __device__ int at(int64_t pos) const {  // the share that holds pos
-        if (even) return (int)(pos / kMinSteps);
-        const int v = (int)((double)pos / unit), v0 = w[0] * rank, v1 = v0 + w[1] * rank;
-        int i = v < v0 ? v / w[0] : v < v1 ? rank + (v - v0) / w[1] : 2 * rank + (v - v1) / w[2];
-        i = min(i, n - 1);
-        while (start(i) > pos) --i;
-        while (start(i + 1) <= pos) ++i;
-        return i;
-    }
-};
-
 // Extents of 64 sequences and the room up to each one's end.
 struct Sequences {
     int64_t upto[64];              // end to end
@@ -821,6 +778,7 @@ kv4_attend_kernel(AttendArgs a, int n_rb, int abreast, int rec_rows, float* reco
         while ((past = __ballot(upto_of(lane) > at - before)) == 0) {
             before += upto_of(63);
             seq0 += 64;
+            if (seq0 >= a.n_seq) return;  // pos was written to meanwhile: no such unit
             __syncthreads();
             measure(seq0);
         }
