@@ -46,7 +46,9 @@ struct Shares {
     // The share that holds pos, for any pos >= 0 one of the n.
     __host__ __device__ int at(int64_t pos) const {
         if (even) return pos < room ? (int)(pos / kMinSteps) : n - 1;
-        const int v = (int)((double)pos / unit), v0 = w[0] * rank, v1 = v0 + w[1] * rank;
+        const double x = (double)pos / unit;
+        const int v = x < 1e9 ? (int)x : 1000000000;  // past the room it may be anything
+        const int v0 = w[0] * rank, v1 = v0 + w[1] * rank;
         int i = v < v0 ? v / w[0] : v < v1 ? rank + (v - v0) / w[1] : 2 * rank + (v - v1) / w[2];
         if (i > n - 1) i = n - 1;
         while (start(i) > pos) --i;
