@@ -19,15 +19,15 @@
 // weights'), with 16 rows or 8, about 1000 cycles of its SIMD; the matrix instructions
 // beside them take 576 with 16 rows and 350 with 8; its 4352 bytes come from HBM
 // in about 1500 cycles of the SIMD's share.  So 8 rows (a decode step of up to 8
-// grouped heads) are bound by HBM, with the vector units busy 65% of the time, 16
+// grouped heads) are bound by HBM, with the vector units busy 64% of the time, 16
 // by the vector instructions and what they wait for (52%).  About 16 us of a launch on
 // the whole chip are round trips one after the other: the positions 2 us, page
 // ids and queries 2.5, the queries' pieces 2 (the first groups come in meanwhile), a
 // cut unit's parts on their way 3, their join 3 to 6.  Measured on one MI355X,
-// head_dim 128, 40 query heads on 8: 16 sessions of 5 to 8192 positions 28.5 us
-// (86 MB, 3.0 TB/s), of 24000 to 32768 94 us (502 MB, 5.4 TB/s; 40 launches on
-// end go from 91 to 120), with 4 tokens each of 1000 to 6000 positions 33.8 us
-// (57 MB); 64 tokens of one session behind 8192 positions 42.5 us (10.7 GFLOP, 252
+// head_dim 128, 40 query heads on 8: 16 sessions of 5 to 8192 positions 27.9 us
+// (86 MB, 3.1 TB/s), of 24000 to 32768 92 us (502 MB, 5.5 TB/s; 40 launches on
+// end go from 90 to 120), with 4 tokens each of 1000 to 6000 positions 32.9 us
+// (57 MB); 64 tokens of one session behind 8192 positions 41.5 us (10.7 GFLOP, 258
 // TFLOP/s; with six pieces for the scores and three for the outputs 4.5 times
 // that in the matrix cores).
 //
@@ -87,8 +87,8 @@ constexpr size_t kCounterBytes = kMaxRowBlocks * sizeof(uint32_t);
 // 32768 positions, 40 heads on 8: 43.6 us without the limit (96 parts), 34.2 with
 // 64, 26.6 with 32; of 100000 positions, 8 heads on 1: 105 (391 parts), 37.7, 42.1.
 // The average is all that the host knows: short companions lift the limit for one
-// long unit.  With two sessions of 20 positions beside them these sessions take
-// 43.5 us (93 parts), and with 15 beside the second 106.
+// long unit.  Now the two take 24.9 and 40.6 us, with two sessions of 20 positions beside
+// the first 38.8 (93 parts), and with 15 beside the second 87.
 constexpr int64_t kMostParts = 32;
 constexpr int kNoVmem = 0x0f70;  // s_waitcnt vmcnt(0), no other count
 

@@ -9,7 +9,7 @@
 // kernels are bound by memory, and for a step's few rows by the latency of
 // one load, one sincos and one store.  Measured on one MI355X, in a graph: 4099
 // rows of 40 heads of 128 rotated in 35.3 us (168 MB, 4.75 TB/s; a copy reaches
-// 5.1), 16 rows of 48 heads in 3.0 us, one row of 24 heads of 64 in 3.1 (a
+// 5.1), 16 rows of 48 heads in 3.0 us, one row of 24 heads of 64 in 2.9 (a
 // launch that does nothing takes 1.7).
 //
 // Rotation alone: a thread takes V pairs at a time and writes both halves, so
