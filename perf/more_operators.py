@@ -1,6 +1,6 @@
 """The decode step's feed-forward side, measured: the norms around a block with
-their residual, gate and scale; quantisation to microscaled 4- and 8-bit
-blocks; the product with weights held in 4 bits; and the gated block, both
+their residual, gate and scale; quantisation to microscaled blocks of 4, 6 and
+8 bits; the product with weights held in 4 bits; and the gated block, both
 projections with the activation and the product.
 
 ``own`` false: ``run`` computes each operator in its plain form, elementary
@@ -11,11 +11,12 @@ definitions in 64 bits, separately from the plain form.
 
 The blocks are 32 consecutive values of a row with one power-of-two scale
 2^(s - 127) (the OCP microscaling formats).  "mx4": 1 sign, 2 exponent and 1
-mantissa bits (magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6); "mx8": 1 sign, 4
-exponent and 3 mantissa bits (largest 448).  For a block with largest
-magnitude a, the scale's exponent is floor(log2 a) - 2 (mx4) or - 8 (mx8), one
-more where a scaled by that exceeds 7 (mx4) or 464 (mx8), held to -125..125;
-values round to the nearest code, ties to the even code, and saturate.
+mantissa bits (magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6); "mx6": 1 sign, 2
+exponent and 3 mantissa bits (largest 7.5); "mx8": integers -127..127 over 64.
+For a block with largest magnitude a, the scale's exponent is floor(log2 a) - 2
+(mx8: floor(log2 a)), one more where a scaled by that would round beyond the
+largest magnitude (7, 7.75, 127.5 / 64), held to -120..125; values round to the
+nearest code, ties to the even code, and saturate.
 """
 
 import math
@@ -52,8 +53,8 @@ def listed():
         dict(name="product_one_row", op="product", live=1, slots=16, outputs=768, width=768, acts="mx8"),
         # a full 16-slot step through the large decoder's QKV projection
         dict(name="product_step", op="product", live=16, slots=16, outputs=7168, width=5120, acts="mx8"),
-        # the same step through the head
-        dict(name="product_head", op="product", live=16, slots=16, outputs=151936, width=5120, acts="mx8"),
+        # 16 sessions with drafted tokens, some of them short of one, through the head
+        dict(name="product_head", op="product", live=61, slots=64, outputs=151936, width=5120, acts="mx8"),
         # a prompt through the QKV projection, activations in 4 bits too
         dict(name="product_prompt", op="product", live=4099, slots=4099, outputs=7168, width=5120, acts="mx4"),
         # one token of one session, a small gated block
@@ -75,7 +76,7 @@ def _log(rng, lo, hi):
 def draw(rng):
     op = rng.choice(("norm", "quantize", "product", "product", "gated", "gated"))
     if op == "norm":
-        out = rng.choice(("y", "y", "mx8", "mx4"))
+        out = rng.choice(("y", "y", "mx8", "mx6", "mx4"))
         width = _log(rng, 1, 16384)
         if out != "y":
             width = 32 * _log(rng, 1, 512)
@@ -88,8 +89,8 @@ def draw(rng):
     if op == "quantize":
         width = 32 * _log(rng, 1, 576)
         return dict(op=op, rows=_log(rng, 1, max(1, min(16384, 7168 * 5120 // width))), width=width,
-                    out=rng.choice(("mx4", "mx8")))
-    acts = rng.choice(("mx8", "mx8", "mx4"))
+                    out=rng.choice(("mx4", "mx6", "mx8")))
+    acts = rng.choice(("mx8", "mx8", "mx6", "mx4"))
     width = 32 * _log(rng, 1, 576)
     both = 2 if op == "gated" else 1
     outputs = _log(rng, 1, min(151936 if op == "product" else 32768, 151936 * 5120 // (both * width)))
@@ -103,7 +104,7 @@ def draw(rng):
     return c
 
 
-HELD = {"mx4": 17 / 32, "mx8": 33 / 32}  # bytes a value
+HELD = {"mx4": 17 / 32, "mx6": 25 / 32, "mx8": 33 / 32}  # bytes a value
 
 
 def work(case):
@@ -132,7 +133,8 @@ def _params(kind):
 # ------------------------------------------------------------------- blocks
 
 MAGNITUDES = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
-TOP = {"mx4": (2, 7.0), "mx8": (8, 464.0)}  # largest exponent; what still rounds to the largest value
+# exponent of the largest magnitude, what still rounds to it, itself, mantissa bits
+FORMS = {"mx4": (2, 7.0, 6.0, 1), "mx6": (2, 7.75, 7.5, 3), "mx8": (0, 127.5 / 64, 127 / 64, 6)}
 
 
 def _pow2(e):
@@ -142,34 +144,40 @@ def _pow2(e):
 
 def _encode(x, form):
     """fp32 [..., d] -> (codes uint8, scale bytes uint8 [..., d/32]); mx4: two
-    codes a byte, the even value low."""
+    codes a byte, the even value low; mx6: sign, exponent and mantissa bits;
+    mx8: a two's complement integer."""
     b = x.reshape(*x.shape[:-1], -1, 32)
     a = b.abs().amax(-1, keepdim=True)
-    bad = ~(a < math.inf)
-    m, e = torch.frexp(a.masked_fill(bad, 1.0))
-    emax, top = TOP[form]
-    e = (e - 1 - emax + (2 ** (1 + emax) * m > top)).clamp(-125, 125)
-    y = (b * _pow2(-e)).masked_fill(bad, 0.0)
-    s = (e + 127).masked_fill(bad, 255).to(torch.uint8).squeeze(-1)
+    m, e = torch.frexp(a)
+    emax, border, _, bits = FORMS[form]
+    e = (e - 1 - emax + (2 ** (1 + emax) * m > border)).clamp(-120, 125)
+    y = b * _pow2(-e)
+    s = (e + 127).to(torch.uint8).squeeze(-1)
     if form == "mx8":
-        return y.clamp(-448.0, 448.0).to(torch.float8_e4m3fn).view(torch.uint8).flatten(-2), s
-    y = y.abs()
+        return torch.round(y * 64).clamp(-127, 127).to(torch.int8).view(torch.uint8).flatten(-2), s
+    neg, y = torch.signbit(y), y.abs()
+    if form == "mx6":  # in steps of 1/8 to 2, 1/4 to 4, 1/2 to 7.5
+        c = torch.where(y < 2, torch.round(y * 8), torch.where(y < 4, torch.round(y * 4) + 8, torch.round(y * 2) + 16))
+        return torch.where(neg, c.clamp_max(31) + 32, c.clamp_max(31)).to(torch.uint8).flatten(-2), s
     c = ((y > .25).to(torch.uint8) + (y >= .75) + (y > 1.25) + (y >= 1.75) + (y > 2.5)
          + (y >= 3.5) + (y > 5)).to(torch.uint8)
-    c = torch.where(torch.signbit(b), c + 8, c).masked_fill(bad, 0).to(torch.uint8)
-    c = c.reshape(*x.shape[:-1], -1, 2)
+    c = torch.where(neg, c + 8, c).to(torch.uint8).reshape(*x.shape[:-1], -1, 2)
     return c[..., 0] | (c[..., 1] << 4), s
 
 
 def _decode(codes, scales, form):
     """The fp32 values that codes and scale bytes stand for."""
     if form == "mx8":
-        v = codes.view(torch.float8_e4m3fn).float().unflatten(-1, (-1, 32))
+        v = codes.view(torch.int8).float() / 64
+    elif form == "mx6":
+        low, high = [i / 8 for i in range(16)], [2 + i / 4 for i in range(8)] + [4 + i / 2 for i in range(8)]
+        one = torch.tensor(low + high, device=codes.device)
+        v = torch.cat((one, -one))[codes.int()]
     else:
         one = torch.tensor(MAGNITUDES + tuple(-m for m in MAGNITUDES), device=codes.device)
         two = torch.stack((one.repeat(16), one.repeat_interleave(16)), -1)
-        v = two[codes.int()].flatten(-2).unflatten(-1, (-1, 32))
-    return (v * _pow2(scales.int() - 127).unsqueeze(-1)).flatten(-2)
+        v = two[codes.int()].flatten(-2)
+    return (v.unflatten(-1, (-1, 32)) * _pow2(scales.int() - 127).unsqueeze(-1)).flatten(-2)
 
 
 # ------------------------------------------------------------------- prepare
@@ -352,8 +360,7 @@ def _hold64(x, form):
     rounded to a multiple of its own binade's step, ties to even multiples."""
     b = x.double().unflatten(-1, (-1, 32))
     a = b.abs().amax(-1, keepdim=True)
-    least, bits, top = {"mx4": (0, 1, 6.0), "mx8": (-6, 3, 448.0)}[form]
-    emax, border = TOP[form]
+    emax, border, top, bits = FORMS[form]
 
     def exponent(v):  # floor(log2 v): the exponent field of v
         return ((v.view(torch.int64) >> 52) & 2047) - 1023
@@ -362,9 +369,9 @@ def _hold64(x, form):
         return ((e + 1023) << 52).view(torch.float64)
 
     e = exponent(a) - emax
-    e = torch.where(a > border * pow2(e), e + 1, e).clamp(-125, 125)
+    e = torch.where(a > border * pow2(e), e + 1, e).clamp(-120, 125)
     y = b.abs() / pow2(e)
-    step = pow2(exponent(y).clamp(min=least) - bits)
+    step = pow2(exponent(y).clamp(min=0) - bits)
     return (torch.copysign((torch.round(y / step) * step).clamp_max(top), b) * pow2(e)).flatten(-2)
 
 
