@@ -17,6 +17,11 @@ cache, its append, read-back and attention) takes two handles that a program
 makes once: ``Rotary`` (a plan, from ``rotary_plan``) and ``KV4Cache``.  Their
 tensors are checked when they are made, so that a step's calls check only
 what changes from step to step.
+
+The feed-forward side (``include/q8ffn.h``: norms around a block, microscaled
+blocks, products with 4-bit weights, the gated block) has handles of the same
+kind: ``MX4Weights``, ``Acts`` (a buffer of quantised activation rows) and
+``Norm``.
 """
 
 from __future__ import annotations
@@ -104,6 +109,35 @@ _KV4_SIGNATURES = {
     "q8_kv4_attend": ([_vp, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _f32, _i32, _vp, _i64, _vp,
                        _size, _vp], _i32),
 }
+
+
+class _MX4Weights(ctypes.Structure):
+    _fields_ = [("data", _vp), ("N", _i64), ("K", _i64)]
+
+
+class _Acts(ctypes.Structure):
+    _fields_ = [("data", _vp), ("K", _i64), ("n_slots", ctypes.c_int32), ("format", ctypes.c_int32)]
+
+
+class _Norm(ctypes.Structure):
+    _fields_ = [("weight", _vp), ("bias", _vp), ("weight_stride", _i64), ("bias_stride", _i64),
+                ("eps", ctypes.c_float), ("offset", ctypes.c_float), ("kind", ctypes.c_int32)]
+
+
+# include/q8ffn.h.
+_FFN_SIGNATURES = {
+    "q8_acts_bytes": ([ctypes.c_int32, _i64, ctypes.c_int32], _size),
+    "q8_mx4_weight_bytes": ([_i64, _i64], _size),
+    "q8_mx4_pack_weights": ([_vp, _vp, _vp], _i32),
+    "q8_mx4_pack_weights_q": ([_vp, _vp, _vp, _vp], _i32),
+    "q8_mx4_unpack_weights": ([_vp, _vp, _vp, _vp], _i32),
+    "q8_mx_quantize_acts": ([_vp, _i64, _i32, _vp, _vp], _i32),
+    "q8_mx_read_acts": ([_vp, _vp, _i32, _vp, _vp], _i32),
+    "q8_mx4_matmul": ([_vp, _vp, _vp, _i32, _vp, _i64, _vp], _i32),
+    "q8_mx4_gated": ([_vp, _vp, _vp, _vp, _i32, _i32, _vp, _i64, _vp, _vp], _i32),
+    "q8_norm_step": ([_vp, _i64, _vp, _vp, _i64, _f32, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _i32, _i64, _vp],
+                     _i32),
+}
 # The timeline build's own symbol (include/q8timeline.h).
 _TIMELINE_SIGNATURES = {
     "q8_timeline_set": ([_vp, _i64], _i32),
@@ -123,7 +157,8 @@ def _load_library():
             f"{LIB_PATH} is not built; run `python -c 'import __graft_entry__ as g; g.build()'` "
             "or `python quantized_weight_streaming_q8_amd/build.py` (hipcc, gfx950)")
     lib = ctypes.CDLL(LIB_PATH)
-    sigs = dict(_SIGNATURES, **_KV4_SIGNATURES, **(_TIMELINE_SIGNATURES if TIMELINE else {}))
+    sigs = dict(_SIGNATURES, **_KV4_SIGNATURES, **_FFN_SIGNATURES,
+                **(_TIMELINE_SIGNATURES if TIMELINE else {}))
     for name, (args, res) in sigs.items():
         fn = getattr(lib, name)
         fn.argtypes = args
@@ -621,6 +656,201 @@ def kv4_attend_workspace(cache: KV4Cache, n_seq: int, tokens_per_seq: int,
         raise ValueError(f"invalid attention shape: {n_seq} sequences of {tokens_per_seq} tokens, "
                          f"{n_q_heads} query heads over {cache.n_kv_heads}")
     return torch.zeros(nbytes, dtype=torch.uint8, device=cache.device)
+
+
+# --------------------------------- the feed-forward side (include/q8ffn.h)
+
+Q8_ACTS_FORMATS = {"q8_0": 0, "mx4": 1, "mx6": 2, "mx8": 3}
+Q8_ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3, "sigmoid": 4, "identity": 5}
+Q8_NORM_KINDS = {"rms": 0, "layer": 1}
+Q8_FFN_MAX_ROWS = 1 << 20
+Q8_NORM_MAX_WIDTH = 1 << 15
+_U8 = (torch.uint8,)
+
+
+def q8_acts_bytes(n_slots: int, K: int, format: str) -> int:
+    return int(_lib.q8_acts_bytes(n_slots, K, Q8_ACTS_FORMATS[format]))
+
+
+def q8_mx4_weight_bytes(N: int, K: int) -> int:
+    return int(_lib.q8_mx4_weight_bytes(N, K))
+
+
+class MX4Weights:
+    """An N x K weight matrix in 4-bit microscaled blocks (``data``: uint8,
+    allocated unless given; fill it with q8_mx4_pack_weights or
+    q8_mx4_pack_weights_q)."""
+
+    def __init__(self, N: int, K: int, data: torch.Tensor | None = None, device="cuda"):
+        nbytes = q8_mx4_weight_bytes(N, K)
+        if nbytes == 0:
+            raise ValueError(f"invalid shape N={N} K={K}")
+        if data is None:
+            data = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        (addr,) = _dev(_arg(data, "data", _ANY, nbytes))
+        self.data, self.N, self.K, self.nbytes = data, N, K, nbytes
+        self.device = data.device
+        self._device_index = data.get_device()
+        self._c = _MX4Weights(addr, N, K)
+        self._ref = ctypes.addressof(self._c)
+
+
+class Acts:
+    """A buffer of ``n_slots`` quantised activation rows of K values: "mx4",
+    "mx6" or "mx8", or "q8_0" for the slot buffer that q8_matmul_narrow takes
+    (as ``data``).  ``data`` is allocated, all zeros, unless given."""
+
+    def __init__(self, n_slots: int, K: int, format: str = "mx8", data: torch.Tensor | None = None,
+                 device="cuda"):
+        if format not in Q8_ACTS_FORMATS:
+            raise ValueError(f"format: expected one of {sorted(Q8_ACTS_FORMATS)}, got {format!r}")
+        nbytes = q8_acts_bytes(n_slots, K, format)
+        if nbytes == 0:
+            raise ValueError(f"invalid buffer shape: {n_slots} slots of {K} values in {format}")
+        if data is None:
+            data = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+        (addr,) = _dev(_arg(data, "data", _ANY, nbytes))
+        self.data, self.n_slots, self.K, self.format, self.nbytes = data, n_slots, K, format, nbytes
+        self.device = data.device
+        self._device_index = data.get_device()
+        self._c = _Acts(addr, K, n_slots, Q8_ACTS_FORMATS[format])
+        self._ref = ctypes.addressof(self._c)
+
+
+class Norm:
+    """A norm of rows of ``width`` values: kind "rms" or "layer", weight and
+    bias fp32 [width] or, one row of them for each row of a call,
+    [rows][width] (None: none).  ``offset`` is added to the weight."""
+
+    def __init__(self, width: int, kind: str = "rms", weight: torch.Tensor | None = None,
+                 bias: torch.Tensor | None = None, eps: float = 1e-6, offset: float = 0.0):
+        if kind not in Q8_NORM_KINDS:
+            raise ValueError(f"kind: expected one of {sorted(Q8_NORM_KINDS)}, got {kind!r}")
+        for name, t in (("weight", weight), ("bias", bias)):
+            if t is not None and (not isinstance(t, torch.Tensor) or t.dim() not in (1, 2) or t.shape[-1] != width):
+                raise ValueError(f"{name}: expected a tensor of [{width}] or [rows][{width}]")
+        w, b = _dev(_arg(weight, "weight", _F32), _arg(bias, "bias", _F32))
+        self.width, self.kind, self.weight, self.bias = width, kind, weight, bias
+        self.eps, self.offset = float(eps), float(offset)
+        given = [t for t in (weight, bias) if t is not None]
+        if len({t.device for t in given}) > 1:
+            raise ValueError(f"bias: on {bias.device}, but the weight is on {weight.device}")
+        # rows that the tensors hold, where there is one for each row of a call
+        self.rows = min((t.shape[0] for t in given if t.dim() == 2), default=None)
+        self.device = given[0].device if given else None
+        self._device_index = given[0].get_device() if given else None
+        stride = [0 if t is None or t.dim() == 1 else width for t in (weight, bias)]
+        self._c = _Norm(w, b, *stride, self.eps, self.offset, Q8_NORM_KINDS[kind])
+        self._ref = ctypes.addressof(self._c)
+
+
+def _norm_ref(n, name: str, width: int, n_rows: int):
+    if n is None:
+        return None
+    if isinstance(n, Norm):
+        if n.width != width:
+            raise ValueError(f"{name}: a norm of {n.width} values for rows of {width}")
+        if n.rows is not None and n.rows < n_rows:
+            raise ValueError(f"{name}: weights of {n.rows} rows for {n_rows}")
+        if n._device_index is None:
+            return n._ref
+    return _handle(n, Norm, name)
+
+
+def q8_mx4_pack_weights(W, weights: MX4Weights, stream=None) -> None:
+    (w,) = _dev(_arg(W, "W", _F32, _n(weights.N * weights.K, 4)))
+    _check(_lib.q8_mx4_pack_weights(w, _handle(weights, MX4Weights, "weights"), _stream(stream)),
+           "q8_mx4_pack_weights")
+
+
+def _codes(codes, scales, weights):
+    return _dev(_arg(codes, "codes", _U8, weights.N * weights.K // 2),
+                _arg(scales, "scales", _U8, weights.N * weights.K // 32))
+
+
+def q8_mx4_pack_weights_q(codes, scales, weights: MX4Weights, stream=None) -> None:
+    """codes uint8 [N][K/2] (two to a byte, the even column low) and scale
+    bytes uint8 [N][K/32]."""
+    c, s = _codes(codes, scales, weights)
+    _check(_lib.q8_mx4_pack_weights_q(c, s, _handle(weights, MX4Weights, "weights"), _stream(stream)),
+           "q8_mx4_pack_weights_q")
+
+
+def q8_mx4_unpack_weights(weights: MX4Weights, codes, scales, stream=None) -> None:
+    c, s = _codes(codes, scales, weights)
+    _check(_lib.q8_mx4_unpack_weights(_handle(weights, MX4Weights, "weights"), c, s, _stream(stream)),
+           "q8_mx4_unpack_weights")
+
+
+def q8_mx_quantize_acts(X, n_rows: int, acts: Acts, x_stride: int | None = None, stream=None) -> None:
+    """Rows of X (x_stride apart, default K) into slots 0 .. n_rows - 1."""
+    x_stride = acts.K if x_stride is None else x_stride
+    dev = _current_device()
+    (x,) = _fast_all(_fast(X, "X", torch.float32, _span(n_rows, x_stride, acts.K), dev))
+    _check(_lib.q8_mx_quantize_acts(x, x_stride, n_rows, _handle(acts, Acts, "acts"), _raw_stream(stream, dev)),
+           "q8_mx_quantize_acts")
+
+
+def q8_mx_read_acts(acts: Acts, batch_index, n_rows: int, X, stream=None) -> None:
+    """The values of slots batch_index[0 .. n_rows - 1] (None: slots 0 ..)."""
+    dev = _current_device()
+    bi, x = _fast_all(_fast(batch_index, "batch_index", torch.int32, _n(n_rows, 4), dev),
+                      _fast(X, "X", torch.float32, _n(n_rows * acts.K, 4), dev))
+    _check(_lib.q8_mx_read_acts(_handle(acts, Acts, "acts"), bi, n_rows, x, _raw_stream(stream, dev)),
+           "q8_mx_read_acts")
+
+
+def q8_mx4_matmul(weights: MX4Weights, acts: Acts, batch_index, n_live: int, Y, y_stride: int | None = None,
+                  stream=None) -> None:
+    """Y [n_live][N] (rows y_stride apart, default N); token t takes slot
+    batch_index[t] (None: slot t)."""
+    y_stride = weights.N if y_stride is None else y_stride
+    dev = _current_device()
+    bi, y = _fast_all(_fast(batch_index, "batch_index", torch.int32, _n(n_live, 4), dev),
+                      _fast(Y, "Y", torch.float32, _span(n_live, y_stride, weights.N), dev))
+    _check(_lib.q8_mx4_matmul(_handle(weights, MX4Weights, "weights"), _handle(acts, Acts, "acts"), bi, n_live, y,
+                              y_stride, _raw_stream(stream, dev)), "q8_mx4_matmul")
+
+
+def q8_mx4_gated(gate: MX4Weights, up: MX4Weights, acts: Acts, batch_index, n_live: int, H=None,
+                 h_acts: Acts | None = None, activation: str = "silu", h_stride: int | None = None,
+                 stream=None) -> None:
+    """activation(gate x) * (up x) for each token: fp32 rows to H, quantised
+    ones to slots 0 .. n_live - 1 of h_acts, or both."""
+    if activation not in Q8_ACTIVATIONS:
+        raise ValueError(f"activation: expected one of {sorted(Q8_ACTIVATIONS)}, got {activation!r}")
+    h_stride = gate.N if h_stride is None else h_stride
+    dev = _current_device()
+    bi, h = _fast_all(_fast(batch_index, "batch_index", torch.int32, _n(n_live, 4), dev),
+                      _fast(H, "H", torch.float32, _span(n_live, h_stride, gate.N), dev))
+    _check(_lib.q8_mx4_gated(_handle(gate, MX4Weights, "gate"), _handle(up, MX4Weights, "up"),
+                             _handle(acts, Acts, "acts"), bi, n_live, Q8_ACTIVATIONS[activation], h, h_stride,
+                             None if h_acts is None else _handle(h_acts, Acts, "h_acts"), _raw_stream(stream, dev)),
+           "q8_mx4_gated")
+
+
+def q8_norm_step(X, n_rows: int, K: int, post: Norm | None = None, gate=None, scale: float = 1.0, residual=None,
+                 residual_out=None, pre: Norm | None = None, Y=None, acts: Acts | None = None,
+                 x_stride: int | None = None, gate_stride: int | None = None, residual_stride: int | None = None,
+                 residual_out_stride: int | None = None, y_stride: int | None = None, stream=None) -> None:
+    """residual_out = residual + scale * gate * post(X); y = pre(residual_out)
+    goes to Y, to acts, or both.  Strides default to K, gate_stride to 0 (one
+    gate for all rows) unless the gate is a tensor of two dimensions."""
+    xs, rs, os, ys = (K if s is None else s for s in (x_stride, residual_stride, residual_out_stride, y_stride))
+    if gate_stride is None:
+        gate_stride = K if isinstance(gate, torch.Tensor) and gate.dim() == 2 else 0
+    dev = _current_device()
+    f32 = torch.float32
+    x, g, r, o, y = _fast_all(
+        _fast(X, "X", f32, _span(n_rows, xs, K), dev),
+        _fast(gate, "gate", f32, _span(n_rows, gate_stride, K), dev),
+        _fast(residual, "residual", f32, _span(n_rows, rs, K), dev),
+        _fast(residual_out, "residual_out", f32, _span(n_rows, os, K), dev),
+        _fast(Y, "Y", f32, _span(n_rows, ys, K), dev))
+    _check(_lib.q8_norm_step(x, xs, _norm_ref(post, "post", K, n_rows), g, gate_stride, scale, r, rs, o, os,
+                             _norm_ref(pre, "pre", K, n_rows), y, ys,
+                             None if acts is None else _handle(acts, Acts, "acts"), n_rows, K,
+                             _raw_stream(stream, dev)), "q8_norm_step")
 
 
 # ------------------------------------------------- torch allocation helpers

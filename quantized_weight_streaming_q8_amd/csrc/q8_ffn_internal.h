@@ -1,0 +1,225 @@
+// q8_ffn_internal.h -- the layouts of MX4 weights and MX activation buffers,
+// the encoding of a block, and the launchers of the feed-forward side.
+//
+// Packed MX4 weights (private).  Row groups of 16 rows, along K chunks of 128
+// columns (KC = ceil(K / 128)), the operand of one
+// v_mfma_scale_f32_16x16x128_f8f6f4 each, and super-chunks of 4 chunks (SC =
+// ceil(KC / 4)), whose scale bytes a lane takes in one 4-byte load:
+//   codes,  1024 bytes per (group, chunk), groups outermost: lane l = 16 g + r
+//     holds block g (columns 128 c + 32 g ..) of row r, 16 bytes at 16 l, the even
+//     value of a byte low;
+//   scales, after all codes, 256 bytes per (group, super-chunk): lane l's byte j,
+//     at 4 l + j, is the scale of its block in chunk 4 sc + j.
+// Rows and columns past the matrix are zeros.
+//
+// Activation buffers: the same with tiles of 16 slots for row groups and
+//   MX4  1024 bytes a chunk, as above;
+//   MX6  1536: the first 16 of a lane's 24 bytes (32 codes of 6 bits, in order)
+//        at 16 l, the other 8 at 1024 + 8 l;
+//   MX8  two such pieces, 3072: an integer q = +-(16 h + l), h 0..8, l 0..15, is
+//        held as the 6-bit codes of l / 8 (first) and h / 8, whose code is the
+//        number itself, so that both enter the matrix instruction as MX6 does,
+//        with the scales 2^(e - 3) and 2^(e + 1) for elements q / 64 * 2^e;
+// and for each piece a region of scales (MX8: 512 bytes per tile and super-chunk,
+// 256 for each piece).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "q8_internal.h"
+#include "q8ffn.h"
+
+namespace q8 {
+
+enum Form { kQ80 = Q8_ACTS_Q8_0, kMx4 = Q8_ACTS_MX4, kMx6 = Q8_ACTS_MX6, kMx8 = Q8_ACTS_MX8 };
+
+constexpr int kMxChunk = 128;      // columns of a matrix instruction
+constexpr int kNanScaleByte = 255;
+constexpr int kMinScaleExp = -120, kMaxScaleExp = 125;
+
+__host__ __device__ constexpr int form_pieces(int f) { return f == kMx8 ? 2 : 1; }
+__host__ __device__ constexpr int form_chunk_bytes(int f) {
+    return f == kMx4 ? 1024 : 1536 * form_pieces(f);
+}
+
+// An MX buffer (weights: rows = N, form kMx4) as the kernels take it.
+struct MxView {
+    uint8_t* codes;
+    uint8_t* scales;
+    int64_t rows, K;
+    int32_t kc, sc;  // chunks and super-chunks of a row
+};
+
+inline int64_t mx_tiles(int64_t rows) { return (rows + 15) / 16; }
+inline int64_t mx_chunks(int64_t K) { return (K + kMxChunk - 1) / kMxChunk; }
+inline int64_t mx_code_bytes(int64_t rows, int64_t K, int form) {
+    return mx_tiles(rows) * mx_chunks(K) * form_chunk_bytes(form);
+}
+inline int64_t mx_bytes(int64_t rows, int64_t K, int form) {
+    return mx_code_bytes(rows, K, form) +
+           mx_tiles(rows) * ((mx_chunks(K) + 3) / 4) * 256 * form_pieces(form);
+}
+inline MxView mx_view(void* data, int64_t rows, int64_t K, int form) {
+    uint8_t* p = static_cast<uint8_t*>(data);
+    const int64_t kc = mx_chunks(K);
+    return {p, p + mx_code_bytes(rows, K, form), rows, K, (int32_t)kc, (int32_t)((kc + 3) / 4)};
+}
+
+// Byte offsets of block b of row r (lane 16 (b & 3) + (r & 15) of a chunk).
+__device__ inline int64_t mx_code_offset(const MxView& v, int form, int64_t r, int b) {
+    return ((r >> 4) * v.kc + (b >> 2)) * form_chunk_bytes(form);
+}
+__device__ inline int mx_lane(int64_t r, int b) { return (b & 3) * 16 + (int)(r & 15); }
+__device__ inline int64_t mx_scale_offset(const MxView& v, int form, int64_t r, int b) {
+    return ((r >> 4) * v.sc + (b >> 4)) * (256 * form_pieces(form)) + mx_lane(r, b) * 4 + (b >> 2 & 3);
+}
+
+// ------------------------------------------------------------ encoding
+
+// The scale's exponent for a block whose largest magnitude is a (finite).
+template <int F>
+__device__ inline int mx_exponent(float a) {
+    constexpr int kTop = F == kMx8 ? 0 : 2;
+    // mantissa bits of 7/4, 7.75/4 and 127.5/64
+    constexpr uint32_t kBorder = F == kMx4 ? 0x600000u : F == kMx6 ? 0x780000u : 0x7f0000u;
+    const uint32_t u = __float_as_uint(a);
+    const int e = (int)(u >> 23) - 127 - kTop + ((u & 0x7fffffu) > kBorder ? 1 : 0);
+    return min(max(e, kMinScaleExp), kMaxScaleExp);
+}
+
+__device__ inline float exp2_int(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// The 6-bit code of v / 2^e (v finite): in units of 1/8 the codes to 15 are the
+// number, and above they are the upper bits of its floating-point form.
+__device__ inline uint32_t mx6_code(float v, int e) {
+    const float y = fminf(fabsf(v) * exp2_int(-e), 7.5f);
+    const uint32_t u = __float_as_uint(y);
+    const uint32_t high = ((u + 0x7ffffu + (u >> 20 & 1u)) >> 20) - (126u << 3);
+    const uint32_t low = (uint32_t)rintf(y * 8.0f);
+    return (y < 1.0f ? low : min(high, 31u)) | (__float_as_uint(v) >> 31) << 5;
+}
+
+// The integer of v / 2^e in units of 1/64, as sign and magnitude.
+__device__ inline uint32_t mx8_magnitude(float v, int e) {
+    return (uint32_t)fminf(rintf(fabsf(v) * exp2_int(6 - e)), 127.0f);
+}
+
+// Largest magnitude of a block held by 8 consecutive lanes, 4 values each;
+// +infinity if it holds a NaN or an infinity.
+__device__ inline float octet_max(const float (&v)[4]) {
+    float a = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float m = fabsf(v[i]);
+        a = fmaxf(a, m <= __FLT_MAX__ ? m : __builtin_inff());
+    }
+#pragma unroll
+    for (int m = 1; m < 8; m <<= 1) a = fmaxf(a, __shfl_xor(a, m, 8));
+    return a;
+}
+
+// 8 lanes' 24 bits each (lane p = 0..7) to the 24 bytes of a block: lanes 0..5
+// store a dword.  at16 and at8: the block's 16-byte and 8-byte places.
+__device__ inline void store_octet24(uint32_t bits, int p, uint8_t* at16, uint8_t* at8) {
+    const int a = 4 * p / 3, off = 32 * p - 24 * a;
+    const uint32_t x = __shfl(bits, a & 7, 8), y = __shfl(bits, (a + 1) & 7, 8);
+    const uint32_t w = x >> off | y << (24 - off);
+    if (p < 6) *reinterpret_cast<uint32_t*>(p < 4 ? at16 + 4 * p : at8 + 4 * (p - 4)) = w;
+}
+
+// Block b of slot r, held by 8 consecutive lanes (p = 0..7, values 4p .. 4p + 3;
+// all active), goes to the buffer.
+template <int F>
+__device__ inline void store_octet(const MxView& m, int64_t r, int b, int p, const float (&v)[4]) {
+    const float a = octet_max(v);
+    const bool nan = !(a <= __FLT_MAX__);
+    const int e = nan ? 0 : mx_exponent<F>(a);
+    uint8_t* c = m.codes + mx_code_offset(m, F, r, b);
+    const int l = mx_lane(r, b);
+    if constexpr (F == kMx4) {
+        uint32_t q = 0;
+        if (!nan) {
+            q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[0], v[1], exp2_int(e), 0);
+            q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[2], v[3], exp2_int(e), 1);
+        }
+        *reinterpret_cast<uint16_t*>(c + 16 * l + 2 * p) = (uint16_t)q;
+    } else if constexpr (F == kMx6) {
+        uint32_t q = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q |= (nan ? 0u : mx6_code(v[i], e)) << (6 * i);
+        store_octet24(q, p, c + 16 * l, c + 1024 + 8 * l);
+    } else {
+        uint32_t low = 0, high = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t n = nan ? 0u : mx8_magnitude(v[i], e);
+            const uint32_t s = (__float_as_uint(v[i]) >> 31) << 5;
+            low |= (s | (n & 15u)) << (6 * i);
+            high |= (s | n >> 4) << (6 * i);
+        }
+        store_octet24(low, p, c + 16 * l, c + 1024 + 8 * l);
+        store_octet24(high, p, c + 1536 + 16 * l, c + 1536 + 1024 + 8 * l);
+    }
+    if (p == 0) {
+        uint8_t* s = m.scales + mx_scale_offset(m, F, r, b);
+        if constexpr (F == kMx8) {
+            s[0] = (uint8_t)(nan ? kNanScaleByte : e + 127 - 3);
+            s[256] = (uint8_t)(nan ? kNanScaleByte : e + 127 + 1);
+        } else {
+            s[0] = (uint8_t)(nan ? kNanScaleByte : e + 127);
+        }
+    }
+}
+
+// ------------------------------------------------------------- launchers
+// Shapes and pointers are validated by the caller.
+
+hipError_t launch_mx_quantize(const float* X, int64_t x_stride, int64_t n_rows, const MxView& v, int form,
+                              bool pad_rows, hipStream_t st);
+hipError_t launch_mx4_import(const uint8_t* codes, const uint8_t* scales, const MxView& v, hipStream_t st);
+hipError_t launch_mx4_export(const MxView& v, uint8_t* codes, uint8_t* scales, hipStream_t st);
+hipError_t launch_mx_read(const MxView& v, int form, const int32_t* batch_index, int64_t n_rows, float* X,
+                          hipStream_t st);
+
+// A product or, with wu.codes, the gated block.
+struct MxProduct {
+    MxView w, wu;   // wu.codes null: no second projection
+    MxView x;
+    int form;
+    const int32_t* batch_index;
+    int n_live;
+    float* Y;       // null: no fp32 rows
+    int64_t y_stride;
+    MxView out;     // out.codes null: no quantised rows
+    int out_form;
+    int activation;
+};
+hipError_t launch_mx_product(const MxProduct& p, hipStream_t st);
+
+struct NormView {
+    const float* weight;
+    const float* bias;
+    int64_t weight_stride, bias_stride;
+    double eps, offset;
+    int kind;  // q8_norm_kind, -1: none
+};
+struct NormStep {
+    const float* X;
+    const float* R;
+    const float* gate;
+    float* R_out;
+    float* Y;
+    int64_t x_stride, r_stride, gate_stride, r_out_stride, y_stride;
+    NormView post, pre;
+    double scale;
+    MxView acts;  // codes null: none
+    int acts_form;
+    uint16_t* q80_scales;  // with kQ80
+    int64_t q80_sc;        // super-chunks of q8_internal.h's layout
+    int64_t K;
+    int n_rows;
+};
+hipError_t launch_norm_step(const NormStep& s, hipStream_t st);
+
+}  // namespace q8

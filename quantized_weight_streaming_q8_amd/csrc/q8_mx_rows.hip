@@ -1,0 +1,185 @@
+// q8_mx_rows.hip -- microscaled blocks: quantisation of rows and weights, import
+// and export of MX4 weights, and the read-back of activation buffers.
+
+#include <algorithm>
+
+#include "q8_ffn_internal.h"
+
+namespace q8 {
+namespace {
+
+constexpr int kThreads = 256;
+
+// 8 consecutive lanes a block, 4 values each.  total = rows x padded blocks x 8.
+template <int F>
+__global__ void __launch_bounds__(kThreads)
+mx_quantize_kernel(const float* __restrict__ X, int64_t x_stride, int64_t n_rows, int64_t total, MxView m,
+                   bool vec) {
+    const int blocks = m.kc * 4;
+    // whole octets: total and the grid are multiples of 8
+    for (int64_t tid = (int64_t)blockIdx.x * kThreads + threadIdx.x; tid < total; tid += (int64_t)gridDim.x * kThreads) {
+        const int p = (int)(tid & 7);
+        const int64_t r = (tid >> 3) / blocks;
+        const int b = (int)((tid >> 3) - r * blocks);
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        if (r < n_rows && (int64_t)b * 32 < m.K) {
+            const float* x = X + r * x_stride + b * 32 + p * 4;
+            if (vec) {
+                const float4 t = *reinterpret_cast<const float4*>(x);
+                v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = x[i];
+            }
+        }
+        store_octet<F>(m, r, b, p, v);
+    }
+}
+
+// A thread a block: 16 bytes of codes and a scale byte.
+__global__ void __launch_bounds__(kThreads)
+mx4_import_kernel(const uint4* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t total, MxView m) {
+    const int64_t tid = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (tid >= total) return;
+    // lanes in the order of a chunk: neighbours write neighbouring bytes
+    const int l = (int)(tid & 63);
+    const int64_t chunk = tid >> 6;
+    const int64_t r = chunk / m.kc * 16 + (l & 15);
+    const int b = (int)(chunk % m.kc) * 4 + (l >> 4);
+    const int64_t blocks = m.K / 32;
+    uint4 q = make_uint4(0u, 0u, 0u, 0u);
+    uint8_t s = 127;
+    if (r < m.rows && b < blocks) {
+        q = codes[r * blocks + b];
+        s = scales[r * blocks + b];
+    }
+    *reinterpret_cast<uint4*>(m.codes + chunk * 1024 + l * 16) = q;
+    m.scales[mx_scale_offset(m, kMx4, r, b)] = s;
+}
+
+__global__ void __launch_bounds__(kThreads)
+mx4_export_kernel(MxView m, int64_t total, uint4* __restrict__ codes, uint8_t* __restrict__ scales) {
+    const int64_t tid = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (tid >= total) return;
+    const int64_t blocks = m.K / 32, r = tid / blocks;
+    const int b = (int)(tid - r * blocks);
+    codes[tid] = *reinterpret_cast<const uint4*>(m.codes + mx_code_offset(m, kMx4, r, b) + 16 * mx_lane(r, b));
+    scales[tid] = m.scales[mx_scale_offset(m, kMx4, r, b)];
+}
+
+// The value of a 6-bit code (sign, 2 exponent, 3 mantissa bits).
+__device__ inline float mx6_value(uint32_t c) {
+    const uint32_t n = c & 31u;
+    // to 15 in units of 1/8; above, the code is the upper bits of a float
+    const float v = n < 8u ? (float)n * 0.125f : __uint_as_float((n + (126u << 3)) << 20);
+    return c & 32u ? -v : v;
+}
+
+// 24 bits from byte 3p of a block's 24 bytes.
+__device__ inline uint32_t load_octet24(const uint8_t* at16, const uint8_t* at8, int p) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const int k = 3 * p + i;
+        w |= (uint32_t)(k < 16 ? at16[k] : at8[k - 16]) << (8 * i);
+    }
+    return w;
+}
+
+template <int F>
+__global__ void __launch_bounds__(kThreads)
+mx_read_kernel(MxView m, const int32_t* __restrict__ batch_index, int64_t total, float* __restrict__ X, bool vec) {
+    const int64_t tid = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (tid >= total) return;
+    const int p = (int)(tid & 7);
+    const int64_t blocks = m.K / 32, t = (tid >> 3) / blocks;
+    const int b = (int)((tid >> 3) - t * blocks);
+    const int64_t r = batch_index ? batch_index[t] : t;
+    float v[4];
+    if (r < 0 || r >= m.rows) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = __builtin_nanf("");
+    } else {
+        const uint8_t* c = m.codes + mx_code_offset(m, F, r, b);
+        const int l = mx_lane(r, b);
+        const int s = m.scales[mx_scale_offset(m, F, r, b)];
+        const bool nan = s == kNanScaleByte;
+        if constexpr (F == kMx4) {
+            const uint32_t w = *reinterpret_cast<const uint16_t*>(c + 16 * l + 2 * p);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t n = w >> (4 * i) & 7u;
+                const float x = n < 2u ? (float)n * 0.5f : __uint_as_float((n + (126u << 1)) << 22);
+                v[i] = ldexpf(w >> (4 * i) & 8u ? -x : x, s - 127);
+            }
+        } else if constexpr (F == kMx6) {
+            const uint32_t w = load_octet24(c + 16 * l, c + 1024 + 8 * l, p);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = ldexpf(mx6_value(w >> (6 * i) & 63u), s - 127);
+        } else {
+            const uint32_t w = load_octet24(c + 16 * l, c + 1024 + 8 * l, p);
+            const uint32_t h = load_octet24(c + 1536 + 16 * l, c + 1536 + 1024 + 8 * l, p);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float n = (float)((h >> (6 * i) & 31u) * 16u + (w >> (6 * i) & 31u));
+                v[i] = ldexpf(w >> (6 * i) & 32u ? -n : n, s + 3 - 127 - 6);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = nan ? __builtin_nanf("") : v[i];
+    }
+    float* x = X + (t * blocks + b) * 32 + p * 4;
+    if (vec) {
+        *reinterpret_cast<float4*>(x) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = v[i];
+    }
+}
+
+// A launch holds fewer than 2^32 threads; a kernel with more to do goes round.
+inline unsigned grid_for(int64_t total) {
+    return (unsigned)std::min<int64_t>((total + kThreads - 1) / kThreads, 1 << 23);
+}
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+}  // namespace
+
+hipError_t launch_mx_quantize(const float* X, int64_t x_stride, int64_t n_rows, const MxView& v, int form,
+                              bool pad_rows, hipStream_t st) {
+    const int64_t rows = pad_rows ? mx_tiles(v.rows) * 16 : n_rows;  // zeros past the matrix
+    const int64_t total = rows * v.kc * 4 * 8;
+    const bool vec = aligned16(X) && x_stride % 4 == 0;
+    const dim3 g(grid_for(total)), b(kThreads);
+    if (form == kMx4) mx_quantize_kernel<kMx4><<<g, b, 0, st>>>(X, x_stride, n_rows, total, v, vec);
+    else if (form == kMx6) mx_quantize_kernel<kMx6><<<g, b, 0, st>>>(X, x_stride, n_rows, total, v, vec);
+    else mx_quantize_kernel<kMx8><<<g, b, 0, st>>>(X, x_stride, n_rows, total, v, vec);
+    return hipGetLastError();
+}
+
+hipError_t launch_mx4_import(const uint8_t* codes, const uint8_t* scales, const MxView& v, hipStream_t st) {
+    const int64_t total = mx_tiles(v.rows) * v.kc * 64;
+    mx4_import_kernel<<<dim3(grid_for(total)), dim3(kThreads), 0, st>>>(reinterpret_cast<const uint4*>(codes), scales,
+                                                                        total, v);
+    return hipGetLastError();
+}
+
+hipError_t launch_mx4_export(const MxView& v, uint8_t* codes, uint8_t* scales, hipStream_t st) {
+    const int64_t total = v.rows * (v.K / 32);
+    mx4_export_kernel<<<dim3(grid_for(total)), dim3(kThreads), 0, st>>>(v, total, reinterpret_cast<uint4*>(codes), scales);
+    return hipGetLastError();
+}
+
+hipError_t launch_mx_read(const MxView& v, int form, const int32_t* batch_index, int64_t n_rows, float* X,
+                          hipStream_t st) {
+    const int64_t total = n_rows * (v.K / 32) * 8;
+    const bool vec = aligned16(X);
+    const dim3 g(grid_for(total)), b(kThreads);
+    if (form == kMx4) mx_read_kernel<kMx4><<<g, b, 0, st>>>(v, batch_index, total, X, vec);
+    else if (form == kMx6) mx_read_kernel<kMx6><<<g, b, 0, st>>>(v, batch_index, total, X, vec);
+    else mx_read_kernel<kMx8><<<g, b, 0, st>>>(v, batch_index, total, X, vec);
+    return hipGetLastError();
+}
+
+}  // namespace q8
