@@ -32,7 +32,7 @@
  * which the host cannot check, is never read through out of range.
  * Shapes: N >= 1, K a multiple of 32, 32..2^20; a weight matrix padded to whole
  * groups of 16 rows and 128 columns holds at most 2^34 values, an activation
- * buffer at most 2^31.  Buffers are 256-byte aligned, fp32 and int32
+ * buffer, its rows padded to 512 columns, at most 2^31.  Buffers are 256-byte aligned, fp32 and int32
  * pointers 4 bytes unless it says otherwise.  Outputs must not overlap inputs
  * unless it says so.
  */
@@ -58,8 +58,7 @@ typedef enum q8_acts_format {
 } q8_acts_format;
 
 /* A buffer of n_slots activation rows of K values.  The layout is private (the
- * order in which the matrix instructions take their operands); an MX4 buffer
- * is the packed form of an n_slots x K weight matrix.  n_slots 1..2^20. */
+ * order in which the matrix instructions take their operands).  n_slots 1..2^20. */
 typedef struct {
     void* data;
     int64_t K;

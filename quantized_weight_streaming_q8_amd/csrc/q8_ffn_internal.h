@@ -1,27 +1,33 @@
 // q8_ffn_internal.h -- the layouts of MX4 weights and MX activation buffers,
 // the encoding of a block, and the launchers of the feed-forward side.
 //
-// Packed MX4 weights (private).  Row groups of 16 rows, along K chunks of 128
-// columns (KC = ceil(K / 128)), the operand of one
-// v_mfma_scale_f32_16x16x128_f8f6f4 each, and super-chunks of 4 chunks (SC =
-// ceil(KC / 4)), whose scale bytes a lane takes in one 4-byte load:
-//   codes,  1024 bytes per (group, chunk), groups outermost: lane l = 16 g + r
-//     holds block g (columns 128 c + 32 g ..) of row r, 16 bytes at 16 l, the even
-//     value of a byte low;
+// Both are cut along K into chunks of 128 columns (KC = ceil(K / 128)), the depth of
+// one v_mfma_scale_f32_16x16x128_f8f6f4, and super-chunks of 4 chunks (SC =
+// ceil(KC / 4)), whose scale bytes a lane takes in one 4-byte load.  Lane l = 16 g
+// + r of the instruction holds block g (32 values) of row r.  Padding is zeros.
+//
+// Packed MX4 weights: in row groups of 16 rows, as the instruction's lanes take
+// them, so that a wave's load is 1 KB of consecutive bytes:
+//   codes,  1024 bytes per (group, chunk), groups outermost: lane l's 16 bytes at
+//     16 l, the even value of a byte low;
 //   scales, after all codes, 256 bytes per (group, super-chunk): lane l's byte j,
 //     at 4 l + j, is the scale of its block in chunk 4 sc + j.
-// Rows and columns past the matrix are zeros.
 //
-// Activation buffers: the same with tiles of 16 slots for row groups and
-//   MX4  1024 bytes a chunk, as above;
-//   MX6  1536: the first 16 of a lane's 24 bytes (32 codes of 6 bits, in order)
-//        at 16 l, the other 8 at 1024 + 8 l;
-//   MX8  two such pieces, 3072: an integer q = +-(16 h + l), h 0..8, l 0..15, is
-//        held as the 6-bit codes of l / 8 (first) and h / 8, whose code is the
-//        number itself, so that both enter the matrix instruction as MX6 does,
-//        with the scales 2^(e - 3) and 2^(e + 1) for elements q / 64 * 2^e;
-// and for each piece a region of scales (MX8: 512 bytes per tile and super-chunk,
-// 256 for each piece).
+// Activation buffers: a slot's row is consecutive bytes, since tokens take slots
+// in any order (a random order over the weights' layout fetched a 128-byte line for
+// each 16 bytes of 4-bit codes: 3.5 times the L2 requests over 4099 tokens).
+// Per slot and chunk
+//   MX4  64 bytes: blocks 0..3, 16 bytes each;
+//   MX6  96: the first 16 of each block's 24 bytes (32 codes of 6 bits, in order),
+//        then the other 8 of each;
+//   MX8  192: two pieces.  An integer q = +-(16 h + l), h 0..8, l 0..15, is held as the
+//        6-bit codes of l / 8 (first) and h / 8, whose code is the number itself, so that
+//        both enter the instruction as MX6 does, with the scales 2^(e - 3) and 2^(e + 1)
+//        for elements q / 64 * 2^e.  16 bytes of each block's first piece, of each
+//        block's second, then 8 bytes of them, in the same order.
+// Rows are padded to whole super-chunks (a multiple of 128 bytes).  After all
+// codes, per slot and super-chunk 16 scale bytes for each piece: byte 4 g + j is block
+// g of chunk j.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -32,18 +38,18 @@
 
 namespace q8 {
 
-enum Form { kQ80 = Q8_ACTS_Q8_0, kMx4 = Q8_ACTS_MX4, kMx6 = Q8_ACTS_MX6, kMx8 = Q8_ACTS_MX8 };
+enum Form { kQ80 = Q8_ACTS_Q8_0, kMx4 = Q8_ACTS_MX4, kMx6 = Q8_ACTS_MX6, kMx8 = Q8_ACTS_MX8, kWeights = 4 };
 
-constexpr int kMxChunk = 128;      // columns of a matrix instruction
+constexpr int kMxChunk = 128;   // columns of a matrix instruction
 constexpr int kNanScaleByte = 255;
 constexpr int kMinScaleExp = -120, kMaxScaleExp = 125;
 
 __host__ __device__ constexpr int form_pieces(int f) { return f == kMx8 ? 2 : 1; }
-__host__ __device__ constexpr int form_chunk_bytes(int f) {
-    return f == kMx4 ? 1024 : 1536 * form_pieces(f);
-}
+// Bytes of a slot's chunk, and of its scales in a super-chunk.
+__host__ __device__ constexpr int chunk_bytes(int f) { return f == kMx4 ? 64 : 96 * form_pieces(f); }
+__host__ __device__ constexpr int scale_bytes(int f) { return 16 * form_pieces(f); }
 
-// An MX buffer (weights: rows = N, form kMx4) as the kernels take it.
+// An MX buffer or packed weights as the kernels take them.
 struct MxView {
     uint8_t* codes;
     uint8_t* scales;
@@ -51,28 +57,45 @@ struct MxView {
     int32_t kc, sc;  // chunks and super-chunks of a row
 };
 
-inline int64_t mx_tiles(int64_t rows) { return (rows + 15) / 16; }
 inline int64_t mx_chunks(int64_t K) { return (K + kMxChunk - 1) / kMxChunk; }
-inline int64_t mx_code_bytes(int64_t rows, int64_t K, int form) {
-    return mx_tiles(rows) * mx_chunks(K) * form_chunk_bytes(form);
+inline int64_t mx_supers(int64_t K) { return (mx_chunks(K) + 3) / 4; }
+inline int64_t weight_groups(int64_t N) { return (N + 15) / 16; }
+inline int64_t weight_bytes(int64_t N, int64_t K) {
+    return weight_groups(N) * (mx_chunks(K) * 1024 + mx_supers(K) * 256);
 }
-inline int64_t mx_bytes(int64_t rows, int64_t K, int form) {
-    return mx_code_bytes(rows, K, form) +
-           mx_tiles(rows) * ((mx_chunks(K) + 3) / 4) * 256 * form_pieces(form);
+inline int64_t acts_code_bytes(int64_t slots, int64_t K, int form) {
+    return (slots * mx_supers(K) * 4 * chunk_bytes(form) + 255) / 256 * 256;
 }
-inline MxView mx_view(void* data, int64_t rows, int64_t K, int form) {
+inline int64_t acts_bytes(int64_t slots, int64_t K, int form) {
+    return acts_code_bytes(slots, K, form) + slots * mx_supers(K) * scale_bytes(form);
+}
+inline MxView weights_view(void* data, int64_t N, int64_t K) {
     uint8_t* p = static_cast<uint8_t*>(data);
-    const int64_t kc = mx_chunks(K);
-    return {p, p + mx_code_bytes(rows, K, form), rows, K, (int32_t)kc, (int32_t)((kc + 3) / 4)};
+    return {p, p + weight_groups(N) * mx_chunks(K) * 1024, N, K, (int32_t)mx_chunks(K), (int32_t)mx_supers(K)};
+}
+inline MxView acts_view(void* data, int64_t slots, int64_t K, int form) {
+    uint8_t* p = static_cast<uint8_t*>(data);
+    return {p, p + acts_code_bytes(slots, K, form), slots, K, (int32_t)mx_chunks(K), (int32_t)mx_supers(K)};
 }
 
-// Byte offsets of block b of row r (lane 16 (b & 3) + (r & 15) of a chunk).
-__device__ inline int64_t mx_code_offset(const MxView& v, int form, int64_t r, int b) {
-    return ((r >> 4) * v.kc + (b >> 2)) * form_chunk_bytes(form);
+// Block b of row r: its 16 bytes of piece i, its 8 bytes of piece i, its scale.
+template <int F>
+__device__ inline uint8_t* block16(const MxView& m, int64_t r, int b, int i) {
+    if constexpr (F == kWeights)
+        return m.codes + ((r >> 4) * m.kc + (b >> 2)) * 1024 + ((b & 3) * 16 + (int)(r & 15)) * 16;
+    else
+        return m.codes + (r * m.sc * 4 + (b >> 2)) * chunk_bytes(F) + 64 * i + (b & 3) * 16;
 }
-__device__ inline int mx_lane(int64_t r, int b) { return (b & 3) * 16 + (int)(r & 15); }
-__device__ inline int64_t mx_scale_offset(const MxView& v, int form, int64_t r, int b) {
-    return ((r >> 4) * v.sc + (b >> 4)) * (256 * form_pieces(form)) + mx_lane(r, b) * 4 + (b >> 2 & 3);
+template <int F>
+__device__ inline uint8_t* block8(const MxView& m, int64_t r, int b, int i) {
+    return m.codes + (r * m.sc * 4 + (b >> 2)) * chunk_bytes(F) + 64 * form_pieces(F) + 32 * i + (b & 3) * 8;
+}
+template <int F>
+__device__ inline uint8_t* block_scale_at(const MxView& m, int64_t r, int b, int i) {
+    if constexpr (F == kWeights)
+        return m.scales + ((r >> 4) * m.sc + (b >> 4)) * 256 + ((b & 3) * 16 + (int)(r & 15)) * 4 + (b >> 2 & 3);
+    else
+        return m.scales + (r * m.sc + (b >> 4)) * scale_bytes(F) + 16 * i + (b & 3) * 4 + (b >> 2 & 3);
 }
 
 // ------------------------------------------------------------ encoding
@@ -82,7 +105,7 @@ template <int F>
 __device__ inline int mx_exponent(float a) {
     constexpr int kTop = F == kMx8 ? 0 : 2;
     // mantissa bits of 7/4, 7.75/4 and 127.5/64
-    constexpr uint32_t kBorder = F == kMx4 ? 0x600000u : F == kMx6 ? 0x780000u : 0x7f0000u;
+    constexpr uint32_t kBorder = F == kMx4 || F == kWeights ? 0x600000u : F == kMx6 ? 0x780000u : 0x7f0000u;
     const uint32_t u = __float_as_uint(a);
     const int e = (int)(u >> 23) - 127 - kTop + ((u & 0x7fffffu) > kBorder ? 1 : 0);
     return min(max(e, kMinScaleExp), kMaxScaleExp);
@@ -128,27 +151,25 @@ __device__ inline void store_octet24(uint32_t bits, int p, uint8_t* at16, uint8_
     if (p < 6) *reinterpret_cast<uint32_t*>(p < 4 ? at16 + 4 * p : at8 + 4 * (p - 4)) = w;
 }
 
-// Block b of slot r, held by 8 consecutive lanes (p = 0..7, values 4p .. 4p + 3;
+// Block b of row r, held by 8 consecutive lanes (p = 0..7, values 4p .. 4p + 3;
 // all active), goes to the buffer.
 template <int F>
 __device__ inline void store_octet(const MxView& m, int64_t r, int b, int p, const float (&v)[4]) {
     const float a = octet_max(v);
     const bool nan = !(a <= __FLT_MAX__);
     const int e = nan ? 0 : mx_exponent<F>(a);
-    uint8_t* c = m.codes + mx_code_offset(m, F, r, b);
-    const int l = mx_lane(r, b);
-    if constexpr (F == kMx4) {
+    if constexpr (F == kMx4 || F == kWeights) {
         uint32_t q = 0;
         if (!nan) {
             q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[0], v[1], exp2_int(e), 0);
             q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[2], v[3], exp2_int(e), 1);
         }
-        *reinterpret_cast<uint16_t*>(c + 16 * l + 2 * p) = (uint16_t)q;
+        *reinterpret_cast<uint16_t*>(block16<F>(m, r, b, 0) + 2 * p) = (uint16_t)q;
     } else if constexpr (F == kMx6) {
         uint32_t q = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) q |= (nan ? 0u : mx6_code(v[i], e)) << (6 * i);
-        store_octet24(q, p, c + 16 * l, c + 1024 + 8 * l);
+        store_octet24(q, p, block16<F>(m, r, b, 0), block8<F>(m, r, b, 0));
     } else {
         uint32_t low = 0, high = 0;
 #pragma unroll
@@ -158,16 +179,15 @@ __device__ inline void store_octet(const MxView& m, int64_t r, int b, int p, con
             low |= (s | (n & 15u)) << (6 * i);
             high |= (s | n >> 4) << (6 * i);
         }
-        store_octet24(low, p, c + 16 * l, c + 1024 + 8 * l);
-        store_octet24(high, p, c + 1536 + 16 * l, c + 1536 + 1024 + 8 * l);
+        store_octet24(low, p, block16<F>(m, r, b, 0), block8<F>(m, r, b, 0));
+        store_octet24(high, p, block16<F>(m, r, b, 1), block8<F>(m, r, b, 1));
     }
     if (p == 0) {
-        uint8_t* s = m.scales + mx_scale_offset(m, F, r, b);
         if constexpr (F == kMx8) {
-            s[0] = (uint8_t)(nan ? kNanScaleByte : e + 127 - 3);
-            s[256] = (uint8_t)(nan ? kNanScaleByte : e + 127 + 1);
+            *block_scale_at<F>(m, r, b, 0) = (uint8_t)(nan ? kNanScaleByte : e + 127 - 3);
+            *block_scale_at<F>(m, r, b, 1) = (uint8_t)(nan ? kNanScaleByte : e + 127 + 1);
         } else {
-            s[0] = (uint8_t)(nan ? kNanScaleByte : e + 127);
+            *block_scale_at<F>(m, r, b, 0) = (uint8_t)(nan ? kNanScaleByte : e + 127);
         }
     }
 }
@@ -176,7 +196,7 @@ __device__ inline void store_octet(const MxView& m, int64_t r, int b, int p, con
 // Shapes and pointers are validated by the caller.
 
 hipError_t launch_mx_quantize(const float* X, int64_t x_stride, int64_t n_rows, const MxView& v, int form,
-                              bool pad_rows, hipStream_t st);
+                              hipStream_t st);  // kWeights: all rows and the padding
 hipError_t launch_mx4_import(const uint8_t* codes, const uint8_t* scales, const MxView& v, hipStream_t st);
 hipError_t launch_mx4_export(const MxView& v, uint8_t* codes, uint8_t* scales, hipStream_t st);
 hipError_t launch_mx_read(const MxView& v, int form, const int32_t* batch_index, int64_t n_rows, float* X,
@@ -196,6 +216,7 @@ struct MxProduct {
     int activation;
 };
 hipError_t launch_mx_product(const MxProduct& p, hipStream_t st);
+hipError_t launch_mx_wide(const MxProduct& p, hipStream_t st);  // q8_mx_prompt.hip
 
 struct NormView {
     const float* weight;

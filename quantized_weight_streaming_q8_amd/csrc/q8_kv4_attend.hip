@@ -70,6 +70,7 @@
 // head after the other: 31.6 us for 16 sessions up to 8192 against 30.2, 51.6 for
 // 64 tokens against 49.2).
 
+#include "q8_lds.h"
 #include "q8_kv4_internal.h"
 #include "q8_kv4_shares.h"
 
@@ -151,28 +152,8 @@ __host__ __device__ constexpr int scale_loads(int nb) {
 }
 __host__ __device__ constexpr int slot_bytes(int nb) { return group_ks(nb) + 256 * scale_loads(nb); }
 
-__device__ inline uint32_t lds_address(const void* p) {
-    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
-}
-
-// 64 lanes x 16 (4) bytes from base + voff to the LDS bytes from `lds` on.  Read
-// once, past the caches' retention (16 sessions near 32768 positions, the loads
-// alone: 95 us against 109 without the hint).
-__device__ inline void lds_load16(uint32_t lds, const uint8_t* base, uint32_t voff) {
-    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt" ::"v"(voff), "s"(base), "{m0}"(lds)
-                 : "memory");
-}
-__device__ inline void lds_load4(uint32_t lds, const uint8_t* base, uint32_t voff) {
-    asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(base), "{m0}"(lds)
-                 : "memory");
-}
-// At most N loads (and stores) still on their way.
-template <int N>
-__device__ inline void wait_loads() {
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-// LDS reads into registers are done: what they read may be overwritten.
-__device__ inline void wait_lds_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+// Groups are read once, past the caches' retention (16 sessions near 32768
+// positions, the loads alone: 95 us against 109 without the hint).
 
 template <int NB>
 constexpr int kGroupLoads = NB + scale_loads(NB);
@@ -180,7 +161,7 @@ constexpr int kGroupLoads = NB + scale_loads(NB);
 template <int NB>
 __device__ inline void load_group(uint32_t lds, const uint8_t* group, int lane) {
 #pragma unroll
-    for (int i = 0; i < NB; ++i) lds_load16(lds + i * 1024, group + i * 1024, lane * 16);
+    for (int i = 0; i < NB; ++i) lds_load16_once(lds + i * 1024, group + i * 1024, lane * 16);
     // lanes past the end repeat the last word
 #pragma unroll
     for (int i = 0; i < scale_loads(NB); ++i)

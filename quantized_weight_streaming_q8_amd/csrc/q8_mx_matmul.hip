@@ -13,15 +13,10 @@
 
 #include <utility>
 
-#include "q8_ffn_internal.h"
+#include "q8_mx_mfma.h"
 
 namespace q8 {
 namespace {
-
-typedef int v8i __attribute__((ext_vector_type(8)));
-typedef float v4f __attribute__((ext_vector_type(4)));
-typedef uint32_t v4u __attribute__((ext_vector_type(4)));
-typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
 constexpr int kMaxWaves = 16;
 
@@ -31,49 +26,13 @@ struct Weights {
     uint32_t s;
 };
 
-// One chunk of 16 tokens.
+// The chunk of a slot's row from `row` on, for lane quarter g.
 template <int F>
-struct Tokens {
-    v4u a[form_pieces(F)];
-    v2u b[form_pieces(F)];
-};
-
-template <int F>
-__device__ inline void load_tokens(Tokens<F>& x, const uint8_t* codes, uint32_t at16, uint32_t at8) {
+__device__ inline void load_tokens(Tokens<F>& x, const uint8_t* row, int g) {
 #pragma unroll
     for (int i = 0; i < form_pieces(F); ++i) {
-        x.a[i] = *reinterpret_cast<const v4u*>(codes + at16 + i * 1536);
-        if constexpr (F != kMx4) x.b[i] = *reinterpret_cast<const v2u*>(codes + at8 + i * 1536);
-    }
-}
-
-// Chunk J of a super-chunk.
-template <int F, int J>
-__device__ inline v4f multiply(v4u w, uint32_t ws, const Tokens<F>& x, const uint32_t (&xs)[2], v4f c) {
-    const v8i a = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < form_pieces(F); ++i) {
-        if constexpr (F == kMx4) {
-            const v8i b = {(int)x.a[i][0], (int)x.a[i][1], (int)x.a[i][2], (int)x.a[i][3], 0, 0, 0, 0};
-            c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, J, (int)ws, J, (int)xs[i]);
-        } else {
-            const v8i b = {(int)x.a[i][0], (int)x.a[i][1], (int)x.a[i][2], (int)x.a[i][3],
-                           (int)x.b[i][0], (int)x.b[i][1], 0, 0};
-            c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 2, J, (int)ws, J, (int)xs[i]);
-        }
-    }
-    return c;
-}
-
-__device__ inline float activate(float x, int kind) {
-    switch (kind) {
-        case Q8_ACT_SILU: return x / (1.0f + expf(-x));
-        case Q8_ACT_GELU: return 0.5f * x * erfcf(-0.70710678118654752440f * x);
-        case Q8_ACT_GELU_TANH:
-            return x / (1.0f + expf(-1.5957691216057307f * (x + 0.044715f * x * x * x)));
-        case Q8_ACT_RELU: return x > 0.0f ? x : x == x ? 0.0f : x;
-        case Q8_ACT_SIGMOID: return 1.0f / (1.0f + expf(-x));
-        default: return x;
+        x.a[i] = *reinterpret_cast<const v4u*>(row + 64 * i + 16 * g);
+        if constexpr (F != kMx4) x.b[i] = *reinterpret_cast<const v2u*>(row + 64 * form_pieces(F) + 32 * i + 8 * g);
     }
 }
 
@@ -103,27 +62,22 @@ mx_narrow_kernel(NarrowArgs n) {
             const float zero[4] = {0.f, 0.f, 0.f, 0.f};
             for (int i = threadIdx.x; i < live * 8; i += blockDim.x) {
                 const int64_t t = t0 + (i >> 3);
-                if (p.out_form == kMx4) store_octet<kMx4>(p.out, t, blockIdx.x, i & 7, zero);
-                else if (p.out_form == kMx6) store_octet<kMx6>(p.out, t, blockIdx.x, i & 7, zero);
-                else store_octet<kMx8>(p.out, t, blockIdx.x, i & 7, zero);
+                store_octet_as(p.out_form, p.out, t, blockIdx.x, i & 7, zero);
             }
             return;
         }
     }
 
-    // this lane's token in each tile, and where its slot lies
-    uint32_t at16[T], at8[T], at_s[T];
+    // this lane's token in each tile, and where its row lies
+    uint32_t row[T], srow[T];
 #pragma unroll
     for (int t = 0; t < T; ++t) {
         const int tok = t0 + t * 16 + (lane & 15);
         int64_t s = 0;
         if (tok < p.n_live) s = p.batch_index ? p.batch_index[tok] : tok;
         if (s < 0 || s >= p.x.rows) s = 0;  // its row is overwritten with NaN below
-        const uint32_t l = (uint32_t)(lane & 48) + (uint32_t)(s & 15);
-        const uint32_t tile = (uint32_t)(s >> 4);
-        at16[t] = tile * (uint32_t)kc * form_chunk_bytes(F) + l * 16;
-        at8[t] = tile * (uint32_t)kc * form_chunk_bytes(F) + 1024 + l * 8;
-        at_s[t] = tile * (uint32_t)sc * (256 * form_pieces(F)) + l * 4;
+        row[t] = (uint32_t)s * (uint32_t)(sc * 4 * chunk_bytes(F));
+        srow[t] = (uint32_t)s * (uint32_t)(sc * scale_bytes(F));
     }
     const uint8_t* wc[R];
     const uint8_t* ws[R];
@@ -154,21 +108,20 @@ mx_narrow_kernel(NarrowArgs n) {
                     w[r].c[j] = __builtin_nontemporal_load(
                         reinterpret_cast<const v4u*>(wc[r] + (uint32_t)(4 * i + j) * 1024u + lane * 16));
         }
-        uint32_t xs[T][2];
+        uint32_t xs[T][form_pieces(F)];
 #pragma unroll
         for (int t = 0; t < T; ++t)
 #pragma unroll
             for (int k = 0; k < form_pieces(F); ++k)
                 xs[t][k] = *reinterpret_cast<const uint32_t*>(
-                    p.x.scales + at_s[t] + (uint32_t)i * (256 * form_pieces(F)) + 256 * k);
+                    p.x.scales + srow[t] + (uint32_t)i * scale_bytes(F) + 16 * k + (lane >> 4) * 4);
         const auto chunk = [&](auto J) {
             constexpr int j = decltype(J)::value;
             if (j >= chunks) return;
 #pragma unroll
             for (int t = 0; t < T; ++t) {
                 Tokens<F> x;
-                const uint32_t o = (uint32_t)(4 * i + j) * form_chunk_bytes(F);
-                load_tokens<F>(x, p.x.codes, at16[t] + o, at8[t] + o);
+                load_tokens<F>(x, p.x.codes + (row[t] + (uint32_t)(4 * i + j) * chunk_bytes(F)), lane >> 4);
 #pragma unroll
                 for (int r = 0; r < R; ++r) acc[r][t] = multiply<F, j>(w[r].c[j], w[r].s, x, xs[t], acc[r][t]);
             }
@@ -222,9 +175,7 @@ mx_narrow_kernel(NarrowArgs n) {
             if constexpr (U == 2) {
                 if (p.out.codes != nullptr) {
                     const float v[4] = {y[0], y[1], y[2], y[3]};
-                    if (p.out_form == kMx4) store_octet<kMx4>(p.out, tok, blockIdx.x, part, v);
-                    else if (p.out_form == kMx6) store_octet<kMx6>(p.out, tok, blockIdx.x, part, v);
-                    else store_octet<kMx8>(p.out, tok, blockIdx.x, part, v);
+                    store_octet_as(p.out_form, p.out, tok, blockIdx.x, part, v);
                 }
             }
         }
@@ -233,7 +184,7 @@ mx_narrow_kernel(NarrowArgs n) {
 
 template <int F, int T, int U, int P>
 hipError_t launch_narrow(const NarrowArgs& n, hipStream_t st) {
-    const int64_t groups = mx_tiles(n.p.w.rows);
+    const int64_t groups = weight_groups(n.p.w.rows);
     int64_t blocks = (groups + U - 1) / U;
     if (n.p.out.codes != nullptr) blocks = n.pad_blocks;
     const size_t lds = (size_t)n.waves * P * U * 1024;
@@ -262,6 +213,7 @@ hipError_t narrow_tiles(const NarrowArgs& n, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_mx_product(const MxProduct& p, hipStream_t st) {
+    if (p.n_live > 64) return launch_mx_wide(p, st);
     NarrowArgs n;
     n.p = p;
     n.per = (p.w.sc + kMaxWaves - 1) / kMaxWaves;

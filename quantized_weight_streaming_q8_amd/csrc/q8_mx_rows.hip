@@ -53,8 +53,8 @@ mx4_import_kernel(const uint4* __restrict__ codes, const uint8_t* __restrict__ s
         q = codes[r * blocks + b];
         s = scales[r * blocks + b];
     }
-    *reinterpret_cast<uint4*>(m.codes + chunk * 1024 + l * 16) = q;
-    m.scales[mx_scale_offset(m, kMx4, r, b)] = s;
+    *reinterpret_cast<uint4*>(block16<kWeights>(m, r, b, 0)) = q;
+    *block_scale_at<kWeights>(m, r, b, 0) = s;
 }
 
 __global__ void __launch_bounds__(kThreads)
@@ -63,8 +63,8 @@ mx4_export_kernel(MxView m, int64_t total, uint4* __restrict__ codes, uint8_t* _
     if (tid >= total) return;
     const int64_t blocks = m.K / 32, r = tid / blocks;
     const int b = (int)(tid - r * blocks);
-    codes[tid] = *reinterpret_cast<const uint4*>(m.codes + mx_code_offset(m, kMx4, r, b) + 16 * mx_lane(r, b));
-    scales[tid] = m.scales[mx_scale_offset(m, kMx4, r, b)];
+    codes[tid] = *reinterpret_cast<const uint4*>(block16<kWeights>(m, r, b, 0));
+    scales[tid] = *block_scale_at<kWeights>(m, r, b, 0);
 }
 
 // The value of a 6-bit code (sign, 2 exponent, 3 mantissa bits).
@@ -100,12 +100,10 @@ mx_read_kernel(MxView m, const int32_t* __restrict__ batch_index, int64_t total,
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = __builtin_nanf("");
     } else {
-        const uint8_t* c = m.codes + mx_code_offset(m, F, r, b);
-        const int l = mx_lane(r, b);
-        const int s = m.scales[mx_scale_offset(m, F, r, b)];
+        const int s = *block_scale_at<F>(m, r, b, 0);
         const bool nan = s == kNanScaleByte;
         if constexpr (F == kMx4) {
-            const uint32_t w = *reinterpret_cast<const uint16_t*>(c + 16 * l + 2 * p);
+            const uint32_t w = *reinterpret_cast<const uint16_t*>(block16<F>(m, r, b, 0) + 2 * p);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint32_t n = w >> (4 * i) & 7u;
@@ -113,12 +111,12 @@ mx_read_kernel(MxView m, const int32_t* __restrict__ batch_index, int64_t total,
                 v[i] = ldexpf(w >> (4 * i) & 8u ? -x : x, s - 127);
             }
         } else if constexpr (F == kMx6) {
-            const uint32_t w = load_octet24(c + 16 * l, c + 1024 + 8 * l, p);
+            const uint32_t w = load_octet24(block16<F>(m, r, b, 0), block8<F>(m, r, b, 0), p);
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = ldexpf(mx6_value(w >> (6 * i) & 63u), s - 127);
         } else {
-            const uint32_t w = load_octet24(c + 16 * l, c + 1024 + 8 * l, p);
-            const uint32_t h = load_octet24(c + 1536 + 16 * l, c + 1536 + 1024 + 8 * l, p);
+            const uint32_t w = load_octet24(block16<F>(m, r, b, 0), block8<F>(m, r, b, 0), p);
+            const uint32_t h = load_octet24(block16<F>(m, r, b, 1), block8<F>(m, r, b, 1), p);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float n = (float)((h >> (6 * i) & 31u) * 16u + (w >> (6 * i) & 31u));
@@ -147,19 +145,20 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 }  // namespace
 
 hipError_t launch_mx_quantize(const float* X, int64_t x_stride, int64_t n_rows, const MxView& v, int form,
-                              bool pad_rows, hipStream_t st) {
-    const int64_t rows = pad_rows ? mx_tiles(v.rows) * 16 : n_rows;  // zeros past the matrix
+                              hipStream_t st) {
+    const int64_t rows = form == kWeights ? weight_groups(v.rows) * 16 : n_rows;  // zeros past the matrix
     const int64_t total = rows * v.kc * 4 * 8;
     const bool vec = aligned16(X) && x_stride % 4 == 0;
     const dim3 g(grid_for(total)), b(kThreads);
-    if (form == kMx4) mx_quantize_kernel<kMx4><<<g, b, 0, st>>>(X, x_stride, n_rows, total, v, vec);
+    if (form == kWeights) mx_quantize_kernel<kWeights><<<g, b, 0, st>>>(X, x_stride, n_rows, total, v, vec);
+    else if (form == kMx4) mx_quantize_kernel<kMx4><<<g, b, 0, st>>>(X, x_stride, n_rows, total, v, vec);
     else if (form == kMx6) mx_quantize_kernel<kMx6><<<g, b, 0, st>>>(X, x_stride, n_rows, total, v, vec);
     else mx_quantize_kernel<kMx8><<<g, b, 0, st>>>(X, x_stride, n_rows, total, v, vec);
     return hipGetLastError();
 }
 
 hipError_t launch_mx4_import(const uint8_t* codes, const uint8_t* scales, const MxView& v, hipStream_t st) {
-    const int64_t total = mx_tiles(v.rows) * v.kc * 64;
+    const int64_t total = weight_groups(v.rows) * v.kc * 64;
     mx4_import_kernel<<<dim3(grid_for(total)), dim3(kThreads), 0, st>>>(reinterpret_cast<const uint4*>(codes), scales,
                                                                         total, v);
     return hipGetLastError();

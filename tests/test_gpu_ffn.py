@@ -170,15 +170,6 @@ def test_weights_pack_import_and_export(q8, n, k):
     assert torch.equal(c, codes) and torch.equal(s, scales)
 
 
-def test_an_mx4_buffer_is_a_packed_matrix(q8):
-    x = rows(10, 40, 352)
-    w, a = q8.MX4Weights(40, 352), q8.Acts(48, 352, "mx4")
-    q8.q8_mx4_pack_weights(to_dev(x), w)
-    q8.q8_mx_quantize_acts(to_dev(x), 40, a)
-    as_acts = q8.Acts(40, 352, "mx4", data=w.data)
-    assert same(values(q8, as_acts), values(q8, a, n=40))
-
-
 # ------------------------------------------------------------------ product
 
 def integer_case(seed, form, n, k, slots):
