@@ -42,8 +42,8 @@ bool valid_stride(int64_t stride, int64_t least, int64_t rows) {
     return stride >= least && stride <= kMaxSpan / rows;
 }
 
-q8::MxView view(const q8_mx4_weights* w) { return q8::weights_view(w->data, w->N, w->K); }
-q8::MxView view(const q8_acts* a) { return q8::acts_view(a->data, a->n_slots, a->K, a->format); }
+q8::MxView view(const q8_mx4_weights* w) { return q8::mx_view(w->data, w->N, w->K, q8::kMx4, true); }
+q8::MxView view(const q8_acts* a) { return q8::mx_view(a->data, a->n_slots, a->K, a->format, q8::acts_in_tiles(a->n_slots)); }
 
 // What a product and the gated block have in common.
 bool valid_product(const q8_mx4_weights* w, const q8_acts* x, const int32_t* batch_index, int n_live) {
@@ -74,17 +74,17 @@ extern "C" {
 size_t q8_acts_bytes(int32_t n_slots, int64_t K, int32_t format) {
     if (format == Q8_ACTS_Q8_0) return q8_act_buffer_bytes_n(K, n_slots);
     if (!valid_mx_shape(n_slots, K, format)) return 0;
-    return (size_t)q8::acts_bytes(n_slots, K, format);
+    return (size_t)q8::mx_bytes(n_slots, K, format, q8::acts_in_tiles(n_slots));
 }
 
 size_t q8_mx4_weight_bytes(int64_t N, int64_t K) {
-    return valid_weight_shape(N, K) ? (size_t)q8::weight_bytes(N, K) : 0;
+    return valid_weight_shape(N, K) ? (size_t)q8::mx_bytes(N, K, q8::kMx4, true) : 0;
 }
 
 q8_status q8_mx4_pack_weights(const float* W, const q8_mx4_weights* Wm, hipStream_t stream) {
     if (!valid_weights(Wm) || !aligned(W, 16)) return Q8_ERR_INVALID_ARG;
     if (!q8_device_supported()) return Q8_ERR_UNSUPPORTED;
-    return from_hip(q8::launch_mx_quantize(W, Wm->K, Wm->N, view(Wm), q8::kWeights, stream));
+    return from_hip(q8::launch_mx_quantize(W, Wm->K, Wm->N, q8::row_groups(Wm->N) * 16, view(Wm), q8::kMx4, stream));
 }
 
 q8_status q8_mx4_pack_weights_q(const uint8_t* codes, const uint8_t* scales, const q8_mx4_weights* Wm,
@@ -105,7 +105,7 @@ q8_status q8_mx_quantize_acts(const float* X, int64_t x_stride, int n_rows, cons
         !valid_stride(x_stride, Xm->K, n_rows))
         return Q8_ERR_INVALID_ARG;
     if (!q8_device_supported()) return Q8_ERR_UNSUPPORTED;
-    return from_hip(q8::launch_mx_quantize(X, x_stride, n_rows, view(Xm), Xm->format, stream));
+    return from_hip(q8::launch_mx_quantize(X, x_stride, n_rows, n_rows, view(Xm), Xm->format, stream));
 }
 
 q8_status q8_mx_read_acts(const q8_acts* Xm, const int32_t* batch_index, int n_rows, float* X, hipStream_t stream) {

@@ -6,28 +6,27 @@
 // ceil(KC / 4)), whose scale bytes a lane takes in one 4-byte load.  Lane l = 16 g
 // + r of the instruction holds block g (32 values) of row r.  Padding is zeros.
 //
-// Packed MX4 weights: in row groups of 16 rows, as the instruction's lanes take
-// them, so that a wave's load is 1 KB of consecutive bytes:
-//   codes,  1024 bytes per (group, chunk), groups outermost: lane l's 16 bytes at
-//     16 l, the even value of a byte low;
-//   scales, after all codes, 256 bytes per (group, super-chunk): lane l's byte j,
-//     at 4 l + j, is the scale of its block in chunk 4 sc + j.
-//
-// Activation buffers: a slot's row is consecutive bytes, since tokens take slots
-// in any order (a random order over the weights' layout fetched a 128-byte line for
-// each 16 bytes of 4-bit codes: 3.5 times the L2 requests over 4099 tokens).
-// Per slot and chunk
-//   MX4  64 bytes: blocks 0..3, 16 bytes each;
+// Both come in one of two orders, which differ in their strides only:
+//   tiles (weights; buffers of up to kTileSlots slots): 16 rows side by side, as
+//     the instruction's lanes take them, so that a wave's load is 1 KB of consecutive
+//     bytes.  Tiles outermost, then chunks.
+//   rows (larger buffers): a slot's row is consecutive bytes, since tokens take
+//     slots in any order and a tile's 16 bytes of each would be a line each: 4099
+//     tokens in a random order fetched 3.5 times as many 128-byte lines from tiles, and
+//     the product took 152 us against 98.  Within a tile any order is the same lines: for
+//     16 tokens 8.0 us against 13.4.
+// Per row and chunk, in the order of rows (times 16 in tiles):
+//   MX4  64 bytes: blocks 0..3, 16 bytes each, the even value of a byte low;
 //   MX6  96: the first 16 of each block's 24 bytes (32 codes of 6 bits, in order),
-//        then the other 8 of each;
+//        then the other 8, blocks in pairs;
 //   MX8  192: two pieces.  An integer q = +-(16 h + l), h 0..8, l 0..15, is held as the
 //        6-bit codes of l / 8 (first) and h / 8, whose code is the number itself, so that
 //        both enter the instruction as MX6 does, with the scales 2^(e - 3) and 2^(e + 1)
 //        for elements q / 64 * 2^e.  16 bytes of each block's first piece, of each
-//        block's second, then 8 bytes of them, in the same order.
-// Rows are padded to whole super-chunks (a multiple of 128 bytes).  After all
-// codes, per slot and super-chunk 16 scale bytes for each piece: byte 4 g + j is block
-// g of chunk j.
+//        block's second, then each block's 8 bytes of the one and of the other.
+// After all codes, per row and super-chunk 16 scale bytes for each piece: byte 4 g + j is
+// block g of chunk j.  Rows in the order of rows are padded to whole super-chunks (a
+// multiple of 128 bytes).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -38,64 +37,76 @@
 
 namespace q8 {
 
-enum Form { kQ80 = Q8_ACTS_Q8_0, kMx4 = Q8_ACTS_MX4, kMx6 = Q8_ACTS_MX6, kMx8 = Q8_ACTS_MX8, kWeights = 4 };
+enum Form { kQ80 = Q8_ACTS_Q8_0, kMx4 = Q8_ACTS_MX4, kMx6 = Q8_ACTS_MX6, kMx8 = Q8_ACTS_MX8 };
 
 constexpr int kMxChunk = 128;   // columns of a matrix instruction
+constexpr int kTileSlots = 64;  // slots of the largest buffer in tiles
 constexpr int kNanScaleByte = 255;
 constexpr int kMinScaleExp = -120, kMaxScaleExp = 125;
 
 __host__ __device__ constexpr int form_pieces(int f) { return f == kMx8 ? 2 : 1; }
-// Bytes of a slot's chunk, and of its scales in a super-chunk.
+// Bytes of a row's chunk, and of its scales in a super-chunk.
 __host__ __device__ constexpr int chunk_bytes(int f) { return f == kMx4 ? 64 : 96 * form_pieces(f); }
 __host__ __device__ constexpr int scale_bytes(int f) { return 16 * form_pieces(f); }
 
-// An MX buffer or packed weights as the kernels take them.
+// An MX buffer or packed weights (form MX4) as the kernels take them.
 struct MxView {
     uint8_t* codes;
     uint8_t* scales;
     int64_t rows, K;
-    int32_t kc, sc;  // chunks and super-chunks of a row
+    int32_t kc, sc;        // chunks and super-chunks of a row
+    int32_t side;          // rows side by side: 16 in tiles, 1 in rows
+    // bytes from a row to the next of its 16, and from 16 rows to the next 16
+    uint32_t row, tile, scale_row, scale_tile;
 };
 
 inline int64_t mx_chunks(int64_t K) { return (K + kMxChunk - 1) / kMxChunk; }
 inline int64_t mx_supers(int64_t K) { return (mx_chunks(K) + 3) / 4; }
-inline int64_t weight_groups(int64_t N) { return (N + 15) / 16; }
-inline int64_t weight_bytes(int64_t N, int64_t K) {
-    return weight_groups(N) * (mx_chunks(K) * 1024 + mx_supers(K) * 256);
+inline int64_t row_groups(int64_t rows) { return (rows + 15) / 16; }
+inline int64_t mx_code_bytes(int64_t rows, int64_t K, int form, bool tiles) {
+    return tiles ? row_groups(rows) * mx_chunks(K) * 16 * chunk_bytes(form)
+                 : (rows * mx_supers(K) * 4 * chunk_bytes(form) + 255) / 256 * 256;
 }
-inline int64_t acts_code_bytes(int64_t slots, int64_t K, int form) {
-    return (slots * mx_supers(K) * 4 * chunk_bytes(form) + 255) / 256 * 256;
+inline int64_t mx_bytes(int64_t rows, int64_t K, int form, bool tiles) {
+    return mx_code_bytes(rows, K, form, tiles) +
+           (tiles ? row_groups(rows) * 16 : rows) * mx_supers(K) * scale_bytes(form);
 }
-inline int64_t acts_bytes(int64_t slots, int64_t K, int form) {
-    return acts_code_bytes(slots, K, form) + slots * mx_supers(K) * scale_bytes(form);
+inline MxView mx_view(void* data, int64_t rows, int64_t K, int form, bool tiles) {
+    MxView v;
+    v.codes = static_cast<uint8_t*>(data);
+    v.scales = v.codes + mx_code_bytes(rows, K, form, tiles);
+    v.rows = rows;
+    v.K = K;
+    v.kc = (int32_t)mx_chunks(K);
+    v.sc = (int32_t)mx_supers(K);
+    v.side = tiles ? 16 : 1;
+    v.row = tiles ? 16 : (uint32_t)(v.sc * 4 * chunk_bytes(form));
+    v.tile = tiles ? (uint32_t)(v.kc * 16 * chunk_bytes(form)) : 16 * v.row;
+    v.scale_row = tiles ? 4 : (uint32_t)(v.sc * scale_bytes(form));
+    v.scale_tile = tiles ? (uint32_t)(v.sc * 16 * scale_bytes(form)) : 16 * v.scale_row;
+    return v;
 }
-inline MxView weights_view(void* data, int64_t N, int64_t K) {
-    uint8_t* p = static_cast<uint8_t*>(data);
-    return {p, p + weight_groups(N) * mx_chunks(K) * 1024, N, K, (int32_t)mx_chunks(K), (int32_t)mx_supers(K)};
-}
-inline MxView acts_view(void* data, int64_t slots, int64_t K, int form) {
-    uint8_t* p = static_cast<uint8_t*>(data);
-    return {p, p + acts_code_bytes(slots, K, form), slots, K, (int32_t)mx_chunks(K), (int32_t)mx_supers(K)};
-}
+inline bool acts_in_tiles(int64_t n_slots) { return n_slots <= kTileSlots; }
 
 // Block b of row r: its 16 bytes of piece i, its 8 bytes of piece i, its scale.
 template <int F>
+__device__ inline int64_t chunk_at(const MxView& m, int64_t r, int b) {
+    return (r >> 4) * m.tile + (int64_t)(r & 15) * m.row + (int64_t)(b >> 2) * chunk_bytes(F) * m.side;
+}
+template <int F>
 __device__ inline uint8_t* block16(const MxView& m, int64_t r, int b, int i) {
-    if constexpr (F == kWeights)
-        return m.codes + ((r >> 4) * m.kc + (b >> 2)) * 1024 + ((b & 3) * 16 + (int)(r & 15)) * 16;
-    else
-        return m.codes + (r * m.sc * 4 + (b >> 2)) * chunk_bytes(F) + 64 * i + (b & 3) * 16;
+    return m.codes + chunk_at<F>(m, r, b) + (64 * i + (b & 3) * 16) * m.side;
 }
 template <int F>
 __device__ inline uint8_t* block8(const MxView& m, int64_t r, int b, int i) {
-    return m.codes + (r * m.sc * 4 + (b >> 2)) * chunk_bytes(F) + 64 * form_pieces(F) + 32 * i + (b & 3) * 8;
+    // 16 bytes hold a block's two pieces (MX8) or those of two blocks (MX6)
+    const int k = F == kMx8 ? 2 * (b & 3) + i : b & 3;
+    return m.codes + chunk_at<F>(m, r, b) + (64 * form_pieces(F) + (k >> 1) * 16) * m.side + (k & 1) * 8;
 }
 template <int F>
 __device__ inline uint8_t* block_scale_at(const MxView& m, int64_t r, int b, int i) {
-    if constexpr (F == kWeights)
-        return m.scales + ((r >> 4) * m.sc + (b >> 4)) * 256 + ((b & 3) * 16 + (int)(r & 15)) * 4 + (b >> 2 & 3);
-    else
-        return m.scales + (r * m.sc + (b >> 4)) * scale_bytes(F) + 16 * i + (b & 3) * 4 + (b >> 2 & 3);
+    return m.scales + (r >> 4) * m.scale_tile + (int64_t)(r & 15) * m.scale_row +
+           ((int64_t)(b >> 4) * scale_bytes(F) + 16 * i + (b & 3) * 4) * m.side + (b >> 2 & 3);
 }
 
 // ------------------------------------------------------------ encoding
@@ -105,7 +116,7 @@ template <int F>
 __device__ inline int mx_exponent(float a) {
     constexpr int kTop = F == kMx8 ? 0 : 2;
     // mantissa bits of 7/4, 7.75/4 and 127.5/64
-    constexpr uint32_t kBorder = F == kMx4 || F == kWeights ? 0x600000u : F == kMx6 ? 0x780000u : 0x7f0000u;
+    constexpr uint32_t kBorder = F == kMx4 ? 0x600000u : F == kMx6 ? 0x780000u : 0x7f0000u;
     const uint32_t u = __float_as_uint(a);
     const int e = (int)(u >> 23) - 127 - kTop + ((u & 0x7fffffu) > kBorder ? 1 : 0);
     return min(max(e, kMinScaleExp), kMaxScaleExp);
@@ -158,7 +169,7 @@ __device__ inline void store_octet(const MxView& m, int64_t r, int b, int p, con
     const float a = octet_max(v);
     const bool nan = !(a <= __FLT_MAX__);
     const int e = nan ? 0 : mx_exponent<F>(a);
-    if constexpr (F == kMx4 || F == kWeights) {
+    if constexpr (F == kMx4) {
         uint32_t q = 0;
         if (!nan) {
             q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[0], v[1], exp2_int(e), 0);
@@ -195,8 +206,9 @@ __device__ inline void store_octet(const MxView& m, int64_t r, int b, int p, con
 // ------------------------------------------------------------- launchers
 // Shapes and pointers are validated by the caller.
 
-hipError_t launch_mx_quantize(const float* X, int64_t x_stride, int64_t n_rows, const MxView& v, int form,
-                              hipStream_t st);  // kWeights: all rows and the padding
+// Rows from n_rows to out_rows become zeros.
+hipError_t launch_mx_quantize(const float* X, int64_t x_stride, int64_t n_rows, int64_t out_rows, const MxView& v,
+                              int form, hipStream_t st);
 hipError_t launch_mx4_import(const uint8_t* codes, const uint8_t* scales, const MxView& v, hipStream_t st);
 hipError_t launch_mx4_export(const MxView& v, uint8_t* codes, uint8_t* scales, hipStream_t st);
 hipError_t launch_mx_read(const MxView& v, int form, const int32_t* batch_index, int64_t n_rows, float* X,

@@ -7,222 +7,294 @@
 //
 // One v_mfma_scale_f32_16x16x128_f8f6f4 takes 16 rows of weights (4-bit codes
 // as they lie in memory, 16 bytes a lane, their scale bytes as its scale operand) and
-// 16 tokens.  A workgroup owns U row groups of 16 rows (of each projection)
-// and all tokens; its waves share out the super-chunks of 512 columns and meet
-// in LDS, where they are added in order: the tree depends on K alone.
+// 16 tokens.  A workgroup's waves share out the super-chunks of 512 columns, so that
+// every token's chunk is fetched once by a workgroup, and go through pairs of row groups
+// (a gate's and the up projection's, or two neighbours), the next pair's weights on
+// their way while one is multiplied.  The waves' sums meet in LDS, where they are added
+// in order: the tree depends on K alone.
 
+#include <algorithm>
 #include <utility>
 
+#include "q8_lds.h"
 #include "q8_mx_mfma.h"
 
 namespace q8 {
 namespace {
 
-constexpr int kMaxWaves = 16;
 
 // A super-chunk of one row group: 4 chunks of codes and their scales.
 struct Weights {
-    v4u c[4];
+    v4u c0, c1, c2, c3;
     uint32_t s;
 };
+template <int J>
+__device__ inline v4u chunk_of(const Weights& w) {
+    return J == 0 ? w.c0 : J == 1 ? w.c1 : J == 2 ? w.c2 : w.c3;
+}
 
 // The chunk of a slot's row from `row` on, for lane quarter g.
 template <int F>
-__device__ inline void load_tokens(Tokens<F>& x, const uint8_t* row, int g) {
-#pragma unroll
-    for (int i = 0; i < form_pieces(F); ++i) {
-        x.a[i] = *reinterpret_cast<const v4u*>(row + 64 * i + 16 * g);
-        if constexpr (F != kMx4) x.b[i] = *reinterpret_cast<const v2u*>(row + 64 * form_pieces(F) + 32 * i + 8 * g);
+__device__ inline void load_tokens(Tokens& x, const uint8_t* row, int side, int g) {
+    x.a0 = *reinterpret_cast<const v4u*>(row + 16 * g * side);
+    if constexpr (F == kMx8) x.a1 = *reinterpret_cast<const v4u*>(row + (64 + 16 * g) * side);
+    if constexpr (F == kMx8) x.b = *reinterpret_cast<const v4u*>(row + (128 + 16 * g) * side);
+    if constexpr (F == kMx6) {
+        const v2u b = *reinterpret_cast<const v2u*>(row + (64 + 16 * (g >> 1)) * side + 8 * (g & 1));
+        x.b = v4u{b[0], b[1], 0u, 0u};
     }
 }
+
+constexpr int kMaxWaves = 12;  // three a SIMD: 168 registers each
 
 struct NarrowArgs {
     MxProduct p;
     int waves, per;  // waves, super-chunks of a wave
-    int out_blocks;  // with quantised rows: blocks of 32 features, and of the padded row
-    int pad_blocks;
+    int pairs;       // of row groups
+    int span;        // pairs that a workgroup takes together: 2 for a block of 32 features
 };
 
-// U row groups of each of P projections, T tiles of 16 tokens.
-template <int F, int T, int U, int P>
-__global__ void __launch_bounds__(kMaxWaves * 64)
+// T tiles of 16 tokens; P projections (2: the gated block).  Kept: super-chunks of a
+// wave whose tokens stay in registers (0: they are fetched with every pair).
+template <int F, int T, int P, int Kept>
+__global__ void __launch_bounds__(Kept == 2 ? 512 : kMaxWaves * 64)
 mx_narrow_kernel(NarrowArgs n) {
-    extern __shared__ v4f lds[];  // [waves][P * U][64 lanes]
-    constexpr int R = P * U;
+    extern __shared__ v4f lds[];  // [2][waves][2][64 lanes], [64]
+    constexpr int PI = form_pieces(F);
+    static_assert(Kept == 0 || T == 1, "a tile stays in registers");
     const MxProduct& p = n.p;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int t0 = (int)blockIdx.y * 64;
-    const int live = min(p.n_live - t0, 16 * T);
-    const int64_t group0 = (int64_t)blockIdx.x * U;
-    const int64_t groups = (p.w.rows + 15) / 16;
-    const int kc = p.w.kc, sc = p.w.sc;
-
-    if constexpr (U == 2) {
-        if (p.out.codes != nullptr && (int)blockIdx.x >= n.out_blocks) {  // padding of the quantised rows
-            const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int i = threadIdx.x; i < live * 8; i += blockDim.x) {
-                const int64_t t = t0 + (i >> 3);
-                store_octet_as(p.out_form, p.out, t, blockIdx.x, i & 7, zero);
-            }
-            return;
-        }
-    }
+    const int groups = (int)((p.w.rows + 15) / 16);
+    const int kc = p.w.kc, sc = p.w.sc, side = p.x.side;
 
     // this lane's token in each tile, and where its row lies
+    int slot[T];
     uint32_t row[T], srow[T];
+    bool outside[T];  // such a token's row is overwritten with NaN
 #pragma unroll
     for (int t = 0; t < T; ++t) {
-        const int tok = t0 + t * 16 + (lane & 15);
-        int64_t s = 0;
-        if (tok < p.n_live) s = p.batch_index ? p.batch_index[tok] : tok;
-        if (s < 0 || s >= p.x.rows) s = 0;  // its row is overwritten with NaN below
-        row[t] = (uint32_t)s * (uint32_t)(sc * 4 * chunk_bytes(F));
-        srow[t] = (uint32_t)s * (uint32_t)(sc * scale_bytes(F));
+        const int tok = t * 16 + (lane & 15);
+        slot[t] = tok >= p.n_live ? 0 : p.batch_index ? p.batch_index[tok] : tok;
     }
-    const uint8_t* wc[R];
-    const uint8_t* ws[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const MxView& w = r < U ? p.w : p.wu;
-        const int64_t g = min(group0 + r % U, groups - 1);
-        wc[r] = w.codes + g * kc * 1024;
-        ws[r] = w.scales + g * sc * 256;
-    }
-
-    v4f acc[R][T];
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int t = 0; t < T; ++t) acc[r][t] = v4f{0.f, 0.f, 0.f, 0.f};
+    // Chunks past the last are the last again: read, and not multiplied.
+    const auto load_chunk = [&](Tokens& x, int t, int c) {
+        load_tokens<F>(x, p.x.codes + (row[t] + (uint32_t)min(c, kc - 1) * (chunk_bytes(F) * side)), side, lane >> 4);
+    };
+    const auto load_scales = [&](Scales& s, int t, int i) {
+        const uint8_t* at = p.x.scales + srow[t] + ((uint32_t)i * scale_bytes(F) + (lane >> 4) * 4) * side;
+        s.s0 = *reinterpret_cast<const uint32_t*>(at);
+        if constexpr (F == kMx8) s.s1 = *reinterpret_cast<const uint32_t*>(at + 16 * side);
+    };
+    // Super-chunk i of one row group of pair b.
+    const auto load_weights = [&](Weights& w, int r, int b, int i) {
+        const MxView& m = P == 2 && r == 1 ? p.wu : p.w;
+        const int64_t g = P == 2 ? b : min(2 * b + r, groups - 1);
+        w.s = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(m.scales + (g * sc + i) * 256 + lane * 4));
+        const uint8_t* c = m.codes + g * kc * 1024 + lane * 16;
+        w.c0 = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(c + (4 * i) * 1024));
+        w.c1 = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(c + min(4 * i + 1, kc - 1) * 1024));
+        w.c2 = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(c + min(4 * i + 2, kc - 1) * 1024));
+        w.c3 = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(c + min(4 * i + 3, kc - 1) * 1024));
+    };
+    const auto pair_of = [&](int round) {
+        return ((int)blockIdx.x + (int)gridDim.x * (round / n.span)) * n.span + round % n.span;
+    };
 
     const int s0 = wave * n.per, s1 = min(sc, s0 + n.per);
-    for (int i = s0; i < s1; ++i) {
-        Weights w[R];
-        const int chunks = min(4, kc - 4 * i);
+    Weights w0, w1;
+    int b = pair_of(0);
+    load_weights(w0, 0, b, s0);
+    load_weights(w1, 1, b, s0);
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            w[r].s = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(ws[r] + i * 256 + lane * 4));
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (j < chunks)
-                    w[r].c[j] = __builtin_nontemporal_load(
-                        reinterpret_cast<const v4u*>(wc[r] + (uint32_t)(4 * i + j) * 1024u + lane * 16));
-        }
-        uint32_t xs[T][form_pieces(F)];
-#pragma unroll
-        for (int t = 0; t < T; ++t)
-#pragma unroll
-            for (int k = 0; k < form_pieces(F); ++k)
-                xs[t][k] = *reinterpret_cast<const uint32_t*>(
-                    p.x.scales + srow[t] + (uint32_t)i * scale_bytes(F) + 16 * k + (lane >> 4) * 4);
-        const auto chunk = [&](auto J) {
-            constexpr int j = decltype(J)::value;
-            if (j >= chunks) return;
-#pragma unroll
-            for (int t = 0; t < T; ++t) {
-                Tokens<F> x;
-                load_tokens<F>(x, p.x.codes + (row[t] + (uint32_t)(4 * i + j) * chunk_bytes(F)), lane >> 4);
-#pragma unroll
-                for (int r = 0; r < R; ++r) acc[r][t] = multiply<F, j>(w[r].c[j], w[r].s, x, xs[t], acc[r][t]);
-            }
-        };
-        chunk(std::integral_constant<int, 0>());
-        chunk(std::integral_constant<int, 1>());
-        chunk(std::integral_constant<int, 2>());
-        chunk(std::integral_constant<int, 3>());
-    }
-
-    // one tile of tokens after the other: the waves' sums meet in LDS
     for (int t = 0; t < T; ++t) {
-        if (t > 0) __syncthreads();
+        outside[t] = slot[t] < 0 || slot[t] >= p.x.rows;
+        const uint32_t s = outside[t] ? 0u : (uint32_t)slot[t];
+        row[t] = (s >> 4) * p.x.tile + (s & 15) * p.x.row;
+        srow[t] = (s >> 4) * p.x.scale_tile + (s & 15) * p.x.scale_row;
+    }
+    constexpr int kKept = Kept > 0 ? Kept : 1;
+    Tokens kept[kKept][4];
+    Scales xs[kKept][T];
+    if constexpr (Kept > 0) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            v4f a = acc[r][0];
+        for (int i = 0; i < Kept; ++i) {
+            const int from = min(s0 + i, sc - 1);
+            load_scales(xs[i][0], 0, from);
 #pragma unroll
-            for (int u = 1; u < T; ++u)
-                if (u == t) a = acc[r][u];
-            lds[(wave * R + r) * 64 + lane] = a;
+            for (int j = 0; j < 4; ++j) load_chunk(kept[i][j], 0, 4 * from + j);
         }
-        __syncthreads();
-        // a thread: 4 consecutive features of one token
-        for (int i = threadIdx.x; i < U * 64; i += blockDim.x) {
-            const int part = i & (4 * U - 1), c = i / (4 * U);
-            const int u = part >> 2, at = (part & 3) * 16 + c;
-            const int tok = t0 + t * 16 + c;
-            v4f y = lds[u * 64 + at];
-            for (int w = 1; w < n.waves; ++w) y += lds[(w * R + u) * 64 + at];
-            if constexpr (P == 2) {
-                v4f z = lds[(U + u) * 64 + at];
-                for (int w = 1; w < n.waves; ++w) z += lds[(w * R + U + u) * 64 + at];
+    }
+    for (int round = 0; b < n.pairs; ++round) {
+        v4f acc[2][T];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) y[k] = activate(y[k], p.activation) * z[k];
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int t = 0; t < T; ++t) acc[r][t] = v4f{0.f, 0.f, 0.f, 0.f};
+        const int next = pair_of(round + 1);
+        // the next super-chunk's weights, past the end these again
+        const auto load_next = [&](int i, Weights& t0, Weights& t1) {
+            const bool here = i + 1 < s1, last = next >= n.pairs;
+            const int nb = here || last ? b : next, ni = here ? i + 1 : last ? i : s0;
+            load_weights(t0, 0, nb, ni);
+            load_weights(t1, 1, nb, ni);
+        };
+        if constexpr (Kept > 0) {
+#pragma unroll
+            for (int k = 0; k < Kept; ++k) {
+                const int i = s0 + k;
+                if (i >= s1) break;
+                Weights t0, t1;
+                load_next(i, t0, t1);
+                const auto chunk = [&](auto J) {
+                    constexpr int j = decltype(J)::value;
+                    if (j > 0 && 4 * i + j >= kc) return;
+                    acc[0][0] = multiply<F, j>(chunk_of<j>(w0), w0.s, kept[k][j], xs[k][0], acc[0][0]);
+                    acc[1][0] = multiply<F, j>(chunk_of<j>(w1), w1.s, kept[k][j], xs[k][0], acc[1][0]);
+                };
+                chunk(std::integral_constant<int, 0>());
+                chunk(std::integral_constant<int, 1>());
+                chunk(std::integral_constant<int, 2>());
+                chunk(std::integral_constant<int, 3>());
+                w0 = t0;
+                w1 = t1;
             }
-            if (tok >= p.n_live) continue;  // whole octets: one token's
-            if (p.batch_index) {
-                const int s = p.batch_index[tok];
-                if (s < 0 || s >= p.x.rows) y = v4f{1.f, 1.f, 1.f, 1.f} * __builtin_nanf("");
+        } else {
+            for (int i = s0; i < s1; ++i) {
+                Weights t0, t1;
+                load_next(i, t0, t1);
+#pragma unroll
+                for (int t = 0; t < T; ++t) load_scales(xs[0][t], t, i);
+                const auto chunk = [&](auto J) {
+                    constexpr int j = decltype(J)::value;
+                    if (j > 0 && 4 * i + j >= kc) return;
+                    Tokens x[T];
+#pragma unroll
+                    for (int t = 0; t < T; ++t) load_chunk(x[t], t, 4 * i + j);
+#pragma unroll
+                    for (int t = 0; t < T; ++t) {
+                        acc[0][t] = multiply<F, j>(chunk_of<j>(w0), w0.s, x[t], xs[0][t], acc[0][t]);
+                        acc[1][t] = multiply<F, j>(chunk_of<j>(w1), w1.s, x[t], xs[0][t], acc[1][t]);
+                    }
+                };
+                chunk(std::integral_constant<int, 0>());
+                chunk(std::integral_constant<int, 1>());
+                chunk(std::integral_constant<int, 2>());
+                chunk(std::integral_constant<int, 3>());
+                w0 = t0;
+                w1 = t1;
             }
-            const int64_t f = group0 * 16 + part * 4;
-            if (p.Y != nullptr && f < p.w.rows) {
-                float* o = p.Y + tok * p.y_stride + f;
-                if (f + 4 <= p.w.rows && (reinterpret_cast<uintptr_t>(o) & 15) == 0) {
-                    *reinterpret_cast<v4f*>(o) = y;
-                } else {
-                    for (int k = 0; k < 4; ++k)
-                        if (f + k < p.w.rows) o[k] = y[k];
+        }
+
+        // One tile of tokens after the other: the waves' sums meet in LDS, in its two
+        // halves in turn, so that one barrier a tile is enough; what is on its way from
+        // memory stays on its way.
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            v4f* half = lds + ((round * T + t) & 1) * (n.waves * 128);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) half[(wave * 2 + r) * 64 + lane] = acc[r][t];
+            wait_lds_reads();
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            // a thread: 4 consecutive features of one token (c, quarter g); waves in turn
+            constexpr int kShares = P == 2 ? 1 : 2;
+#pragma unroll
+            for (int v = 0; v < kShares; ++v) {
+                if ((round * T * kShares + t * kShares + v) % n.waves != wave) continue;
+                v4f y = half[v * 64 + lane];
+                for (int k = 1; k < n.waves; ++k) y += half[(k * 2 + v) * 64 + lane];
+                if constexpr (P == 2) {
+                    v4f z = half[64 + lane];
+                    for (int k = 1; k < n.waves; ++k) z += half[(k * 2 + 1) * 64 + lane];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) y[k] = activate(y[k], p.activation) * z[k];
+                }
+                const int tok = t * 16 + (lane & 15);
+                if (outside[t]) y = v4f{1.f, 1.f, 1.f, 1.f} * __builtin_nanf("");
+                const int64_t f = ((int64_t)b * kShares + v) * 16 + (lane >> 4) * 4;
+                if (tok < p.n_live && p.Y != nullptr && f < p.w.rows) {
+                    float* o = p.Y + tok * p.y_stride + f;
+                    if (f + 4 <= p.w.rows && (reinterpret_cast<uintptr_t>(o) & 15) == 0) {
+                        *reinterpret_cast<v4f*>(o) = y;
+                    } else {
+                        for (int k = 0; k < 4; ++k)
+                            if (f + k < p.w.rows) o[k] = y[k];
+                    }
+                }
+                if constexpr (P == 2) {
+                    // blocks of 32 features: two pairs' results, by 8 lanes a token
+                    if (p.out.codes == nullptr) continue;
+                    v4f* even = lds + 2 * (n.waves * 128) + t * 64;
+                    if ((b & 1) == 0) {
+                        even[lane] = y;  // another wave's after the next barrier
+                    } else {
+                        v4f* odd = lds + 2 * (n.waves * 128) + T * 64;
+                        odd[lane] = y;
+                        wait_lds_reads();
+                        for (int h = 0; h < 2; ++h) {
+                            const int c = h * 8 + (lane >> 3), part = lane & 7;
+                            const v4f q = (part < 4 ? even : odd)[(part & 3) * 16 + c];
+                            if (t * 16 + c >= p.n_live) continue;
+                            const float x[4] = {q[0], q[1], q[2], q[3]};
+                            store_octet_as(p.out_form, p.out, t * 16 + c, b >> 1, part, x);
+                        }
+                    }
                 }
             }
-            if constexpr (U == 2) {
-                if (p.out.codes != nullptr) {
-                    const float v[4] = {y[0], y[1], y[2], y[3]};
-                    store_octet_as(p.out_form, p.out, tok, blockIdx.x, part, v);
-                }
-            }
         }
+        b = next;
+    }
+    if constexpr (P == 2) {  // the padding of the quantised rows
+        if (p.out.codes == nullptr || blockIdx.x != 0) return;
+        const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+        const int blocks = (int)(p.w.rows / 32), each = (p.out.kc * 4 - blocks) * 8;
+        for (int i = threadIdx.x; i < p.n_live * each; i += blockDim.x)
+            store_octet_as(p.out_form, p.out, i / each, blocks + i % each / 8, i & 7, zero);
     }
 }
 
-template <int F, int T, int U, int P>
+template <int F, int T, int P, int Kept>
 hipError_t launch_narrow(const NarrowArgs& n, hipStream_t st) {
-    const int64_t groups = weight_groups(n.p.w.rows);
-    int64_t blocks = (groups + U - 1) / U;
-    if (n.p.out.codes != nullptr) blocks = n.pad_blocks;
-    const size_t lds = (size_t)n.waves * P * U * 1024;
-    mx_narrow_kernel<F, T, U, P><<<dim3((unsigned)blocks, (unsigned)((n.p.n_live + 63) / 64)), dim3(n.waves * 64), lds,
-                                   st>>>(n);
+    const size_t lds = (size_t)n.waves * 4096 + (P == 2 ? (T + 1) * 1024 : 0);
+    const int grid = std::min((n.pairs + n.span - 1) / n.span, 256);
+    mx_narrow_kernel<F, T, P, Kept><<<dim3((unsigned)grid), dim3(n.waves * 64), lds, st>>>(n);
     return hipGetLastError();
 }
 
-template <int F, int T>
-hipError_t narrow_shape(const NarrowArgs& n, hipStream_t st) {
-    if (n.p.wu.codes == nullptr) return launch_narrow<F, T, 1, 1>(n, st);
-    if (n.p.out.codes != nullptr) return launch_narrow<F, T, 2, 2>(n, st);
-    return launch_narrow<F, T, 1, 2>(n, st);
+template <int F, int P>
+hipError_t narrow_tiles(const NarrowArgs& n, hipStream_t st) {
+    switch ((n.p.n_live + 15) / 16) {
+        case 1:
+            if (n.per == 1) return launch_narrow<F, 1, P, 1>(n, st);
+            if (n.per == 2 && n.waves <= 8) return launch_narrow<F, 1, P, 2>(n, st);
+            return launch_narrow<F, 1, P, 0>(n, st);
+        case 2: return launch_narrow<F, 2, P, 0>(n, st);
+        case 3: return launch_narrow<F, 3, P, 0>(n, st);
+        default: return launch_narrow<F, 4, P, 0>(n, st);
+    }
 }
 
 template <int F>
-hipError_t narrow_tiles(const NarrowArgs& n, hipStream_t st) {
-    switch (n.p.n_live > 48 ? 4 : (n.p.n_live + 15) / 16) {
-        case 1: return narrow_shape<F, 1>(n, st);
-        case 2: return narrow_shape<F, 2>(n, st);
-        case 3: return narrow_shape<F, 3>(n, st);
-        default: return narrow_shape<F, 4>(n, st);
-    }
+hipError_t narrow_form(const NarrowArgs& n, hipStream_t st) {
+    return n.p.wu.codes != nullptr ? narrow_tiles<F, 2>(n, st) : narrow_tiles<F, 1>(n, st);
 }
 
 }  // namespace
 
 hipError_t launch_mx_product(const MxProduct& p, hipStream_t st) {
-    if (p.n_live > 64) return launch_mx_wide(p, st);
+    if (p.n_live > 16) return launch_mx_wide(p, st);
     NarrowArgs n;
     n.p = p;
-    n.per = (p.w.sc + kMaxWaves - 1) / kMaxWaves;
+    // one super-chunk a wave; from 13 to 16 two, whose tokens still fit the registers of
+    // a wave when there are at most 8; above that as few as 12 waves need
+    n.per = p.w.sc <= kMaxWaves ? 1 : p.w.sc <= 16 ? 2 : (p.w.sc + kMaxWaves - 1) / kMaxWaves;
     n.waves = (p.w.sc + n.per - 1) / n.per;
-    n.out_blocks = (int)(p.w.rows / 32);
-    n.pad_blocks = p.out.kc * 4;
-    if (p.form == kMx4) return narrow_tiles<kMx4>(n, st);
-    if (p.form == kMx6) return narrow_tiles<kMx6>(n, st);
-    return narrow_tiles<kMx8>(n, st);
+    const int groups = (int)row_groups(p.w.rows);
+    n.pairs = p.wu.codes != nullptr ? groups : (groups + 1) / 2;
+    n.span = p.out.codes != nullptr ? 2 : 1;
+    if (p.form == kMx4) return narrow_form<kMx4>(n, st);
+    if (p.form == kMx6) return narrow_form<kMx6>(n, st);
+    return narrow_form<kMx8>(n, st);
 }
 
 }  // namespace q8

@@ -11,29 +11,34 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
-// One chunk (128 columns) of 16 tokens.
-template <int F>
+// One chunk (128 columns) of 16 tokens, and the scale bytes of a super-chunk's:
+// two pieces for MX8.  Members of their own, since arrays end up in scratch memory here.
 struct Tokens {
-    v4u a[form_pieces(F)];
-    v2u b[form_pieces(F)];  // not for MX4
+    v4u a0, a1;
+    v4u b;  // the last 8 bytes of each piece; not for MX4
+};
+struct Scales {
+    uint32_t s0, s1;
 };
 
-// c += chunk J of a super-chunk: 16 rows of weights (codes w, scale bytes ws)
-// times 16 tokens (x, scale bytes xs).
-template <int F, int J>
-__device__ inline v4f multiply(v4u w, uint32_t ws, const Tokens<F>& x, const uint32_t (&xs)[form_pieces(F)], v4f c) {
-    const v8i a = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < form_pieces(F); ++i) {
-        if constexpr (F == kMx4) {
-            const v8i b = {(int)x.a[i][0], (int)x.a[i][1], (int)x.a[i][2], (int)x.a[i][3], 0, 0, 0, 0};
-            c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, J, (int)ws, J, (int)xs[i]);
-        } else {
-            const v8i b = {(int)x.a[i][0], (int)x.a[i][1], (int)x.a[i][2], (int)x.a[i][3],
-                           (int)x.b[i][0], (int)x.b[i][1], 0, 0};
-            c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 2, J, (int)ws, J, (int)xs[i]);
-        }
+template <int Fmt, int J>
+__device__ inline v4f multiply_piece(v4u w, uint32_t ws, v4u a, uint32_t b0, uint32_t b1, uint32_t xs, v4f c) {
+    const v8i x = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
+    if constexpr (Fmt == 4) {
+        const v8i y = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, J, (int)ws, J, (int)xs);
+    } else {
+        const v8i y = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b0, (int)b1, 0, 0};
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 2, J, (int)ws, J, (int)xs);
     }
+}
+
+// c += chunk J of a super-chunk: 16 rows of weights (codes w, scale bytes ws)
+// times 16 tokens.
+template <int F, int J>
+__device__ inline v4f multiply(v4u w, uint32_t ws, const Tokens& x, const Scales& xs, v4f c) {
+    c = multiply_piece<F == kMx4 ? 4 : 2, J>(w, ws, x.a0, x.b[0], x.b[1], xs.s0, c);
+    if constexpr (F == kMx8) c = multiply_piece<2, J>(w, ws, x.a1, x.b[2], x.b[3], xs.s1, c);
     return c;
 }
 

@@ -1,8 +1,8 @@
 // q8_mx_prompt.hip -- products of MX4 weights with MX activations, and the gated
 // block, for many tokens: bound by the matrix cores.
 //
-// A workgroup of 8 waves makes a tile of 16 TN rows x 16 TT tokens, waves 2 x 4,
-// each with 8 x 4 of the instruction's 16 x 16 tiles in registers.  Operands go from memory to
+// A workgroup of 8 waves, WN x WT, makes a tile of 16 WN RN rows x 16 WT RT tokens, each
+// wave RN x RT of the instruction's 16 x 16 tiles in registers.  Operands go from memory to
 // LDS past the registers, a chunk of 128 columns a stage, in the order in which the
 // instruction takes them (no bank conflicts, no address arithmetic); a stage is
 // loaded D stages ahead, so that its latency hides behind the products.
@@ -16,25 +16,28 @@
 namespace q8 {
 namespace {
 
-constexpr int kWaves = 8, kWaveN = 2, kWaveT = 4;
-constexpr int kTileN = 16;  // row groups of a tile: of both projections together
+constexpr int kWaves = 8;
 
-// RT: token tiles of a wave.
-template <int F, int RT>
-struct Stage {
-    static constexpr int RN = kTileN / kWaveN;
-    static constexpr int TT = RT * kWaveT;          // token tiles of a workgroup
+// The shape of a workgroup's tile.
+template <int F, int WN, int WT, int RN, int RT>
+struct Tile {
+    static_assert(WN * WT == kWaves, "waves");
+    static constexpr int TN = WN * RN, TT = WT * RT;  // row groups (of both projections together), token tiles
     static constexpr int PI = form_pieces(F);
-    static constexpr int kCb = 16 * chunk_bytes(F);   // a chunk of 16 tokens
-    static constexpr int kBytes = kTileN * 1024 + TT * kCb;
-    static constexpr int kScaleItems = kTileN + TT * PI;  // 256 bytes each, a super-chunk
-    static constexpr int kScaleLoads = (kScaleItems + 4 * kWaves - 1) / (4 * kWaves);
+    // 1 KB loads of the tokens: 16-byte parts of each piece, 8-byte parts of a tile's two
+    // pieces or of two tiles (MX6)
+    static constexpr int kParts16 = TT * PI, kParts8 = F == kMx4 ? 0 : F == kMx6 ? (TT + 1) / 2 : TT;
+    static constexpr int kTokens = kParts16 + kParts8;
+    static constexpr int kBytes = (TN + kTokens) * 1024;  // a stage
+    static constexpr int kScales = TN + TT * PI;          // 256-byte loads a super-chunk
     // loads of a wave for a stage
-    static constexpr int kLoads = kTileN / kWaves + TT * kCb / 1024 / kWaves + kScaleLoads;
-    static constexpr int kFit = (160 * 1024 - 2 * kScaleItems * 256) / kBytes;
+    static constexpr int kLoadN = (TN + kWaves - 1) / kWaves, kLoadT = (kTokens + kWaves - 1) / kWaves;
+    static constexpr int kLoadS = (kScales + 4 * kWaves - 1) / (4 * kWaves);
+    static constexpr int kLoads = kLoadN + kLoadT + kLoadS;
+    static constexpr int kFit = (160 * 1024 - 2 * kScales * 256) / kBytes;
     static constexpr int kStages = kFit > 4 ? 4 : kFit;
-    static constexpr int kLds = kStages * kBytes + 2 * kScaleItems * 256;
-    static_assert(TT % kWaves == 0 && RT % (TT / kWaves) == 0 && kStages >= 2, "tile");
+    static constexpr int kLds = kStages * kBytes + 2 * kScales * 256;
+    static_assert(kStages >= 2, "two stages");
 };
 
 struct WideArgs {
@@ -44,11 +47,11 @@ struct WideArgs {
 };
 
 // P: projections (2: the gated block; a wave then has RN / 2 row groups of each).
-template <int F, int RT, int P>
+template <int F, int WN, int WT, int RN, int RT, int P>
 __global__ void __launch_bounds__(kWaves * 64, 2)
 mx_wide_kernel(WideArgs n) {
-    using S = Stage<F, RT>;
-    constexpr int RN = S::RN, TT = S::TT, PI = S::PI, D = S::kStages - 1;
+    using S = Tile<F, WN, WT, RN, RT>;
+    constexpr int TN = S::TN, TT = S::TT, PI = S::PI, D = S::kStages - 1;
     __shared__ __attribute__((aligned(256))) uint8_t lds[S::kLds];
     const MxProduct& p = n.p;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -63,59 +66,62 @@ mx_wide_kernel(WideArgs n) {
     const int t0 = tt * 16 * TT;
     const int kc = p.w.kc, sc = p.w.sc;
     const int groups = (int)((p.w.rows + 15) / 16);
-    const int wn = wave & (kWaveN - 1), wt = wave / kWaveN;
+    const int wn = wave % WN, wt = wave / WN;
+    const uint32_t side = p.x.side;
 
     // Row group i of the tile: P = 2 gives each row wave RN/2 of the gate's and
     // RN/2 of the up projection's.
     const auto group_of = [&](int i) {
-        const int g = P == 1 ? nt * kTileN + i : nt * (kTileN / 2) + i / RN * (RN / 2) + i % (RN / 2);
+        const int g = P == 1 ? nt * TN + i : nt * (TN / 2) + i / RN * (RN / 2) + i % (RN / 2);
         return min(g, groups - 1);
     };
     const auto weights_of = [&](int i) -> const MxView& { return P == 2 && i % RN >= RN / 2 ? p.wu : p.w; };
-    const auto slot_of = [&](int tile, int i) {
-        const int tok = t0 + tile * 16 + i;
+    const auto slot_of = [&](int tile) {  // of this lane's token
+        const int tok = t0 + tile * 16 + (lane & 15);
         int64_t s = 0;
         if (tok < p.n_live) s = p.batch_index ? p.batch_index[tok] : tok;
         return s >= 0 && s < p.x.rows ? (uint32_t)s : 0u;  // another's row becomes NaN at the end
     };
-    const auto row_of = [&](int tile, int i) { return slot_of(tile, i) * (uint32_t)(sc * 4 * chunk_bytes(F)); };
-    // what this wave loads: TN/8 row groups, TT/8 token tiles, its part of the scales
-    const uint8_t* wbase[kTileN / kWaves];
+
+    // What this wave loads.  A load too many repeats the last one's, to the same place.
+    const uint8_t* wbase[S::kLoadN];
 #pragma unroll
-    for (int i = 0; i < kTileN / kWaves; ++i) {
-        const int r = wave * (kTileN / kWaves) + i;
-        wbase[i] = weights_of(r).codes + (int64_t)group_of(r) * kc * 1024;
+    for (int m = 0; m < S::kLoadN; ++m) {
+        const int r = min(wave + kWaves * m, TN - 1);
+        wbase[m] = weights_of(r).codes + (int64_t)group_of(r) * kc * 1024;
     }
-    // Token tiles, in LDS the 16-byte parts [piece][block][token] and, for a pair of
-    // pieces or (MX6) of tiles, the 8-byte parts [pair][half][token][2 blocks].
-    constexpr int kTiles = TT / kWaves;  // of a wave
-    uint32_t at[kTiles], at8[kTiles];
+    // Tokens: in LDS the 16-byte parts [tile][piece][block][token], then the 8-byte parts in
+    // 16 bytes, [tile][block][token][piece] or (MX6) [tile][half][token][2 blocks].
+    uint32_t at[S::kLoadT];
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) at[i] = row_of(wave * kTiles + i, lane & 15) + (lane >> 4) * 16;
-    if constexpr (F != kMx4) {
-        static_assert(F == kMx8 || kTiles % 2 == 0, "8-byte parts in pairs");
-#pragma unroll
-        for (int i = 0; i < kTiles / (3 - PI); ++i)
-            at8[i] = row_of(wave * kTiles + (F == kMx8 ? i : 2 * i + (lane >> 5)), lane & 15) + 64 * PI +
-                     (F == kMx8 ? (lane >> 5) * 32 : 0) + (lane >> 4 & 1) * 16;
+    for (int m = 0; m < S::kLoadT; ++m) {
+        const int item = min(wave + kWaves * m, S::kTokens - 1);
+        const bool wide = item < S::kParts16;
+        const int e = item - S::kParts16;
+        const int tile = wide ? item / PI : F == kMx6 ? min(2 * e + (lane >> 5), TT - 1) : e;
+        const uint32_t s = slot_of(tile);
+        const uint32_t in = wide ? 64 * (item % PI) + (lane >> 4) * 16
+                                 : 64 * PI + (F == kMx6 ? lane >> 4 & 1 : lane >> 4) * 16;
+        at[m] = (s >> 4) * p.x.tile + (s & 15) * p.x.row + in * side;
     }
-    const uint8_t* sbase[4][S::kScaleLoads];
-    uint32_t sat[4][S::kScaleLoads];
-    uint32_t sstep[4][S::kScaleLoads];
+    const uint8_t* sbase[4][S::kLoadS];
+    uint32_t sat[4][S::kLoadS];
+    uint32_t sstep[4][S::kLoadS];
 #pragma unroll
     for (int q = 0; q < 4; ++q)
 #pragma unroll
-        for (int m = 0; m < S::kScaleLoads; ++m) {
-            const int item = min(q * kWaves + wave + 4 * kWaves * m, S::kScaleItems - 1);
-            if (item < kTileN) {
+        for (int m = 0; m < S::kLoadS; ++m) {
+            const int item = min(q * kWaves + wave + 4 * kWaves * m, S::kScales - 1);
+            if (item < TN) {
                 sbase[q][m] = weights_of(item).scales + (int64_t)group_of(item) * sc * 256;
                 sat[q][m] = lane * 4;
                 sstep[q][m] = 256;
             } else {
-                const int tile = (item - kTileN) / PI, piece = (item - kTileN) % PI;
-                sbase[q][m] = p.x.scales + piece * 16;
-                sat[q][m] = slot_of(tile, lane & 15) * (uint32_t)(sc * scale_bytes(F)) + (lane >> 4) * 4;
-                sstep[q][m] = scale_bytes(F);
+                const int tile = (item - TN) / PI, piece = (item - TN) % PI;
+                const uint32_t s = slot_of(tile);
+                sbase[q][m] = p.x.scales + piece * 16 * side;
+                sat[q][m] = (s >> 4) * p.x.scale_tile + (s & 15) * p.x.scale_row + (lane >> 4) * 4 * side;
+                sstep[q][m] = scale_bytes(F) * side;
             }
         }
     const uint32_t lds0 = lds_address(lds), scales0 = lds0 + S::kStages * S::kBytes;
@@ -124,9 +130,9 @@ mx_wide_kernel(WideArgs n) {
         constexpr int q = decltype(Q)::value;
         const int from = min(c, sc - 1);
 #pragma unroll
-        for (int m = 0; m < S::kScaleLoads; ++m) {
-            const int item = min(q * kWaves + wave + 4 * kWaves * m, S::kScaleItems - 1);
-            lds_load4(scales0 + ((c & 1) * S::kScaleItems + item) * 256, sbase[q][m] + (int64_t)from * sstep[q][m],
+        for (int m = 0; m < S::kLoadS; ++m) {
+            const int item = min(q * kWaves + wave + 4 * kWaves * m, S::kScales - 1);
+            lds_load4(scales0 + ((c & 1) * S::kScales + item) * 256, sbase[q][m] + (int64_t)from * sstep[q][m],
                       sat[q][m]);
         }
     };
@@ -136,18 +142,12 @@ mx_wide_kernel(WideArgs n) {
         const uint32_t to = lds0 + stage * S::kBytes;
         const int from = min(c, kc - 1);
 #pragma unroll
-        for (int i = 0; i < kTileN / kWaves; ++i)
-            lds_load16(to + (wave * (kTileN / kWaves) + i) * 1024, wbase[i] + (int64_t)from * 1024, lane * 16);
-        const uint8_t* src = p.x.codes + (int64_t)from * chunk_bytes(F);
-        const uint32_t tiles = to + kTileN * 1024 + wave * kTiles * S::kCb;
+        for (int m = 0; m < S::kLoadN; ++m)
+            lds_load16(to + min(wave + kWaves * m, TN - 1) * 1024, wbase[m] + (int64_t)from * 1024, lane * 16);
+        const uint8_t* src = p.x.codes + (int64_t)from * (chunk_bytes(F) * side);
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i) {
-#pragma unroll
-            for (int k = 0; k < PI; ++k) lds_load16(tiles + i * 1024 * PI + k * 1024, src + k * 64, at[i]);
-            if constexpr (F == kMx8) lds_load16(tiles + kTiles * 2048 + i * 1024, src, at8[i]);
-            if constexpr (F == kMx6)
-                if (i & 1) lds_load16(tiles + kTiles * 1024 + (i >> 1) * 1024, src, at8[i >> 1]);
-        }
+        for (int m = 0; m < S::kLoadT; ++m)
+            lds_load16(to + (TN + min(wave + kWaves * m, S::kTokens - 1)) * 1024, src, at[m]);
         load_scales(Q, c / 4 + 1);
     };
 
@@ -156,7 +156,8 @@ mx_wide_kernel(WideArgs n) {
     for (int r = 0; r < RN; ++r)
 #pragma unroll
         for (int t = 0; t < RT; ++t) acc[r][t] = v4f{0.f, 0.f, 0.f, 0.f};
-    uint32_t ws[RN], xs[RT][PI];
+    uint32_t ws[RN];
+    Scales xs[RT];
 
     using std::integral_constant;
     load_scales(integral_constant<int, 0>(), 0);
@@ -178,30 +179,33 @@ mx_wide_kernel(WideArgs n) {
         load_stage(integral_constant<int, (j + D) & 3>(), c + D, stage == 0 ? S::kStages - 1 : stage - 1);
         if constexpr (j == 0) {
             const uint32_t* s = reinterpret_cast<const uint32_t*>(lds + S::kStages * S::kBytes +
-                                                                  (c >> 2 & 1) * S::kScaleItems * 256);
+                                                                  (c >> 2 & 1) * S::kScales * 256);
 #pragma unroll
             for (int r = 0; r < RN; ++r) ws[r] = s[(wn * RN + r) * 64 + lane];
 #pragma unroll
-            for (int t = 0; t < RT; ++t)
-#pragma unroll
-                for (int k = 0; k < PI; ++k) xs[t][k] = s[(kTileN + (wt * RT + t) * PI + k) * 64 + lane];
+            for (int t = 0; t < RT; ++t) {
+                xs[t].s0 = s[(TN + (wt * RT + t) * PI) * 64 + lane];
+                if constexpr (F == kMx8) xs[t].s1 = s[(TN + (wt * RT + t) * PI + 1) * 64 + lane];
+            }
         }
-        const uint8_t* at = lds + stage * S::kBytes;
+        const uint8_t* here = lds + stage * S::kBytes;
         v4u a[RN];
 #pragma unroll
-        for (int r = 0; r < RN; ++r) a[r] = *reinterpret_cast<const v4u*>(at + (wn * RN + r) * 1024 + lane * 16);
+        for (int r = 0; r < RN; ++r) a[r] = *reinterpret_cast<const v4u*>(here + (wn * RN + r) * 1024 + lane * 16);
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-            Tokens<F> x;
-            // tile wt * RT + t is tile ti of wave tw's loads
-            const int tw = (wt * RT + t) / kTiles, ti = t % kTiles;
-            const uint8_t* b = at + kTileN * 1024 + tw * kTiles * S::kCb;
-#pragma unroll
-            for (int k = 0; k < PI; ++k) {
-                x.a[k] = *reinterpret_cast<const v4u*>(b + (ti * PI + k) * 1024 + lane * 16);
-                if constexpr (F != kMx4)
-                    x.b[k] = *reinterpret_cast<const v2u*>(b + kTiles * PI * 1024 + (ti * PI + k) * 512 +
-                                                           (lane >> 5) * 256 + (lane & 15) * 16 + (lane >> 4 & 1) * 8);
+            Tokens x;
+            const int tile = wt * RT + t;
+            const uint8_t* b = here + TN * 1024;
+            const uint8_t* b8 = b + S::kParts16 * 1024;
+            x.a0 = *reinterpret_cast<const v4u*>(b + tile * PI * 1024 + lane * 16);
+            if constexpr (F == kMx8) {
+                x.a1 = *reinterpret_cast<const v4u*>(b + (tile * 2 + 1) * 1024 + lane * 16);
+                x.b = *reinterpret_cast<const v4u*>(b8 + tile * 1024 + lane * 16);
+            } else if constexpr (F == kMx6) {
+                const v2u y = *reinterpret_cast<const v2u*>(b8 + tile * 512 + (lane >> 5) * 256 + (lane & 15) * 16 +
+                                                            (lane >> 4 & 1) * 8);
+                x.b = v4u{y[0], y[1], 0u, 0u};
             }
 #pragma unroll
             for (int r = 0; r < RN; ++r) acc[r][t] = multiply<F, j>(a[r], ws[r], x, xs[t], acc[r][t]);
@@ -225,7 +229,7 @@ mx_wide_kernel(WideArgs n) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) acc[r][t][k] = activate(acc[r][t][k], p.activation) * acc[r + RH][t][k];
     }
-    const int row0 = (nt * kWaveN + wn) * RH * 16 + (lane >> 4) * 4;
+    const int row0 = (nt * WN + wn) * RH * 16 + (lane >> 4) * 4;
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
         const int tok = t0 + (wt * RT + t) * 16 + (lane & 15);
@@ -253,7 +257,7 @@ mx_wide_kernel(WideArgs n) {
     if constexpr (P == 2) {
         if (p.out.codes == nullptr) return;
         // Quantised rows: through LDS to 8 lanes a block.
-        constexpr int kRow = kWaveN * RH * 16 + 4;  // floats of a token, 4 more against bank conflicts
+        constexpr int kRow = WN * RH * 16 + 4;  // floats of a token, 4 more against bank conflicts
         static_assert(TT * 16 * kRow * 4 <= S::kLds, "results fit");
         float* h = reinterpret_cast<float*>(lds);
         __syncthreads();
@@ -264,12 +268,12 @@ mx_wide_kernel(WideArgs n) {
                 *reinterpret_cast<v4f*>(h + ((wt * RT + t) * 16 + (lane & 15)) * kRow + (wn * RH + r) * 16 +
                                         (lane >> 4) * 4) = acc[r][t];
         __syncthreads();
-        constexpr int kUnits = kWaveN * RH * 4;  // of 4 values
+        constexpr int kUnits = WN * RH * 4;  // of 4 values
         const int live = min(p.n_live - t0, TT * 16);
         const int blocks = p.out.kc * 4, rows = (int)p.w.rows;
         for (int i = threadIdx.x; i < live * kUnits; i += kWaves * 64) {  // whole octets
             const int t = i / kUnits, u = i % kUnits;
-            const int f = nt * (kWaveN * RH * 16) + u * 4;
+            const int f = nt * (WN * RH * 16) + u * 4;
             if (f / 32 >= blocks) continue;
             v4f y = *reinterpret_cast<const v4f*>(h + t * kRow + u * 4);
             if (f >= rows) y = v4f{0.f, 0.f, 0.f, 0.f};  // padding
@@ -279,28 +283,36 @@ mx_wide_kernel(WideArgs n) {
     }
 }
 
-template <int F, int RT>
+template <int F, int WN, int WT, int RN, int RT>
 hipError_t launch_wide(const MxProduct& p, hipStream_t st) {
+    using S = Tile<F, WN, WT, RN, RT>;
     WideArgs n;
     n.p = p;
     const bool two = p.wu.codes != nullptr;
-    const int64_t rows = two ? kTileN * 8 : kTileN * 16;  // of a tile's results
+    const int64_t rows = S::TN * (two ? 8 : 16);  // of a tile's results
     n.n_tiles = (int)((p.w.rows + rows - 1) / rows);
-    n.t_tiles = (p.n_live + RT * kWaveT * 16 - 1) / (RT * kWaveT * 16);
+    n.t_tiles = (p.n_live + S::TT * 16 - 1) / (S::TT * 16);
     n.vec = (reinterpret_cast<uintptr_t>(p.Y) & 15) == 0 && p.y_stride % 4 == 0;
     const int64_t total = (int64_t)n.n_tiles * n.t_tiles;
     const dim3 grid((unsigned)((total + 7) / 8 * 8)), block(kWaves * 64);
-    if (two) mx_wide_kernel<F, RT, 2><<<grid, block, 0, st>>>(n);
-    else mx_wide_kernel<F, RT, 1><<<grid, block, 0, st>>>(n);
+    if (two) mx_wide_kernel<F, WN, WT, RN, RT, 2><<<grid, block, 0, st>>>(n);
+    else mx_wide_kernel<F, WN, WT, RN, RT, 1><<<grid, block, 0, st>>>(n);
     return hipGetLastError();
+}
+
+template <int F>
+hipError_t wide_shape(const MxProduct& p, hipStream_t st) {
+    if (p.n_live <= 32) return launch_wide<F, 4, 2, 4, 1>(p, st);
+    if (p.n_live <= 64) return launch_wide<F, 4, 2, 4, 2>(p, st);
+    return launch_wide<F, 2, 4, 8, 4>(p, st);
 }
 
 }  // namespace
 
 hipError_t launch_mx_wide(const MxProduct& p, hipStream_t st) {
-    if (p.form == kMx4) return launch_wide<kMx4, 4>(p, st);
-    if (p.form == kMx6) return launch_wide<kMx6, 4>(p, st);
-    return launch_wide<kMx8, 4>(p, st);
+    if (p.form == kMx4) return wide_shape<kMx4>(p, st);
+    if (p.form == kMx6) return wide_shape<kMx6>(p, st);
+    return wide_shape<kMx8>(p, st);
 }
 
 }  // namespace q8

@@ -53,8 +53,8 @@ mx4_import_kernel(const uint4* __restrict__ codes, const uint8_t* __restrict__ s
         q = codes[r * blocks + b];
         s = scales[r * blocks + b];
     }
-    *reinterpret_cast<uint4*>(block16<kWeights>(m, r, b, 0)) = q;
-    *block_scale_at<kWeights>(m, r, b, 0) = s;
+    *reinterpret_cast<uint4*>(block16<kMx4>(m, r, b, 0)) = q;
+    *block_scale_at<kMx4>(m, r, b, 0) = s;
 }
 
 __global__ void __launch_bounds__(kThreads)
@@ -63,8 +63,8 @@ mx4_export_kernel(MxView m, int64_t total, uint4* __restrict__ codes, uint8_t* _
     if (tid >= total) return;
     const int64_t blocks = m.K / 32, r = tid / blocks;
     const int b = (int)(tid - r * blocks);
-    codes[tid] = *reinterpret_cast<const uint4*>(block16<kWeights>(m, r, b, 0));
-    scales[tid] = *block_scale_at<kWeights>(m, r, b, 0);
+    codes[tid] = *reinterpret_cast<const uint4*>(block16<kMx4>(m, r, b, 0));
+    scales[tid] = *block_scale_at<kMx4>(m, r, b, 0);
 }
 
 // The value of a 6-bit code (sign, 2 exponent, 3 mantissa bits).
@@ -144,21 +144,19 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 
 }  // namespace
 
-hipError_t launch_mx_quantize(const float* X, int64_t x_stride, int64_t n_rows, const MxView& v, int form,
-                              hipStream_t st) {
-    const int64_t rows = form == kWeights ? weight_groups(v.rows) * 16 : n_rows;  // zeros past the matrix
-    const int64_t total = rows * v.kc * 4 * 8;
+hipError_t launch_mx_quantize(const float* X, int64_t x_stride, int64_t n_rows, int64_t out_rows, const MxView& v,
+                              int form, hipStream_t st) {
+    const int64_t total = out_rows * v.kc * 4 * 8;
     const bool vec = aligned16(X) && x_stride % 4 == 0;
     const dim3 g(grid_for(total)), b(kThreads);
-    if (form == kWeights) mx_quantize_kernel<kWeights><<<g, b, 0, st>>>(X, x_stride, n_rows, total, v, vec);
-    else if (form == kMx4) mx_quantize_kernel<kMx4><<<g, b, 0, st>>>(X, x_stride, n_rows, total, v, vec);
+    if (form == kMx4) mx_quantize_kernel<kMx4><<<g, b, 0, st>>>(X, x_stride, n_rows, total, v, vec);
     else if (form == kMx6) mx_quantize_kernel<kMx6><<<g, b, 0, st>>>(X, x_stride, n_rows, total, v, vec);
     else mx_quantize_kernel<kMx8><<<g, b, 0, st>>>(X, x_stride, n_rows, total, v, vec);
     return hipGetLastError();
 }
 
 hipError_t launch_mx4_import(const uint8_t* codes, const uint8_t* scales, const MxView& v, hipStream_t st) {
-    const int64_t total = weight_groups(v.rows) * v.kc * 64;
+    const int64_t total = row_groups(v.rows) * v.kc * 64;
     mx4_import_kernel<<<dim3(grid_for(total)), dim3(kThreads), 0, st>>>(reinterpret_cast<const uint4*>(codes), scales,
                                                                         total, v);
     return hipGetLastError();

@@ -46,12 +46,17 @@ def test_buffer_sizes(q8):
     assert q8.q8_mx4_weight_bytes(16, 128) == 1024 + 256
     assert q8.q8_mx4_weight_bytes(17, 544) == 2 * (5 * 1024 + 2 * 256)
     assert q8.q8_mx4_weight_bytes(7168, 5120) == 7168 * 5120 * 17 // 32
-    # a slot's row in whole super-chunks of 512 values, codes rounded up to 256 bytes, and
-    # a scale byte for each 32 values (two for MX8, which holds 12 bits a value)
-    for n, k in ((1, 32), (40, 672), (4099, 5120)):
-        wide = n * -(-k // 512) * 512
+    # up to 64 slots tiles of 16 rows, above that rows of whole super-chunks of 512 values,
+    # codes rounded up to 256 bytes; a scale byte for each 32 values (two for MX8,
+    # which holds 12 bits a value)
+    for n, k in ((1, 32), (40, 672), (64, 5120), (65, 160), (4099, 5120)):
+        wide = -(-k // 512) * 512
         for form, bits, pieces in (("mx4", 4, 1), ("mx6", 6, 1), ("mx8", 12, 2)):
-            assert q8.q8_acts_bytes(n, k, form) == -(-wide * bits // 8 // 256) * 256 + wide // 32 * pieces
+            if n <= 64:
+                rows, codes = -(-n // 16) * 16, -(-n // 16) * 16 * -(-k // 128) * 128 * bits // 8
+            else:
+                rows, codes = n, -(-n * wide * bits // 8 // 256) * 256
+            assert q8.q8_acts_bytes(n, k, form) == codes + rows * wide // 32 * pieces, (n, k, form)
     for n in (16, 32, 48, 64):
         assert q8.q8_acts_bytes(n, 5120, "q8_0") == q8.q8_act_buffer_bytes_n(5120, n)
 
