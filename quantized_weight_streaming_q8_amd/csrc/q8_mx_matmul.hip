@@ -206,8 +206,10 @@ mx_narrow_kernel(NarrowArgs n) {
                 if constexpr (P == 2) {
                     v4f z = half[64 + lane];
                     for (int k = 1; k < n.waves; ++k) z += half[(k * 2 + 1) * 64 + lane];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) y[k] = activate(y[k], p.activation) * z[k];
+                    v4f gate[1] = {y};
+                    const v4f up[1] = {z};
+                    gate_values(gate, up, p.activation);
+                    y = gate[0];
                 }
                 const int tok = t * 16 + (lane & 15);
                 if (outside[t]) y = v4f{1.f, 1.f, 1.f, 1.f} * __builtin_nanf("");

@@ -42,17 +42,41 @@ __device__ inline v4f multiply(v4u w, uint32_t ws, const Tokens& x, const Scales
     return c;
 }
 
-// Sums of several roundings each; their size is next to nothing beside the
-// products', so the plain library functions do.
-__device__ inline float activate(float x, int kind) {
+// 1 / (1 + exp(-x)) with the instructions for 2^x and 1/x, each good to a unit in the
+// last place.  A tile of 128 features and 256 tokens has 64 of these a lane: with
+// expf and a division they took 14 us of a tile's 95.  Below 2^-126 it is 0.
+__device__ inline float sigmoid(float x) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * x));
+}
+
+template <int Kind>
+__device__ inline float activate(float x) {
+    if constexpr (Kind == Q8_ACT_SILU) return x * sigmoid(x);
+    else if constexpr (Kind == Q8_ACT_GELU) return 0.5f * x * erfcf(-0.70710678118654752440f * x);
+    else if constexpr (Kind == Q8_ACT_GELU_TANH)
+        return x * sigmoid(1.5957691216057307f * (x + 0.044715f * x * x * x));
+    else if constexpr (Kind == Q8_ACT_RELU) return x > 0.0f ? x : x == x ? 0.0f : x;
+    else if constexpr (Kind == Q8_ACT_SIGMOID) return sigmoid(x);
+    else return x;
+}
+
+// gate = activation(gate) * up, 4 N values at once: one branch for all of them.
+template <int Kind, int N>
+__device__ inline void gate_with(v4f (&gate)[N], const v4f (&up)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) gate[i][k] = activate<Kind>(gate[i][k]) * up[i][k];
+}
+template <int N>
+__device__ inline void gate_values(v4f (&gate)[N], const v4f (&up)[N], int kind) {
     switch (kind) {
-        case Q8_ACT_SILU: return x / (1.0f + expf(-x));
-        case Q8_ACT_GELU: return 0.5f * x * erfcf(-0.70710678118654752440f * x);
-        case Q8_ACT_GELU_TANH:
-            return x / (1.0f + expf(-1.5957691216057307f * (x + 0.044715f * x * x * x)));
-        case Q8_ACT_RELU: return x > 0.0f ? x : x == x ? 0.0f : x;
-        case Q8_ACT_SIGMOID: return 1.0f / (1.0f + expf(-x));
-        default: return x;
+        case Q8_ACT_SILU: return gate_with<Q8_ACT_SILU>(gate, up);
+        case Q8_ACT_GELU: return gate_with<Q8_ACT_GELU>(gate, up);
+        case Q8_ACT_GELU_TANH: return gate_with<Q8_ACT_GELU_TANH>(gate, up);
+        case Q8_ACT_RELU: return gate_with<Q8_ACT_RELU>(gate, up);
+        case Q8_ACT_SIGMOID: return gate_with<Q8_ACT_SIGMOID>(gate, up);
+        default: return gate_with<Q8_ACT_IDENTITY>(gate, up);
     }
 }
 

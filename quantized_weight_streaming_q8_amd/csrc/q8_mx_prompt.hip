@@ -76,8 +76,16 @@ mx_wide_kernel(WideArgs n) {
         return min(g, groups - 1);
     };
     const auto weights_of = [&](int i) -> const MxView& { return P == 2 && i % RN >= RN / 2 ? p.wu : p.w; };
-    const auto slot_of = [&](int tile) {  // of this lane's token
-        const int tok = t0 + tile * 16 + (lane & 15);
+    // Which token and block of a tile a lane loads: 16 bytes of a token to a lane, in the
+    // order of the buffer, so that neighbours' addresses fall into one line.  In
+    // tiles that is the instruction's order; in rows a token's 4 blocks come to 4 lanes,
+    // at positions turned with the token so that a quarter wave's reads meet no bank twice.
+    const bool rows = side == 1;
+    const int lr = rows ? lane >> 2 : lane & 15, lg = rows ? (lane & 3) ^ (lane >> 4) : lane >> 4;
+    const int read16 = rows ? ((lane & 15) * 4 + ((lane >> 4) ^ (lane >> 2 & 3))) * 16 : lane * 16;
+    const int read_scale = rows ? (lane & 15) * 4 + (lane >> 4) : lane;
+    const auto slot_of = [&](int tile, int r) {
+        const int tok = t0 + tile * 16 + r;
         int64_t s = 0;
         if (tok < p.n_live) s = p.batch_index ? p.batch_index[tok] : tok;
         return s >= 0 && s < p.x.rows ? (uint32_t)s : 0u;  // another's row becomes NaN at the end
@@ -90,20 +98,32 @@ mx_wide_kernel(WideArgs n) {
         const int r = min(wave + kWaves * m, TN - 1);
         wbase[m] = weights_of(r).codes + (int64_t)group_of(r) * kc * 1024;
     }
-    // Tokens: in LDS the 16-byte parts [tile][piece][block][token], then the 8-byte parts in
-    // 16 bytes, [tile][block][token][piece] or (MX6) [tile][half][token][2 blocks].
+    // Tokens: in LDS the 16-byte parts [tile][piece][block and token], then the 8-byte
+    // parts in 16 bytes, [tile][block and token][piece] or (MX6) [tile][half and token][2 blocks].
     uint32_t at[S::kLoadT];
 #pragma unroll
     for (int m = 0; m < S::kLoadT; ++m) {
         const int item = min(wave + kWaves * m, S::kTokens - 1);
-        const bool wide = item < S::kParts16;
         const int e = item - S::kParts16;
-        const int tile = wide ? item / PI : F == kMx6 ? min(2 * e + (lane >> 5), TT - 1) : e;
-        const uint32_t s = slot_of(tile);
-        const uint32_t in = wide ? 64 * (item % PI) + (lane >> 4) * 16
-                                 : 64 * PI + (F == kMx6 ? lane >> 4 & 1 : lane >> 4) * 16;
+        int tile, r = lr;
+        uint32_t in;
+        if (e < 0) {
+            tile = item / PI;
+            in = 64 * (item % PI) + lg * 16;
+        } else if constexpr (F == kMx6) {
+            tile = min(2 * e + (lane >> 5), TT - 1);
+            if (rows) r = lane >> 1 & 15;
+            in = 64 + (rows ? (lane & 1) ^ (lane >> 4 & 1) : lane >> 4 & 1) * 16;
+        } else {
+            tile = e;
+            in = 64 * PI + lg * 16;
+        }
+        const uint32_t s = slot_of(tile, r);
         at[m] = (s >> 4) * p.x.tile + (s & 15) * p.x.row + in * side;
     }
+    // MX6: where this lane's 8 bytes of a tile are
+    const int read8 = rows ? (lane & 15) * 32 + ((lane >> 5) ^ (lane >> 3 & 1)) * 16 + (lane >> 4 & 1) * 8
+                           : (lane >> 5) * 256 + (lane & 15) * 16 + (lane >> 4 & 1) * 8;
     const uint8_t* sbase[4][S::kLoadS];
     uint32_t sat[4][S::kLoadS];
     uint32_t sstep[4][S::kLoadS];
@@ -118,9 +138,9 @@ mx_wide_kernel(WideArgs n) {
                 sstep[q][m] = 256;
             } else {
                 const int tile = (item - TN) / PI, piece = (item - TN) % PI;
-                const uint32_t s = slot_of(tile);
+                const uint32_t s = slot_of(tile, lr);
                 sbase[q][m] = p.x.scales + piece * 16 * side;
-                sat[q][m] = (s >> 4) * p.x.scale_tile + (s & 15) * p.x.scale_row + (lane >> 4) * 4 * side;
+                sat[q][m] = (s >> 4) * p.x.scale_tile + (s & 15) * p.x.scale_row + (rows ? lane & 3 : lg) * 4 * side;
                 sstep[q][m] = scale_bytes(F) * side;
             }
         }
@@ -184,8 +204,8 @@ mx_wide_kernel(WideArgs n) {
             for (int r = 0; r < RN; ++r) ws[r] = s[(wn * RN + r) * 64 + lane];
 #pragma unroll
             for (int t = 0; t < RT; ++t) {
-                xs[t].s0 = s[(TN + (wt * RT + t) * PI) * 64 + lane];
-                if constexpr (F == kMx8) xs[t].s1 = s[(TN + (wt * RT + t) * PI + 1) * 64 + lane];
+                xs[t].s0 = s[(TN + (wt * RT + t) * PI) * 64 + read_scale];
+                if constexpr (F == kMx8) xs[t].s1 = s[(TN + (wt * RT + t) * PI + 1) * 64 + read_scale];
             }
         }
         const uint8_t* here = lds + stage * S::kBytes;
@@ -198,13 +218,12 @@ mx_wide_kernel(WideArgs n) {
             const int tile = wt * RT + t;
             const uint8_t* b = here + TN * 1024;
             const uint8_t* b8 = b + S::kParts16 * 1024;
-            x.a0 = *reinterpret_cast<const v4u*>(b + tile * PI * 1024 + lane * 16);
+            x.a0 = *reinterpret_cast<const v4u*>(b + tile * PI * 1024 + read16);
             if constexpr (F == kMx8) {
-                x.a1 = *reinterpret_cast<const v4u*>(b + (tile * 2 + 1) * 1024 + lane * 16);
-                x.b = *reinterpret_cast<const v4u*>(b8 + tile * 1024 + lane * 16);
+                x.a1 = *reinterpret_cast<const v4u*>(b + (tile * 2 + 1) * 1024 + read16);
+                x.b = *reinterpret_cast<const v4u*>(b8 + tile * 1024 + read16);
             } else if constexpr (F == kMx6) {
-                const v2u y = *reinterpret_cast<const v2u*>(b8 + tile * 512 + (lane >> 5) * 256 + (lane & 15) * 16 +
-                                                            (lane >> 4 & 1) * 8);
+                const v2u y = *reinterpret_cast<const v2u*>(b8 + tile * 512 + read8);
                 x.b = v4u{y[0], y[1], 0u, 0u};
             }
 #pragma unroll
@@ -223,62 +242,57 @@ mx_wide_kernel(WideArgs n) {
     constexpr int RH = RN / P;  // row groups of a wave's results
     if constexpr (P == 2) {
 #pragma unroll
-        for (int r = 0; r < RH; ++r)
-#pragma unroll
-            for (int t = 0; t < RT; ++t)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) acc[r][t][k] = activate(acc[r][t][k], p.activation) * acc[r + RH][t][k];
+        for (int r = 0; r < RH; ++r) gate_values(acc[r], acc[r + RH], p.activation);
     }
-    const int row0 = (nt * WN + wn) * RH * 16 + (lane >> 4) * 4;
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
         const int tok = t0 + (wt * RT + t) * 16 + (lane & 15);
-        if (tok >= p.n_live) continue;
-        if (p.batch_index) {
-            const int s = p.batch_index[tok];
-            if (s < 0 || s >= p.x.rows)
-                for (int r = 0; r < RH; ++r) acc[r][t] = v4f{1.f, 1.f, 1.f, 1.f} * __builtin_nanf("");
-        }
-        if (p.Y == nullptr) continue;
-        float* y = p.Y + tok * p.y_stride;
-#pragma unroll
-        for (int r = 0; r < RH; ++r) {
-            const int64_t row = (int64_t)row0 + r * 16;
-            if (row >= p.w.rows) continue;
-            if (n.vec && row + 4 <= p.w.rows) {
-                *reinterpret_cast<v4f*>(y + row) = acc[r][t];
-            } else {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (row + k < p.w.rows) y[row + k] = acc[r][t][k];
-            }
-        }
+        if (tok >= p.n_live || p.batch_index == nullptr) continue;
+        const int s = p.batch_index[tok];
+        if (s < 0 || s >= p.x.rows)
+            for (int r = 0; r < RH; ++r) acc[r][t] = v4f{1.f, 1.f, 1.f, 1.f} * __builtin_nanf("");
     }
-    if constexpr (P == 2) {
-        if (p.out.codes == nullptr) return;
-        // Quantised rows: through LDS to 8 lanes a block.
-        constexpr int kRow = WN * RH * 16 + 4;  // floats of a token, 4 more against bank conflicts
-        static_assert(TT * 16 * kRow * 4 <= S::kLds, "results fit");
-        float* h = reinterpret_cast<float*>(lds);
+    // Results go through LDS, so that a wave stores whole lines: from the lanes as they are
+    // neighbours would write to 16 rows.  In two passes where all do not fit.
+    constexpr int kRows = WN * RH * 16, kRow = kRows + 4;  // floats of a token, 4 more against bank conflicts
+    constexpr int kPasses = TT * 16 * kRow * 4 <= S::kLds ? 1 : 2, kPassT = RT / kPasses;
+    static_assert(WT * kPassT * 16 * kRow * 4 <= S::kLds, "results fit");
+    float* h = reinterpret_cast<float*>(lds);
+    const int64_t f0 = (int64_t)nt * kRows;
+#pragma unroll
+    for (int pass = 0; pass < kPasses; ++pass) {
         __syncthreads();
 #pragma unroll
-        for (int t = 0; t < RT; ++t)
+        for (int t = 0; t < kPassT; ++t)
 #pragma unroll
             for (int r = 0; r < RH; ++r)
-                *reinterpret_cast<v4f*>(h + ((wt * RT + t) * 16 + (lane & 15)) * kRow + (wn * RH + r) * 16 +
-                                        (lane >> 4) * 4) = acc[r][t];
+                *reinterpret_cast<v4f*>(h + ((wt * kPassT + t) * 16 + (lane & 15)) * kRow + (wn * RH + r) * 16 +
+                                        (lane >> 4) * 4) = acc[r][pass * kPassT + t];
         __syncthreads();
-        constexpr int kUnits = WN * RH * 4;  // of 4 values
-        const int live = min(p.n_live - t0, TT * 16);
-        const int blocks = p.out.kc * 4, rows = (int)p.w.rows;
-        for (int i = threadIdx.x; i < live * kUnits; i += kWaves * 64) {  // whole octets
-            const int t = i / kUnits, u = i % kUnits;
-            const int f = nt * (WN * RH * 16) + u * 4;
-            if (f / 32 >= blocks) continue;
-            v4f y = *reinterpret_cast<const v4f*>(h + t * kRow + u * 4);
-            if (f >= rows) y = v4f{0.f, 0.f, 0.f, 0.f};  // padding
-            const float v[4] = {y[0], y[1], y[2], y[3]};
-            store_octet_as(p.out_form, p.out, t0 + t, f / 32, u & 7, v);
+        constexpr int kUnits = kRows / 4;  // of 4 values, of a token
+        for (int i = threadIdx.x; i < WT * kPassT * 16 * kUnits; i += kWaves * 64) {
+            const int line = i / kUnits, u = i % kUnits;
+            const int tile = line / 16;
+            const int tok = t0 + ((tile / kPassT) * RT + pass * kPassT + tile % kPassT) * 16 + line % 16;
+            if (tok >= p.n_live) continue;
+            v4f y = *reinterpret_cast<const v4f*>(h + line * kRow + u * 4);
+            const int64_t f = f0 + u * 4;
+            if (p.Y != nullptr && f < p.w.rows) {
+                float* o = p.Y + tok * p.y_stride + f;
+                if (n.vec && f + 4 <= p.w.rows) {
+                    *reinterpret_cast<v4f*>(o) = y;
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (f + k < p.w.rows) o[k] = y[k];
+                }
+            }
+            if constexpr (P == 2) {  // 8 lanes a block of 32 features
+                if (p.out.codes == nullptr || f / 32 >= p.out.kc * 4) continue;
+                if (f >= p.w.rows) y = v4f{0.f, 0.f, 0.f, 0.f};  // padding
+                const float v[4] = {y[0], y[1], y[2], y[3]};
+                store_octet_as(p.out_form, p.out, tok, (int)(f / 32), u & 7, v);
+            }
         }
     }
 }
