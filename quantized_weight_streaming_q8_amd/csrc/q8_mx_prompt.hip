@@ -19,7 +19,7 @@ namespace {
 constexpr int kWaves = 8;
 
 // The shape of a workgroup's tile.
-template <int F, int WN, int WT, int RN, int RT>
+template <int F, int WN, int WT, int RN, int RT, int kMaxStages = 4>
 struct Tile {
     static_assert(WN * WT == kWaves, "waves");
     static constexpr int TN = WN * RN, TT = WT * RT;  // row groups (of both projections together), token tiles
@@ -34,8 +34,8 @@ struct Tile {
     static constexpr int kLoadN = (TN + kWaves - 1) / kWaves, kLoadT = (kTokens + kWaves - 1) / kWaves;
     static constexpr int kLoadS = (kScales + 4 * kWaves - 1) / (4 * kWaves);
     static constexpr int kLoads = kLoadN + kLoadT + kLoadS;
-    static constexpr int kFit = (160 * 1024 - 2 * kScales * 256) / kBytes;
-    static constexpr int kStages = kFit > 4 ? 4 : kFit;
+    static constexpr int kFit = (160 * 1024 - 2 * kScales * 256 - TT * 64) / kBytes;
+    static constexpr int kStages = kFit > kMaxStages ? kMaxStages : kFit;
     static constexpr int kLds = kStages * kBytes + 2 * kScales * 256;
     static_assert(kStages >= 2, "two stages");
 };
@@ -47,12 +47,13 @@ struct WideArgs {
 };
 
 // P: projections (2: the gated block; a wave then has RN / 2 row groups of each).
-template <int F, int WN, int WT, int RN, int RT, int P>
+template <int F, int WN, int WT, int RN, int RT, int P, int kMaxStages>
 __global__ void __launch_bounds__(kWaves * 64, 2)
 mx_wide_kernel(WideArgs n) {
-    using S = Tile<F, WN, WT, RN, RT>;
+    using S = Tile<F, WN, WT, RN, RT, kMaxStages>;
     constexpr int TN = S::TN, TT = S::TT, PI = S::PI, D = S::kStages - 1;
     __shared__ __attribute__((aligned(256))) uint8_t lds[S::kLds];
+    __shared__ int slots[TT * 16];  // of the tile's tokens, -1: outside the buffer
     const MxProduct& p = n.p;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // Workgroups go to the 8 dies in turn; each die takes a run of tiles, 4 token
@@ -84,12 +85,14 @@ mx_wide_kernel(WideArgs n) {
     const int lr = rows ? lane >> 2 : lane & 15, lg = rows ? (lane & 3) ^ (lane >> 4) : lane >> 4;
     const int read16 = rows ? ((lane & 15) * 4 + ((lane >> 4) ^ (lane >> 2 & 3))) * 16 : lane * 16;
     const int read_scale = rows ? (lane & 15) * 4 + (lane >> 4) : lane;
-    const auto slot_of = [&](int tile, int r) {
-        const int tok = t0 + tile * 16 + r;
-        int64_t s = 0;
-        if (tok < p.n_live) s = p.batch_index ? p.batch_index[tok] : tok;
-        return s >= 0 && s < p.x.rows ? (uint32_t)s : 0u;  // another's row becomes NaN at the end
-    };
+    // One fetch for all of a workgroup's slots.
+    for (int i = threadIdx.x; i < TT * 16; i += kWaves * 64) {
+        const int tok = t0 + i;
+        const int s = tok >= p.n_live ? 0 : p.batch_index ? p.batch_index[tok] : tok;
+        slots[i] = s >= 0 && s < p.x.rows ? s : -1;
+    }
+    __syncthreads();
+    const auto slot_of = [&](int tile, int r) { return (uint32_t)max(slots[tile * 16 + r], 0); };
 
     // What this wave loads.  A load too many repeats the last one's, to the same place.
     const uint8_t* wbase[S::kLoadN];
@@ -246,11 +249,10 @@ mx_wide_kernel(WideArgs n) {
     }
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-        const int tok = t0 + (wt * RT + t) * 16 + (lane & 15);
-        if (tok >= p.n_live || p.batch_index == nullptr) continue;
-        const int s = p.batch_index[tok];
-        if (s < 0 || s >= p.x.rows)
+        if (slots[(wt * RT + t) * 16 + (lane & 15)] < 0) {
+#pragma unroll
             for (int r = 0; r < RH; ++r) acc[r][t] = v4f{1.f, 1.f, 1.f, 1.f} * __builtin_nanf("");
+        }
     }
     // Results go through LDS, so that a wave stores whole lines: from the lanes as they are
     // neighbours would write to 16 rows.  In two passes where all do not fit.
@@ -297,9 +299,9 @@ mx_wide_kernel(WideArgs n) {
     }
 }
 
-template <int F, int WN, int WT, int RN, int RT>
+template <int F, int WN, int WT, int RN, int RT, int kMaxStages = 4>
 hipError_t launch_wide(const MxProduct& p, hipStream_t st) {
-    using S = Tile<F, WN, WT, RN, RT>;
+    using S = Tile<F, WN, WT, RN, RT, kMaxStages>;
     WideArgs n;
     n.p = p;
     const bool two = p.wu.codes != nullptr;
@@ -309,8 +311,8 @@ hipError_t launch_wide(const MxProduct& p, hipStream_t st) {
     n.vec = (reinterpret_cast<uintptr_t>(p.Y) & 15) == 0 && p.y_stride % 4 == 0;
     const int64_t total = (int64_t)n.n_tiles * n.t_tiles;
     const dim3 grid((unsigned)((total + 7) / 8 * 8)), block(kWaves * 64);
-    if (two) mx_wide_kernel<F, WN, WT, RN, RT, 2><<<grid, block, 0, st>>>(n);
-    else mx_wide_kernel<F, WN, WT, RN, RT, 1><<<grid, block, 0, st>>>(n);
+    if (two) mx_wide_kernel<F, WN, WT, RN, RT, 2, kMaxStages><<<grid, block, 0, st>>>(n);
+    else mx_wide_kernel<F, WN, WT, RN, RT, 1, kMaxStages><<<grid, block, 0, st>>>(n);
     return hipGetLastError();
 }
 
