@@ -782,34 +782,65 @@ def q8_mx4_unpack_weights(weights: MX4Weights, codes, scales, stream=None) -> No
            "q8_mx4_unpack_weights")
 
 
+_Tensor, _float32, _int32 = torch.Tensor, torch.float32, torch.int32
+_get_device, _get_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
+def _address(x, name: str, dtype, need_bytes: int, dev: int):
+    """_fast, without its test for a device that get_device() answers too."""
+    if type(x) is _Tensor and x.get_device() == dev and x.dtype is dtype and x.nbytes >= need_bytes \
+            and x.is_contiguous() and dev >= 0:
+        return x.data_ptr()
+    return _fast(x, name, dtype, need_bytes, dev)
+
+
+def _short(h, kind, name: str, dev: int):
+    """_handle(h, kind, name) where the current device is known."""
+    return h._ref if type(h) is kind and h._device_index == dev else _handle(h, kind, name)
+
+
 def q8_mx_quantize_acts(X, n_rows: int, acts: Acts, x_stride: int | None = None, stream=None) -> None:
     """Rows of X (x_stride apart, default K) into slots 0 .. n_rows - 1."""
-    x_stride = acts.K if x_stride is None else x_stride
-    dev = _current_device()
-    (x,) = _fast_all(_fast(X, "X", torch.float32, _span(n_rows, x_stride, acts.K), dev))
-    _check(_lib.q8_mx_quantize_acts(x, x_stride, n_rows, _handle(acts, Acts, "acts"), _raw_stream(stream, dev)),
-           "q8_mx_quantize_acts")
+    K = acts.K
+    if x_stride is None:
+        x_stride = K
+    dev = _get_device() if type(acts) is Acts else _current_device()
+    x = _address(X, "X", _float32, 4 * ((n_rows - 1) * x_stride + K), dev)
+    if type(x) is tuple:
+        (x,) = _fast_all(x)
+    rc = _lib.q8_mx_quantize_acts(x, x_stride, n_rows, _short(acts, Acts, "acts", dev), _get_stream(dev) if stream is None and dev >= 0 else _stream(stream))
+    if rc:
+        _check(rc, "q8_mx_quantize_acts")
 
 
 def q8_mx_read_acts(acts: Acts, batch_index, n_rows: int, X, stream=None) -> None:
     """The values of slots batch_index[0 .. n_rows - 1] (None: slots 0 ..)."""
-    dev = _current_device()
-    bi, x = _fast_all(_fast(batch_index, "batch_index", torch.int32, _n(n_rows, 4), dev),
-                      _fast(X, "X", torch.float32, _n(n_rows * acts.K, 4), dev))
-    _check(_lib.q8_mx_read_acts(_handle(acts, Acts, "acts"), bi, n_rows, x, _raw_stream(stream, dev)),
-           "q8_mx_read_acts")
+    dev = _get_device() if type(acts) is Acts else _current_device()
+    bi = None if batch_index is None else _address(batch_index, "batch_index", _int32, 4 * n_rows, dev)
+    x = _address(X, "X", _float32, 4 * n_rows * acts.K, dev)
+    if type(bi) is tuple or type(x) is tuple:
+        bi, x = _fast_all(bi, x)
+    rc = _lib.q8_mx_read_acts(_short(acts, Acts, "acts", dev), bi, n_rows, x, _get_stream(dev) if stream is None and dev >= 0 else _stream(stream))
+    if rc:
+        _check(rc, "q8_mx_read_acts")
 
 
 def q8_mx4_matmul(weights: MX4Weights, acts: Acts, batch_index, n_live: int, Y, y_stride: int | None = None,
                   stream=None) -> None:
     """Y [n_live][N] (rows y_stride apart, default N); token t takes slot
     batch_index[t] (None: slot t)."""
-    y_stride = weights.N if y_stride is None else y_stride
-    dev = _current_device()
-    bi, y = _fast_all(_fast(batch_index, "batch_index", torch.int32, _n(n_live, 4), dev),
-                      _fast(Y, "Y", torch.float32, _span(n_live, y_stride, weights.N), dev))
-    _check(_lib.q8_mx4_matmul(_handle(weights, MX4Weights, "weights"), _handle(acts, Acts, "acts"), bi, n_live, y,
-                              y_stride, _raw_stream(stream, dev)), "q8_mx4_matmul")
+    N = weights.N
+    if y_stride is None:
+        y_stride = N
+    dev = _get_device() if type(weights) is MX4Weights else _current_device()
+    bi = None if batch_index is None else _address(batch_index, "batch_index", _int32, 4 * n_live, dev)
+    y = _address(Y, "Y", _float32, 4 * ((n_live - 1) * y_stride + N), dev)
+    if type(bi) is tuple or type(y) is tuple:
+        bi, y = _fast_all(bi, y)
+    rc = _lib.q8_mx4_matmul(_short(weights, MX4Weights, "weights", dev), _short(acts, Acts, "acts", dev), bi, n_live, y,
+                            y_stride, _get_stream(dev) if stream is None and dev >= 0 else _stream(stream))
+    if rc:
+        _check(rc, "q8_mx4_matmul")
 
 
 def q8_mx4_gated(gate: MX4Weights, up: MX4Weights, acts: Acts, batch_index, n_live: int, H=None,
@@ -817,16 +848,22 @@ def q8_mx4_gated(gate: MX4Weights, up: MX4Weights, acts: Acts, batch_index, n_li
                  stream=None) -> None:
     """activation(gate x) * (up x) for each token: fp32 rows to H, quantised
     ones to slots 0 .. n_live - 1 of h_acts, or both."""
-    if activation not in Q8_ACTIVATIONS:
+    kind = Q8_ACTIVATIONS.get(activation)
+    if kind is None:
         raise ValueError(f"activation: expected one of {sorted(Q8_ACTIVATIONS)}, got {activation!r}")
-    h_stride = gate.N if h_stride is None else h_stride
-    dev = _current_device()
-    bi, h = _fast_all(_fast(batch_index, "batch_index", torch.int32, _n(n_live, 4), dev),
-                      _fast(H, "H", torch.float32, _span(n_live, h_stride, gate.N), dev))
-    _check(_lib.q8_mx4_gated(_handle(gate, MX4Weights, "gate"), _handle(up, MX4Weights, "up"),
-                             _handle(acts, Acts, "acts"), bi, n_live, Q8_ACTIVATIONS[activation], h, h_stride,
-                             None if h_acts is None else _handle(h_acts, Acts, "h_acts"), _raw_stream(stream, dev)),
-           "q8_mx4_gated")
+    N = gate.N
+    if h_stride is None:
+        h_stride = N
+    dev = _get_device() if type(gate) is MX4Weights else _current_device()
+    bi = None if batch_index is None else _address(batch_index, "batch_index", _int32, 4 * n_live, dev)
+    h = None if H is None else _address(H, "H", _float32, 4 * ((n_live - 1) * h_stride + N), dev)
+    if type(bi) is tuple or type(h) is tuple:
+        bi, h = _fast_all(bi, h)
+    rc = _lib.q8_mx4_gated(_short(gate, MX4Weights, "gate", dev), _short(up, MX4Weights, "up", dev),
+                           _short(acts, Acts, "acts", dev), bi, n_live, kind, h, h_stride,
+                           None if h_acts is None else _short(h_acts, Acts, "h_acts", dev), _get_stream(dev) if stream is None and dev >= 0 else _stream(stream))
+    if rc:
+        _check(rc, "q8_mx4_gated")
 
 
 def q8_norm_step(X, n_rows: int, K: int, post: Norm | None = None, gate=None, scale: float = 1.0, residual=None,
@@ -836,21 +873,27 @@ def q8_norm_step(X, n_rows: int, K: int, post: Norm | None = None, gate=None, sc
     """residual_out = residual + scale * gate * post(X); y = pre(residual_out)
     goes to Y, to acts, or both.  Strides default to K, gate_stride to 0 (one
     gate for all rows) unless the gate is a tensor of two dimensions."""
-    xs, rs, os, ys = (K if s is None else s for s in (x_stride, residual_stride, residual_out_stride, y_stride))
+    xs = K if x_stride is None else x_stride
+    rs = K if residual_stride is None else residual_stride
+    os = K if residual_out_stride is None else residual_out_stride
+    ys = K if y_stride is None else y_stride
     if gate_stride is None:
         gate_stride = K if isinstance(gate, torch.Tensor) and gate.dim() == 2 else 0
-    dev = _current_device()
-    f32 = torch.float32
-    x, g, r, o, y = _fast_all(
-        _fast(X, "X", f32, _span(n_rows, xs, K), dev),
-        _fast(gate, "gate", f32, _span(n_rows, gate_stride, K), dev),
-        _fast(residual, "residual", f32, _span(n_rows, rs, K), dev),
-        _fast(residual_out, "residual_out", f32, _span(n_rows, os, K), dev),
-        _fast(Y, "Y", f32, _span(n_rows, ys, K), dev))
-    _check(_lib.q8_norm_step(x, xs, _norm_ref(post, "post", K, n_rows), g, gate_stride, scale, r, rs, o, os,
-                             _norm_ref(pre, "pre", K, n_rows), y, ys,
-                             None if acts is None else _handle(acts, Acts, "acts"), n_rows, K,
-                             _raw_stream(stream, dev)), "q8_norm_step")
+    dev = _get_device() if type(X) is _Tensor and X.is_cuda else _current_device()
+    f32 = _float32
+    x = _address(X, "X", f32, 4 * ((n_rows - 1) * xs + K), dev)
+    g = None if gate is None else _address(gate, "gate", f32, 4 * ((n_rows - 1) * gate_stride + K), dev)
+    r = None if residual is None else _address(residual, "residual", f32, 4 * ((n_rows - 1) * rs + K), dev)
+    o = None if residual_out is None else _address(residual_out, "residual_out", f32, 4 * ((n_rows - 1) * os + K), dev)
+    y = None if Y is None else _address(Y, "Y", f32, 4 * ((n_rows - 1) * ys + K), dev)
+    if type(x) is tuple or type(g) is tuple or type(r) is tuple or type(o) is tuple or type(y) is tuple:
+        x, g, r, o, y = _fast_all(x, g, r, o, y)
+    rc = _lib.q8_norm_step(x, xs, None if post is None else _norm_ref(post, "post", K, n_rows), g, gate_stride, scale,
+                           r, rs, o, os, None if pre is None else _norm_ref(pre, "pre", K, n_rows), y, ys,
+                           None if acts is None else _short(acts, Acts, "acts", dev), n_rows, K,
+                           _get_stream(dev) if stream is None and dev >= 0 else _stream(stream))
+    if rc:
+        _check(rc, "q8_norm_step")
 
 
 # ------------------------------------------------- torch allocation helpers

@@ -210,6 +210,7 @@ q8_status q8_norm_step(const float* X, int64_t x_stride, const q8_norm* post, co
     s.pre = view(pre);
     s.scale = (double)scale;
     s.K = K;
+    s.rK = 1.0 / (double)K;
     s.n_rows = n_rows;
     return from_hip(q8::launch_norm_step(s, stream));
 }

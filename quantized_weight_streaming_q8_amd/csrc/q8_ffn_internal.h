@@ -251,6 +251,7 @@ struct NormStep {
     uint16_t* q80_scales;  // with kQ80
     int64_t q80_sc;        // super-chunks of q8_internal.h's layout
     int64_t K;
+    double rK;  // 1 / K
     int n_rows;
 };
 hipError_t launch_norm_step(const NormStep& s, hipStream_t st);
