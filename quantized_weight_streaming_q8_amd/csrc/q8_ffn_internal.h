@@ -23,7 +23,7 @@
 //        6-bit codes of l / 8 (first) and h / 8, whose code is the number itself, so that
 //        both enter the instruction as MX6 does, with the scales 2^(e - 3) and 2^(e + 1)
 //        for elements q / 64 * 2^e.  16 bytes of each block's first piece, of each
-//        block's second, then each block's 8 bytes of the one and of the other.
+//        block's second, then 8 bytes of each, in the same order, blocks in pairs.
 // After all codes, per row and super-chunk 16 scale bytes for each piece: byte 4 g + j is
 // block g of chunk j.  Rows in the order of rows are padded to whole super-chunks (a
 // multiple of 128 bytes).
@@ -99,9 +99,7 @@ __device__ inline uint8_t* block16(const MxView& m, int64_t r, int b, int i) {
 }
 template <int F>
 __device__ inline uint8_t* block8(const MxView& m, int64_t r, int b, int i) {
-    // 16 bytes hold a block's two pieces (MX8) or those of two blocks (MX6)
-    const int k = F == kMx8 ? 2 * (b & 3) + i : b & 3;
-    return m.codes + chunk_at<F>(m, r, b) + (64 * form_pieces(F) + (k >> 1) * 16) * m.side + (k & 1) * 8;
+    return m.codes + chunk_at<F>(m, r, b) + (64 * form_pieces(F) + 32 * i + (b >> 1 & 1) * 16) * m.side + (b & 1) * 8;
 }
 template <int F>
 __device__ inline uint8_t* block_scale_at(const MxView& m, int64_t r, int b, int i) {
@@ -228,7 +226,8 @@ struct MxProduct {
     int activation;
 };
 hipError_t launch_mx_product(const MxProduct& p, hipStream_t st);
-hipError_t launch_mx_wide(const MxProduct& p, hipStream_t st);  // q8_mx_prompt.hip
+hipError_t launch_mx_columns(const MxProduct& p, hipStream_t st);  // q8_mx_columns.hip
+hipError_t launch_mx_wide(const MxProduct& p, hipStream_t st);     // q8_mx_prompt.hip
 
 struct NormView {
     const float* weight;

@@ -38,10 +38,16 @@ template <int F>
 __device__ inline void load_tokens(Tokens& x, const uint8_t* row, int side, int g) {
     x.a0 = *reinterpret_cast<const v4u*>(row + 16 * g * side);
     if constexpr (F == kMx8) x.a1 = *reinterpret_cast<const v4u*>(row + (64 + 16 * g) * side);
-    if constexpr (F == kMx8) x.b = *reinterpret_cast<const v4u*>(row + (128 + 16 * g) * side);
-    if constexpr (F == kMx6) {
-        const v2u b = *reinterpret_cast<const v2u*>(row + (64 + 16 * (g >> 1)) * side + 8 * (g & 1));
-        x.b = v4u{b[0], b[1], 0u, 0u};
+    if constexpr (F != kMx4) {
+        const uint8_t* at = row + (64 * form_pieces(F) + 16 * (g >> 1)) * side + 8 * (g & 1);
+        const v2u b = *reinterpret_cast<const v2u*>(at);
+        x.b00 = b[0];
+        x.b01 = b[1];
+        if constexpr (F == kMx8) {
+            const v2u y = *reinterpret_cast<const v2u*>(at + 32 * side);
+            x.b10 = y[0];
+            x.b11 = y[1];
+        }
     }
 }
 
@@ -284,7 +290,8 @@ hipError_t narrow_form(const NarrowArgs& n, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_mx_product(const MxProduct& p, hipStream_t st) {
-    if (p.n_live > 16) return launch_mx_wide(p, st);
+    if (p.n_live > 64) return launch_mx_wide(p, st);
+    if (p.n_live > 16) return launch_mx_columns(p, st);
     NarrowArgs n;
     n.p = p;
     // one super-chunk a wave; from 13 to 16 two, whose tokens still fit the registers of

@@ -10,12 +10,13 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+typedef uint32_t v6u __attribute__((ext_vector_type(6)));
 
 // One chunk (128 columns) of 16 tokens, and the scale bytes of a super-chunk's:
 // two pieces for MX8.  Members of their own, since arrays end up in scratch memory here.
 struct Tokens {
     v4u a0, a1;
-    v4u b;  // the last 8 bytes of each piece; not for MX4
+    uint32_t b00, b01, b10, b11;  // the last 8 bytes of each piece; not for MX4
 };
 struct Scales {
     uint32_t s0, s1;
@@ -37,8 +38,8 @@ __device__ inline v4f multiply_piece(v4u w, uint32_t ws, v4u a, uint32_t b0, uin
 // times 16 tokens.
 template <int F, int J>
 __device__ inline v4f multiply(v4u w, uint32_t ws, const Tokens& x, const Scales& xs, v4f c) {
-    c = multiply_piece<F == kMx4 ? 4 : 2, J>(w, ws, x.a0, x.b[0], x.b[1], xs.s0, c);
-    if constexpr (F == kMx8) c = multiply_piece<2, J>(w, ws, x.a1, x.b[2], x.b[3], xs.s1, c);
+    c = multiply_piece<F == kMx4 ? 4 : 2, J>(w, ws, x.a0, x.b00, x.b01, xs.s0, c);
+    if constexpr (F == kMx8) c = multiply_piece<2, J>(w, ws, x.a1, x.b10, x.b11, xs.s1, c);
     return c;
 }
 

@@ -102,7 +102,7 @@ mx_wide_kernel(WideArgs n) {
         wbase[m] = weights_of(r).codes + (int64_t)group_of(r) * kc * 1024;
     }
     // Tokens: in LDS the 16-byte parts [tile][piece][block and token], then the 8-byte
-    // parts in 16 bytes, [tile][block and token][piece] or (MX6) [tile][half and token][2 blocks].
+    // parts, blocks in pairs, [tile][piece and pair and token] or (MX6) [tile][pair and token].
     uint32_t at[S::kLoadT];
 #pragma unroll
     for (int m = 0; m < S::kLoadT; ++m) {
@@ -124,9 +124,13 @@ mx_wide_kernel(WideArgs n) {
         const uint32_t s = slot_of(tile, r);
         at[m] = (s >> 4) * p.x.tile + (s & 15) * p.x.row + in * side;
     }
-    // MX6: where this lane's 8 bytes of a tile are
-    const int read8 = rows ? (lane & 15) * 32 + ((lane >> 5) ^ (lane >> 3 & 1)) * 16 + (lane >> 4 & 1) * 8
-                           : (lane >> 5) * 256 + (lane & 15) * 16 + (lane >> 4 & 1) * 8;
+    // where this lane's 8 bytes of a tile are: (piece and) pair lane >> 5
+    const auto read8_of = [&](int piece) {
+        const int r = lane & 15, pair = 2 * piece + (lane >> 5), in = (lane >> 4 & 1) * 8;
+        if (!rows) return (pair * 16 + r) * 16 + in;
+        return (F == kMx8 ? (r * 4 + (pair ^ (r >> 2))) * 16 : (r * 2 + (pair ^ (r >> 3))) * 16) + in;
+    };
+    const int read8 = read8_of(0), read8_high = read8_of(1);
     const uint8_t* sbase[4][S::kLoadS];
     uint32_t sat[4][S::kLoadS];
     uint32_t sstep[4][S::kLoadS];
@@ -224,10 +228,14 @@ mx_wide_kernel(WideArgs n) {
             x.a0 = *reinterpret_cast<const v4u*>(b + tile * PI * 1024 + read16);
             if constexpr (F == kMx8) {
                 x.a1 = *reinterpret_cast<const v4u*>(b + (tile * 2 + 1) * 1024 + read16);
-                x.b = *reinterpret_cast<const v4u*>(b8 + tile * 1024 + read16);
-            } else if constexpr (F == kMx6) {
-                const v2u y = *reinterpret_cast<const v2u*>(b8 + tile * 512 + read8);
-                x.b = v4u{y[0], y[1], 0u, 0u};
+                const v2u z = *reinterpret_cast<const v2u*>(b8 + tile * 1024 + read8_high);
+                x.b10 = z[0];
+                x.b11 = z[1];
+            }
+            if constexpr (F != kMx4) {
+                const v2u y = *reinterpret_cast<const v2u*>(b8 + tile * (512 * PI) + read8);
+                x.b00 = y[0];
+                x.b01 = y[1];
             }
 #pragma unroll
             for (int r = 0; r < RN; ++r) acc[r][t] = multiply<F, j>(a[r], ws[r], x, xs[t], acc[r][t]);
