@@ -47,7 +47,8 @@ mx_columns_kernel(ColumnArgs n) {
     constexpr int PI = S::PI;
     constexpr int kGroups = P == 2 ? R : kHalves * R;  // row groups of a tile's results
     __shared__ __attribute__((aligned(256))) uint8_t lds[2 * S::kBytes + kWaves * R * 1024];
-    __shared__ int slots[2][T * 16];  // of this tile's tokens and the next one's, -1: outside the buffer
+    // This tile's columns and the next one's: their slots, -1 outside the buffer, and tokens.
+    __shared__ int slots[2][T * 16], tokens[2][T * 16];
     v4f* const parts = reinterpret_cast<v4f*>(lds + 2 * S::kBytes);  // [wave][R][64]
     const MxProduct& p = n.p;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -70,13 +71,28 @@ mx_columns_kernel(ColumnArgs n) {
     };
     const int read8 = read8_of(0), read8_high = read8_of(1);
 
-    // Tiles: all of the weights for one block of tokens, then for the next.
+    // Tiles: all of the weights for one block of tokens, then for the next.  A block's tokens
+    // become columns in the order of their slots, so that neighbouring lanes load
+    // neighbouring bytes (64 tokens in a random order: 141 us for 151936 x 5120).
     const auto find_slots = [&](int id, int half) {
-        const int t0 = id / n.n_tiles * (16 * T);
-        for (int i = threadIdx.x; i < T * 16; i += kWaves * 64) {
-            const int tok = t0 + i;
-            const int s = tok >= p.n_live ? 0 : p.batch_index ? p.batch_index[tok] : tok;
-            slots[half][i] = s >= 0 && s < p.x.rows ? s : -1;
+        if (wave != 0) return;
+        const int tok = id / n.n_tiles * (16 * T) + lane;
+        int s = INT32_MAX;  // a column of no token, last
+        if (lane < 16 * T && tok < p.n_live) {
+            s = p.batch_index ? p.batch_index[tok] : tok;
+            if (s < 0 || s >= p.x.rows) s = -1;
+        }
+        int rank = lane;
+        if (p.batch_index) {
+            rank = 0;
+            for (int i = 0; i < 16 * T; ++i) {
+                const int other = __builtin_amdgcn_readlane(s, i);
+                rank += other < s || (other == s && i < lane) ? 1 : 0;
+            }
+        }
+        if (lane < 16 * T) {
+            slots[half][rank] = s == INT32_MAX ? 0 : s;
+            tokens[half][rank] = s == INT32_MAX ? INT32_MAX : tok;
         }
     };
     uint32_t at[S::kLoads], sat[S::kLoadS];
@@ -109,34 +125,29 @@ mx_columns_kernel(ColumnArgs n) {
     };
     const uint32_t lds0 = lds_address(lds);
     // The tokens of super-chunk s to buffer (to & 1).  Chunks past the last are the last again.
-    const auto load_tokens = [&](int s, int to) {
+    const auto load_tokens = [&](int i, int s, int to) {  // load i of kLoads + kLoadS
         const uint32_t base = lds0 + (to & 1) * S::kBytes;
-#pragma unroll
-        for (int m = 0; m < S::kLoads; ++m) {
-            const int item = min(wave + kWaves * m, S::kItems - 1);
+        if (i < S::kLoads) {
+            const int item = min(wave + kWaves * i, S::kItems - 1);
             const int c = min(4 * s + item / S::kChunk, kc - 1);
-            lds_load16(base + item * 1024, p.x.codes + (int64_t)c * (chunk_bytes(F) * side), at[m]);
-        }
-#pragma unroll
-        for (int m = 0; m < S::kLoadS; ++m) {
-            const int item = min(wave + kWaves * m, S::kScales - 1);
+            lds_load16(base + item * 1024, p.x.codes + (int64_t)c * (chunk_bytes(F) * side), at[i]);
+        } else {
+            const int m = i - S::kLoads, item = min(wave + kWaves * m, S::kScales - 1);
             lds_load4(base + S::kItems * 1024 + item * 256, p.x.scales + (int64_t)s * (scale_bytes(F) * side), sat[m]);
         }
     };
+    constexpr int kTokenLoads = S::kLoads + S::kLoadS;
     struct Weights {
         v4u c[R];
         uint32_t s[R];
     };
     // This wave's chunk of super-chunk s of a tile's weights.
-    const auto load_weights = [&](Weights& w, int id, int s) {
-        const int nt = id % n.n_tiles, c = min(4 * s + kw, kc - 1);
+    const auto load_weights = [&](Weights& w, int r, int nt, int s) {  // row group r
+        const int c = min(4 * s + kw, kc - 1);
         const MxView& m = P == 2 && rw == 1 ? p.wu : p.w;
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int64_t g = min((P == 2 ? nt * R : (nt * kHalves + rw) * R) + r, groups - 1);
-            w.c[r] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(m.codes + (g * kc + c) * 1024 + lane * 16));
-            w.s[r] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(m.scales + (g * sc + s) * 256 + lane * 4));
-        }
+        const int64_t g = min((P == 2 ? nt * R : (nt * kHalves + rw) * R) + r, groups - 1);
+        w.c[r] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(m.codes + (g * kc + c) * 1024 + lane * 16));
+        w.s[r] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(m.scales + (g * sc + s) * 256 + lane * 4));
     };
 
     // The steps are numbered through all of this workgroup's tiles; past the last the last
@@ -151,6 +162,9 @@ mx_columns_kernel(ColumnArgs n) {
         }
         return k;
     };
+    // Where a tile's lane (column c, quarter q) of row group g lies among the 64: so that
+    // 16 readers, two columns of two row groups, meet no bank twice.
+    const auto place = [](int c, int q, int g) { return q * 16 + (c ^ (4 * q) ^ (2 * (g & 1))); };
     v4f acc[R][T];
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -158,14 +172,19 @@ mx_columns_kernel(ColumnArgs n) {
         for (int t = 0; t < T; ++t) acc[r][t] = v4f{0.f, 0.f, 0.f, 0.f};
     Step k0{(int)blockIdx.x, 0}, k1 = after(k0), k2 = after(k1);
     Weights w0, w1;
-    load_weights(w0, k0.id, k0.s);
+#pragma unroll
+    for (int r = 0; r < R; ++r) load_weights(w0, r, k0.id % n.n_tiles, k0.s);
     find_slots(k0.id, 0);
     __syncthreads();
     find_addresses(0);
-    load_tokens(0, 0);
-    load_weights(w1, k1.id, k1.s);
+#pragma unroll
+    for (int i = 0; i < kTokenLoads; ++i) load_tokens(i, 0, 0);
+#pragma unroll
+    for (int r = 0; r < R; ++r) load_weights(w1, r, k1.id % n.n_tiles, k1.s);
     int half = 0;
-    for (int step = 0;; ++step) {
+    // One step; the last of all gives false.  The three sets of weights change places by
+    // name: a copy would wait for what is still on its way.
+    const auto run = [&](int step, Weights& w0, Weights& w2) {
         // tokens and weights of this step are here, the next one's weights on their way
 #pragma unroll
         for (int r = 0; r < R; ++r) asm volatile("" : "+v"(w0.c[r]), "+v"(w0.s[r]));
@@ -183,53 +202,53 @@ mx_columns_kernel(ColumnArgs n) {
             }
             find_addresses(half ^ 1);
         }
-        load_tokens(k1.s, step + 1);
-        Weights w2;
-        load_weights(w2, k2.id, k2.s);
-
-        if (4 * k0.s + kw < kc) {
-            const uint8_t* here = lds + (step & 1) * S::kBytes;
-            const uint8_t* chunk = here + kw * S::kChunk * 1024;
-            const uint32_t* scales = reinterpret_cast<const uint32_t*>(here + S::kItems * 1024);
+        const int nt2 = k2.id % n.n_tiles;
+        const uint8_t* here = lds + (step & 1) * S::kBytes;
+        const uint8_t* chunk = here + kw * S::kChunk * 1024;
+        const uint32_t* scales = reinterpret_cast<const uint32_t*>(here + S::kItems * 1024);
+        const bool live = 4 * k0.s + kw < kc;
+        // Loads go out between the products, tokens in the first half and weights in the
+        // second: at once they would keep the wave from its products for 1 us.
+        constexpr int kBlocks = T * PI, kFirst = (kBlocks + 1) / 2, kSecond = kBlocks - kFirst;
 #pragma unroll
-            for (int t = 0; t < T; ++t)
+        for (int b = 0; b < kBlocks; ++b) {
+            const int t = b / PI, k = b % PI;
+            if (b < kFirst) {
 #pragma unroll
-                for (int k = 0; k < PI; ++k) {
-                    const v4u v = *reinterpret_cast<const v4u*>(chunk + (t * PI + k) * 1024 + read16);
-                    const uint32_t xs = scales[(t * PI + k) * 64 + read_scale] >> (8 * kw);
-                    Tokens x;
-                    x.a0 = v;
-                    if constexpr (F != kMx4) {
-                        const v2u y = *reinterpret_cast<const v2u*>(chunk + S::kParts16 * 1024 + t * (512 * PI) +
-                                                                    (k == 0 ? read8 : read8_high));
-                        x.b00 = y[0];
-                        x.b01 = y[1];
-                    }
+                for (int i = b * kTokenLoads / kFirst; i < (b + 1) * kTokenLoads / kFirst; ++i) load_tokens(i, k1.s, step + 1);
+            } else {
 #pragma unroll
-                    for (int r = 0; r < R; ++r)
-                        acc[r][t] = multiply_piece<F == kMx4 ? 4 : 2, 0>(w0.c[r], w0.s[r] >> (8 * kw), x.a0, x.b00, x.b01, xs,
-                                                                          acc[r][t]);
-                }
+                for (int r = (b - kFirst) * R / kSecond; r < (b - kFirst + 1) * R / kSecond; ++r) load_weights(w2, r, nt2, k2.s);
+            }
+            if (live) {
+                const v4u v = *reinterpret_cast<const v4u*>(chunk + (t * PI + k) * 1024 + read16);
+                const uint32_t xs = scales[(t * PI + k) * 64 + read_scale] >> (8 * kw);
+                v2u y = {0u, 0u};
+                if constexpr (F != kMx4)
+                    y = *reinterpret_cast<const v2u*>(chunk + S::kParts16 * 1024 + t * (512 * PI) + (k == 0 ? read8 : read8_high));
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    acc[r][t] = multiply_piece<F == kMx4 ? 4 : 2, 0>(w0.c[r], w0.s[r] >> (8 * kw), v, y[0], y[1], xs, acc[r][t]);
+            }
         }
-        w0 = w1;
-        w1 = w2;
-
         if (k0.s == sc - 1) {  // a tile's end
-            const int nt = k0.id % n.n_tiles, t0 = k0.id / n.n_tiles * (16 * T);
+            const int nt = k0.id % n.n_tiles;
 #pragma unroll
             for (int t = 0; t < T; ++t) {
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    parts[(wave * R + r) * 64 + lane] = acc[r][t];
+                    parts[(wave * R + r) * 64 + place(lane & 15, lane >> 4, P == 2 ? r : rw * R + r)] = acc[r][t];
                     acc[r][t] = v4f{0.f, 0.f, 0.f, 0.f};
                 }
                 wait_lds_reads();
                 __builtin_amdgcn_s_barrier();
                 asm volatile("" ::: "memory");
-                // a thread: 4 consecutive features of one token, neighbours the next ones
-                for (int i = threadIdx.x; i < kGroups * 64; i += kWaves * 64) {
-                    const int c = i / (kGroups * 4), u = i % (kGroups * 4);
-                    const int from = (u & 3) * 16 + c, g = u >> 2;
+                // a thread: 4 consecutive features of one token; 8 neighbours its next ones, of
+                // two row groups
+                for (int i = threadIdx.x; i < (kGroups + 1) / 2 * 128; i += kWaves * 64) {
+                    const int c = i >> 3 & 15, g = (i >> 7) * 2 + (i >> 2 & 1), u = g * 4 + (i & 3);
+                    if (g >= kGroups) continue;  // the second of a pair
+                    const int from = place(c, i & 3, g);
                     const int h = P == 2 ? 0 : g / R, r = P == 2 ? g : g % R;
                     v4f y = parts[(h * R + r) * 64 + from];
 #pragma unroll
@@ -243,7 +262,7 @@ mx_columns_kernel(ColumnArgs n) {
                         gate_values(gate, up, p.activation);
                         y = gate[0];
                     }
-                    const int tok = t0 + t * 16 + c;
+                    const int tok = tokens[half][t * 16 + c];
                     if (tok >= p.n_live) continue;  // whole octets: one token's
                     if (slots[half][t * 16 + c] < 0) y = v4f{1.f, 1.f, 1.f, 1.f} * __builtin_nanf("");
                     const int64_t f = (int64_t)nt * (kGroups * 16) + u * 4;
@@ -268,12 +287,16 @@ mx_columns_kernel(ColumnArgs n) {
                 __builtin_amdgcn_s_barrier();  // the sums have been read
                 asm volatile("" ::: "memory");
             }
-            if (!turn) break;
+            if (!turn) return false;
             if (n.t_tiles > 1) half ^= 1;
         }
         k0 = k1;
         k1 = k2;
         k2 = after(k2);
+        return true;
+    };
+    Weights w2;
+    for (int step = 0; run(step, w0, w2) && run(step + 1, w1, w0) && run(step + 2, w2, w1); step += 3) {
     }
     wait_loads<0>();  // those past the end
 }
