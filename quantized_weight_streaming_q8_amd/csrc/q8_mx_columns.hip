@@ -1,5 +1,5 @@
 // q8_mx_columns.hip -- products of MX4 weights with MX activations, and the gated
-// block, for 17 to 64 tokens at a time: the weights still bound the time, but the
+// block, for blocks of 17 to 64 tokens: the weights still bound the time, but the
 // tokens no longer fit the registers.
 //
 // A workgroup of 8 waves makes tiles of 2 R row groups (P = 2: R of the gate's and as many
@@ -10,7 +10,6 @@
 // for memory half of the time).  The 4 chunks' sums meet in LDS and are added in order.
 
 #include <algorithm>
-#include <type_traits>
 
 #include "q8_lds.h"
 #include "q8_mx_mfma.h"
@@ -43,7 +42,6 @@ template <int F, int T, int R, int P>
 __global__ void __launch_bounds__(kWaves * 64, 2)
 mx_columns_kernel(ColumnArgs n) {
     using S = Super<F, T>;
-    using Operand = std::conditional_t<F == kMx4, v4u, v6u>;
     constexpr int PI = S::PI;
     constexpr int kGroups = P == 2 ? R : kHalves * R;  // row groups of a tile's results
     __shared__ __attribute__((aligned(256))) uint8_t lds[2 * S::kBytes + kWaves * R * 1024];
@@ -318,19 +316,33 @@ hipError_t launch_columns(const MxProduct& p, hipStream_t st) {
     return hipGetLastError();
 }
 
+// Time of a tile's super-chunk of 512 columns in us, 2 r row groups x 64 tokens: the
+// tokens' way to LDS and the row groups'.
+constexpr float column_time(int form, int r) {
+    return form == kMx4 ? 0.50f + 0.17f * r : form == kMx6 ? 0.67f + 0.15f * r : 0.86f + 0.16f * r;
+}
+
+// Row groups of the tiles that need the least time: whole rounds of the 256 CUs.
+float columns_best(const MxProduct& p, int* best) {
+    const int64_t groups = (row_groups(p.w.rows) * (p.wu.codes != nullptr ? 2 : 1) + 1) / 2;
+    const int64_t blocks = (p.n_live + 63) / 64;
+    const auto cost = [&](int r) {
+        return (float)(((groups + r - 1) / r * blocks + 255) / 256) * column_time(p.form, r);
+    };
+    const bool pairs = p.out.codes != nullptr;  // blocks of 32 features
+    *best = pairs ? 2 : 1;
+    for (int r : {2, 4, 5})
+        if ((!pairs || r % 2 == 0) && cost(r) < cost(*best)) *best = r;
+    return cost(*best);
+}
+
 template <int F, int T>
 hipError_t columns_rows(const MxProduct& p, hipStream_t st) {
-    // Rounds of 256 workgroups, each as long as its row groups and the tokens' own way.
-    const int64_t groups = (row_groups(p.w.rows) * (p.wu.codes != nullptr ? 2 : 1) + 1) / 2;
-    const int64_t blocks = (p.n_live + 16 * T - 1) / (16 * T);
-    const auto cost = [&](int64_t r) { return ((groups + r - 1) / r * blocks + 255) / 256 * (r + 1); };
-    const bool pairs = p.out.codes != nullptr;  // blocks of 32 features
-    int best = pairs ? 2 : 1;
-    for (int r : {2, 4, 5})
-        if ((!pairs || r % 2 == 0) && cost(r) < cost(best)) best = r;
-    if (best == 5) return launch_columns<F, T, 5>(p, st);
-    if (best == 4) return launch_columns<F, T, 4>(p, st);
-    if (best == 2) return launch_columns<F, T, 2>(p, st);
+    int r;
+    columns_best(p, &r);
+    if (r == 5) return launch_columns<F, T, 5>(p, st);
+    if (r == 4) return launch_columns<F, T, 4>(p, st);
+    if (r == 2) return launch_columns<F, T, 2>(p, st);
     return launch_columns<F, T, 1>(p, st);
 }
 
@@ -344,6 +356,11 @@ hipError_t columns_tokens(const MxProduct& p, hipStream_t st) {
 }
 
 }  // namespace
+
+float mx_columns_cost(const MxProduct& p) {
+    int r;
+    return columns_best(p, &r);
+}
 
 hipError_t launch_mx_columns(const MxProduct& p, hipStream_t st) {
     if (p.form == kMx4) return columns_tokens<kMx4>(p, st);

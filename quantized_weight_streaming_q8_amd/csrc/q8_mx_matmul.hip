@@ -281,7 +281,10 @@ hipError_t narrow_form(const NarrowArgs& n, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_mx_product(const MxProduct& p, hipStream_t st) {
-    if (p.n_live > 64) return launch_mx_wide(p, st);
+    // Up to 64 tokens the way of the weights bounds the time.  Above, blocks of 64
+    // fill the chip where few large tiles would not (7168 x 5120, MX8: 128 tokens 20.2 us
+    // against 37.5, 512 44 against 40), and cost more once both fill it.
+    if (p.n_live > 64 && mx_wide_cost(p) < mx_columns_cost(p)) return launch_mx_wide(p, st);
     if (p.n_live > 16) return launch_mx_columns(p, st);
     NarrowArgs n;
     n.p = p;

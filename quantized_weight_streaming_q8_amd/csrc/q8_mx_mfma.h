@@ -10,7 +10,6 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
-typedef uint32_t v6u __attribute__((ext_vector_type(6)));
 
 // One chunk (128 columns) of 16 tokens, and the scale bytes of a super-chunk's:
 // two pieces for MX8.  Members of their own, since arrays end up in scratch memory here.

@@ -1,12 +1,17 @@
 // q8_mx_prompt.hip -- products of MX4 weights with MX activations, and the gated
 // block, for many tokens: bound by the matrix cores.
 //
-// A workgroup of 8 waves, WN x WT, makes a tile of 16 WN RN rows x 16 WT RT tokens, each
-// wave RN x RT of the instruction's 16 x 16 tiles in registers.  Operands go from memory to
+// A workgroup of 8 waves, 2 x 4, makes a tile of 256 rows x 64 RT tokens, each wave
+// 8 x RT of the instruction's 16 x 16 tiles in registers.  Operands go from memory to
 // LDS past the registers, a chunk of 128 columns a stage, in the order in which the
 // instruction takes them (no bank conflicts, no address arithmetic); a stage is
-// loaded D stages ahead, so that its latency hides behind the products.
-// Scale bytes come a super-chunk (4 chunks) ahead, a part of them with each stage.
+// loaded D stages ahead, so that its latency hides behind the products, and its loads
+// go out one by one between them (all at a chunk's start they kept both waves of a SIMD
+// from their products: 41.2 instead of 38.5 us for 1024 tokens, MX4, 7168 x 5120).
+// A wave reads a token tile's operands while it multiplies the one before.  With MX8 the
+// products of the first pieces come before those of the second, so that none waits
+// for the one before it.  Scale bytes come a super-chunk (4 chunks) ahead, a part of
+// them with each stage.
 
 #include <utility>
 
@@ -16,12 +21,11 @@
 namespace q8 {
 namespace {
 
-constexpr int kWaves = 8;
+constexpr int kWaves = 8, WN = 2, WT = 4, RN = 8;
 
 // The shape of a workgroup's tile.
-template <int F, int WN, int WT, int RN, int RT, int kMaxStages = 4>
+template <int F, int RT>
 struct Tile {
-    static_assert(WN * WT == kWaves, "waves");
     static constexpr int TN = WN * RN, TT = WT * RT;  // row groups (of both projections together), token tiles
     static constexpr int PI = form_pieces(F);
     // 1 KB loads of the tokens: 16-byte parts of each piece, 8-byte parts of a tile's two
@@ -35,7 +39,7 @@ struct Tile {
     static constexpr int kLoadS = (kScales + 4 * kWaves - 1) / (4 * kWaves);
     static constexpr int kLoads = kLoadN + kLoadT + kLoadS;
     static constexpr int kFit = (160 * 1024 - 2 * kScales * 256 - TT * 64) / kBytes;
-    static constexpr int kStages = kFit > kMaxStages ? kMaxStages : kFit;
+    static constexpr int kStages = kFit > 4 ? 4 : kFit;
     static constexpr int kLds = kStages * kBytes + 2 * kScales * 256;
     static_assert(kStages >= 2, "two stages");
 };
@@ -47,10 +51,10 @@ struct WideArgs {
 };
 
 // P: projections (2: the gated block; a wave then has RN / 2 row groups of each).
-template <int F, int WN, int WT, int RN, int RT, int P, int kMaxStages>
+template <int F, int RT, int P>
 __global__ void __launch_bounds__(kWaves * 64, 2)
 mx_wide_kernel(WideArgs n) {
-    using S = Tile<F, WN, WT, RN, RT, kMaxStages>;
+    using S = Tile<F, RT>;
     constexpr int TN = S::TN, TT = S::TT, PI = S::PI, D = S::kStages - 1;
     __shared__ __attribute__((aligned(256))) uint8_t lds[S::kLds];
     __shared__ int slots[TT * 16];  // of the tile's tokens, -1: outside the buffer
@@ -153,29 +157,35 @@ mx_wide_kernel(WideArgs n) {
         }
     const uint32_t lds0 = lds_address(lds), scales0 = lds0 + S::kStages * S::kBytes;
     // Quarter q of the scales of super-chunk c.
-    const auto load_scales = [&](auto Q, int c) {
+    const auto load_scale = [&](auto Q, int m, int c) {
         constexpr int q = decltype(Q)::value;
         const int from = min(c, sc - 1);
+        const int item = min(q * kWaves + wave + 4 * kWaves * m, S::kScales - 1);
+        lds_load4(scales0 + ((c & 1) * S::kScales + item) * 256, sbase[q][m] + (int64_t)from * sstep[q][m], sat[q][m]);
+    };
+    const auto load_scales = [&](auto Q, int c) {
 #pragma unroll
-        for (int m = 0; m < S::kLoadS; ++m) {
-            const int item = min(q * kWaves + wave + 4 * kWaves * m, S::kScales - 1);
-            lds_load4(scales0 + ((c & 1) * S::kScales + item) * 256, sbase[q][m] + (int64_t)from * sstep[q][m],
-                      sat[q][m]);
-        }
+        for (int m = 0; m < S::kLoadS; ++m) load_scale(Q, m, c);
     };
     // Chunk c into stage c % kStages, and with it quarter Q = c % 4 of the next
     // super-chunk's scales.  Past the end the last chunk again: the counts stay.
-    const auto load_stage = [&](auto Q, int c, int stage) {
+    const auto load_item = [&](auto Q, int m, int c, int stage) {
+        constexpr int q = decltype(Q)::value;
         const uint32_t to = lds0 + stage * S::kBytes;
         const int from = min(c, kc - 1);
-#pragma unroll
-        for (int m = 0; m < S::kLoadN; ++m)
+        if (m < S::kLoadN) {
             lds_load16(to + min(wave + kWaves * m, TN - 1) * 1024, wbase[m] + (int64_t)from * 1024, lane * 16);
-        const uint8_t* src = p.x.codes + (int64_t)from * (chunk_bytes(F) * side);
+        } else if (m < S::kLoadN + S::kLoadT) {
+            const int i = m - S::kLoadN;
+            lds_load16(to + (TN + min(wave + kWaves * i, S::kTokens - 1)) * 1024,
+                       p.x.codes + (int64_t)from * (chunk_bytes(F) * side), at[i]);
+        } else {
+            load_scale(Q, m - S::kLoadN - S::kLoadT, c / 4 + 1);
+        }
+    };
+    const auto load_stage = [&](auto Q, int c, int stage) {
 #pragma unroll
-        for (int m = 0; m < S::kLoadT; ++m)
-            lds_load16(to + (TN + min(wave + kWaves * m, S::kTokens - 1)) * 1024, src, at[m]);
-        load_scales(Q, c / 4 + 1);
+        for (int m = 0; m < S::kLoads; ++m) load_item(Q, m, c, stage);
     };
 
     v4f acc[RN][RT];
@@ -203,7 +213,14 @@ mx_wide_kernel(WideArgs n) {
         wait_loads<(D - 1) * S::kLoads>();  // this one is here
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        load_stage(integral_constant<int, (j + D) & 3>(), c + D, stage == 0 ? S::kStages - 1 : stage - 1);
+        using Next = integral_constant<int, (j + D) & 3>;
+        const int to = stage == 0 ? S::kStages - 1 : stage - 1;
+        constexpr int kParts = 2, kBlocks = RT * PI * kParts;  // loads go out between them
+        const auto loads = [&](int b) {
+#pragma unroll
+            for (int m = b * S::kLoads / kBlocks; m < (b + 1) * S::kLoads / kBlocks; ++m) load_item(Next(), m, c + D, to);
+            __builtin_amdgcn_sched_barrier(0);
+        };
         if constexpr (j == 0) {
             const uint32_t* s = reinterpret_cast<const uint32_t*>(lds + S::kStages * S::kBytes +
                                                                   (c >> 2 & 1) * S::kScales * 256);
@@ -219,9 +236,7 @@ mx_wide_kernel(WideArgs n) {
         v4u a[RN];
 #pragma unroll
         for (int r = 0; r < RN; ++r) a[r] = *reinterpret_cast<const v4u*>(here + (wn * RN + r) * 1024 + lane * 16);
-#pragma unroll
-        for (int t = 0; t < RT; ++t) {
-            Tokens x;
+        const auto fetch = [&](Tokens& x, int t) {
             const int tile = wt * RT + t;
             const uint8_t* b = here + TN * 1024;
             const uint8_t* b8 = b + S::kParts16 * 1024;
@@ -237,8 +252,26 @@ mx_wide_kernel(WideArgs n) {
                 x.b00 = y[0];
                 x.b01 = y[1];
             }
+        };
+        Tokens x[2];
+        fetch(x[0], 0);
 #pragma unroll
-            for (int r = 0; r < RN; ++r) acc[r][t] = multiply<F, j>(a[r], ws[r], x, xs[t], acc[r][t]);
+        for (int t = 0; t < RT; ++t) {
+            if (t + 1 < RT) fetch(x[(t + 1) & 1], t + 1);
+            __builtin_amdgcn_sched_barrier(0);
+            const Tokens& q = x[t & 1];
+#pragma unroll
+            for (int k = 0; k < PI; ++k)
+#pragma unroll
+                for (int h = 0; h < kParts; ++h) {
+                    loads((t * PI + k) * kParts + h);
+#pragma unroll
+                    for (int r = h * RN / kParts; r < (h + 1) * RN / kParts; ++r)
+                        acc[r][t] = multiply_piece<F == kMx4 ? 4 : 2, j>(a[r], ws[r], k ? q.a1 : q.a0, k ? q.b10 : q.b00,
+                                                                         k ? q.b11 : q.b01, k ? xs[t].s1 : xs[t].s0,
+                                                                         acc[r][t]);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
         }
         stage = stage + 1 == S::kStages ? 0 : stage + 1;
     };
@@ -266,7 +299,7 @@ mx_wide_kernel(WideArgs n) {
     // neighbours would write to 16 rows.  In two passes where all do not fit.
     constexpr int kRows = WN * RH * 16, kRow = kRows + 4;  // floats of a token, 4 more against bank conflicts
     constexpr int kPasses = TT * 16 * kRow * 4 <= S::kLds ? 1 : 2, kPassT = RT / kPasses;
-    static_assert(WT * kPassT * 16 * kRow * 4 <= S::kLds, "results fit");
+    static_assert(RT % kPasses == 0 && WT * kPassT * 16 * kRow * 4 <= S::kLds, "results fit");
     float* h = reinterpret_cast<float*>(lds);
     const int64_t f0 = (int64_t)nt * kRows;
 #pragma unroll
@@ -307,9 +340,9 @@ mx_wide_kernel(WideArgs n) {
     }
 }
 
-template <int F, int WN, int WT, int RN, int RT, int kMaxStages = 4>
+template <int F, int RT>
 hipError_t launch_wide(const MxProduct& p, hipStream_t st) {
-    using S = Tile<F, WN, WT, RN, RT, kMaxStages>;
+    using S = Tile<F, RT>;
     WideArgs n;
     n.p = p;
     const bool two = p.wu.codes != nullptr;
@@ -319,24 +352,43 @@ hipError_t launch_wide(const MxProduct& p, hipStream_t st) {
     n.vec = (reinterpret_cast<uintptr_t>(p.Y) & 15) == 0 && p.y_stride % 4 == 0;
     const int64_t total = (int64_t)n.n_tiles * n.t_tiles;
     const dim3 grid((unsigned)((total + 7) / 8 * 8)), block(kWaves * 64);
-    if (two) mx_wide_kernel<F, WN, WT, RN, RT, 2, kMaxStages><<<grid, block, 0, st>>>(n);
-    else mx_wide_kernel<F, WN, WT, RN, RT, 1, kMaxStages><<<grid, block, 0, st>>>(n);
+    if (two) mx_wide_kernel<F, RT, 2><<<grid, block, 0, st>>>(n);
+    else mx_wide_kernel<F, RT, 1><<<grid, block, 0, st>>>(n);
     return hipGetLastError();
 }
 
-template <int F>
-hipError_t wide_shape(const MxProduct& p, hipStream_t st) {
-    if (p.n_live <= 32) return launch_wide<F, 4, 2, 4, 1>(p, st);
-    if (p.n_live <= 64) return launch_wide<F, 4, 2, 4, 2>(p, st);
-    return launch_wide<F, 2, 4, 8, 4>(p, st);
+// Time of a tile's super-chunk of 512 columns in us, 256 rows x 64 RT tokens.
+constexpr float wide_time(int form, int rt) {
+    if (rt == 4) return form == kMx4 ? 2.7f : 3.0f;
+    return form == kMx4 ? 1.8f : form == kMx6 ? 2.0f : 2.8f;
+}
+
+// Tokens of the tiles that need the least time: whole rounds of the 256 CUs.  MX8
+// has the small ones alone: two of them take 5.6 us, a large one, whose stages leave
+// room for only two, 5.8.
+float wide_best(const MxProduct& p, int* best) {
+    const int64_t rows = (p.w.rows * (p.wu.codes != nullptr ? 2 : 1) + 255) / 256;
+    const auto cost = [&](int rt) {
+        const int64_t tiles = rows * ((p.n_live + 64 * rt - 1) / (64 * rt));
+        return (float)((tiles + 255) / 256) * wide_time(p.form, rt);
+    };
+    *best = p.form != kMx8 && cost(4) <= cost(2) ? 4 : 2;
+    return cost(*best);
 }
 
 }  // namespace
 
+float mx_wide_cost(const MxProduct& p) {
+    int rt;
+    return wide_best(p, &rt);
+}
+
 hipError_t launch_mx_wide(const MxProduct& p, hipStream_t st) {
-    if (p.form == kMx4) return wide_shape<kMx4>(p, st);
-    if (p.form == kMx6) return wide_shape<kMx6>(p, st);
-    return wide_shape<kMx8>(p, st);
+    int rt;
+    wide_best(p, &rt);
+    if (p.form == kMx4) return rt == 4 ? launch_wide<kMx4, 4>(p, st) : launch_wide<kMx4, 2>(p, st);
+    if (p.form == kMx6) return rt == 4 ? launch_wide<kMx6, 4>(p, st) : launch_wide<kMx6, 2>(p, st);
+    return launch_wide<kMx8, 2>(p, st);
 }
 
 }  // namespace q8
