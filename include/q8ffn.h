@@ -32,9 +32,9 @@
  * which the host cannot check, is never read through out of range.
  * Shapes: N >= 1, K a multiple of 32, 32..2^20; a weight matrix padded to whole
  * groups of 16 rows and 128 columns holds at most 2^34 values, an activation
- * buffer, its rows padded to 512 columns, at most 2^31.  Buffers are 256-byte aligned, fp32 and int32
- * pointers 4 bytes unless it says otherwise.  Outputs must not overlap inputs
- * unless it says so.
+ * buffer, its rows padded to 512 columns, at most 2^31.  Buffers are 256-byte
+ * aligned, fp32 and int32 pointers 4 bytes unless it says otherwise.  Outputs
+ * must not overlap inputs unless it says so.
  */
 #ifndef Q8FFN_H
 #define Q8FFN_H
@@ -104,7 +104,7 @@ q8_status q8_mx_quantize_acts(const float* X, int64_t x_stride, int n_rows, cons
 
 /* The values an MX buffer holds: X [n_rows][K], row t from slot batch_index[t]
  * (NULL: slot t, n_rows <= n_slots).  A slot outside the buffer gives NaN.
- * 1 <= n_rows <= 2^20. */
+ * 1 <= n_rows <= 2^20, n_rows * K <= 2^33. */
 q8_status q8_mx_read_acts(const q8_acts* Xm, const int32_t* batch_index, int n_rows, float* X,
                           hipStream_t stream);
 
@@ -117,9 +117,10 @@ q8_status q8_mx_read_acts(const q8_acts* Xm, const int32_t* batch_index, int n_r
  * for slot t (then n_live <= n_slots).  A token whose slot lies outside the
  * buffer gets a row of NaN.  1 <= n_live <= 2^20.
  *
- * Products are exact, sums are fp32.  Up to 64 tokens the weights are read
- * once and a row's bits depend on that row and (N, K) alone; above, the matrix is
- * cut into tiles, and the order of the sums is another. */
+ * Products are exact, sums are fp32.  A row's bits depend on that row, the weights,
+ * K and which of three orders of the sums the call takes: one up to 16 tokens, one
+ * in blocks of 64, one in large tiles (for more than 64 tokens, by N and n_live).
+ * n_live * N <= 2^36. */
 q8_status q8_mx4_matmul(const q8_mx4_weights* Wm, const q8_acts* Xm, const int32_t* batch_index,
                         int n_live, float* Y, int64_t y_stride, hipStream_t stream);
 

@@ -276,16 +276,81 @@ def test_output_rows_at_a_stride(q8):
             assert (got[:-1, 45:] == 7).all() and (host(y)[off + live * stride - stride + 45:] == 7).all()
 
 
+# Large tiles (enough of them that blocks of 64 tokens take longer), small and large, with
+# ends in both directions: by cost, not by these sizes.
 @pytest.mark.parametrize("form", FORMS)
-def test_a_row_up_to_64_does_not_depend_on_the_others(q8, form):
+@pytest.mark.parametrize("n,k,live", [(2077, 544, 1290), (4093, 160, 3701), (2080, 96, 3700), (7001, 1184, 515)])
+def test_product_in_large_tiles(q8, form, n, k, live):
+    codes, scales, w, x = integer_case(n + live, form, n, k, 700)
+    index = np.random.default_rng(live).integers(0, 700, live)
+    index[[3, live - 1]] = [-1, 700]
+    y = torch.full((live + 1, n), 7.0, device="cuda")
+    q8.q8_mx4_matmul(weights_of(q8, codes, scales), acts_of(q8, x, form), i32(index), live, y)
+    got = host(y)
+    good = np.ones(live + 1, bool)
+    good[[3, live - 1, live]] = False
+    assert np.isnan(got[[3, live - 1]]).all() and (got[live] == 7).all()
+    want = (x.astype(np.float64) @ w.T)[index[good[:live]]]
+    assert np.array_equal(got[good].astype(np.float64), want)
+
+
+# Super-chunks of 512 columns: 13 and 16 (two a wave, kept), 18 and 34 (fetched again), odd ones.
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("n,k", [(53, 6176), (53, 6432), (40, 8192), (53, 8736), (33, 17408), (530, 6688)])
+def test_product_and_gated_of_wide_rows(q8, form, n, k):
+    codes, scales, w, x = integer_case(k, form, n, k, 21)
+    for live in (1, 16, 21):
+        y = torch.empty(live, n, device="cuda")
+        q8.q8_mx4_matmul(weights_of(q8, codes, scales), acts_of(q8, x, form), None, live, y)
+        assert np.array_equal(host(y).astype(np.float64), x[:live].astype(np.float64) @ w.T)
+        h = torch.empty(live, n, device="cuda")
+        one = weights_of(q8, codes, scales)
+        q8.q8_mx4_gated(one, one, acts_of(q8, x, form), None, live, H=h, activation="identity")
+        v = (x[:live].astype(np.float64) @ w.T).astype(np.float32)
+        assert np.array_equal(host(h), v * v)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("slots", [64, 65, 700])
+def test_the_same_rows_in_buffers_of_any_size(q8, form, slots):
+    codes, scales, w, x = integer_case(slots, form, 97, 1312, slots)
+    a, m = acts_of(q8, x, form), weights_of(q8, codes, scales)
+    assert same(values(q8, a), x)
+    want = x.astype(np.float64) @ w.T
+    for live in (1, 9, 16, 17, 33, 64, 80):
+        for index in (np.random.default_rng(live).integers(0, slots, live), np.full(live, slots - 1),
+                      np.arange(live)[::-1] % slots):
+            y = torch.empty(live, 97, device="cuda")
+            q8.q8_mx4_matmul(m, a, i32(index), live, y)
+            assert np.array_equal(host(y).astype(np.float64), want[index]), live
+            h, held = torch.empty(live, 97, device="cuda"), q8.Acts(slots, 96, form)
+            q8.q8_mx4_gated(m, m, a, i32(index), live, H=h, activation="identity")
+            v = want[index].astype(np.float32)
+            assert np.array_equal(host(h), v * v), live
+    few = q8.MX4Weights(96, 1312)
+    q8.q8_mx4_pack_weights_q(to_dev(codes[:96]), to_dev(scales[:96]), few)
+    for live in (9, 40):
+        held, want_held = (q8.Acts(slots, 96, form) for _ in range(2))
+        for b in (held, want_held):
+            b.data.fill_(0x29)
+        h = torch.empty(live, 96, device="cuda")
+        q8.q8_mx4_gated(few, few, a, None, live, H=h, h_acts=held)
+        q8.q8_mx_quantize_acts(h, live, want_held)
+        assert torch.equal(held.data, want_held.data)
+
+
+# The order of a row's sums is one up to 16 tokens, another in blocks of 64.
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("most,lives", [(16, (1, 5, 15)), (130, (17, 33, 40, 63, 64, 100))])
+def test_a_row_does_not_depend_on_the_others(q8, form, most, lives):
     n, k = 70, 2592
-    x, wf = rows(18, 64, k), rows(19, n, k)
+    x, wf = rows(18, most, k, 3.0), rows(19, n, k, 3.0)
     w, a = q8.MX4Weights(n, k), acts_of(q8, x, form)
     q8.q8_mx4_pack_weights(to_dev(wf), w)
-    full = torch.empty(64, n, device="cuda")
-    q8.q8_mx4_matmul(w, a, None, 64, full)
-    for live in (1, 16, 17, 40, 63):
-        index = np.random.default_rng(live).permutation(64)[:live]
+    full = torch.empty(most, n, device="cuda")
+    q8.q8_mx4_matmul(w, a, None, most, full)
+    for live in lives:
+        index = np.random.default_rng(live).permutation(most)[:live]
         y = torch.empty(live, n, device="cuda")
         q8.q8_mx4_matmul(w, a, i32(index), live, y)
         assert torch.equal(y, full[torch.from_numpy(index).cuda()])
@@ -333,6 +398,37 @@ def test_gated_quantised_rows_are_the_quantised_fp32_rows(q8, form, out, n, k, l
     q8.q8_mx4_gated(*w, a, None, live, h_acts=alone)
     q8.q8_mx_quantize_acts(h, live, want)
     assert torch.equal(both.data, want.data) and torch.equal(alone.data, want.data)
+
+
+@pytest.mark.parametrize("kind", ACTIVATIONS)
+@pytest.mark.parametrize("n,k,live,form", [(1050, 288, 1300, "mx8"), (4095, 96, 1900, "mx4"), (4095, 96, 1900, "mx8")])
+def test_gated_in_large_tiles(q8, kind, n, k, live, form):
+    wf = [(rows(24 + i, n, k, 0.3) * np.float32(3 / k ** 0.5)) for i in range(2)]
+    x = rows(26, 90, k, 0.3)
+    x[0] *= 8
+    w = [q8.MX4Weights(n, k) for _ in wf]
+    for a, b in zip(wf, w):
+        q8.q8_mx4_pack_weights(to_dev(a), b)
+    index = np.random.default_rng(n).integers(0, 90, live)
+    h = torch.empty(live, n, device="cuda")
+    q8.q8_mx4_gated(*w, acts_of(q8, x, form), i32(index), live, H=h, activation=kind)
+    want, tol = ref.gated(*(ref.hold(a, "mx4") for a in wf), ref.hold(x, form), PIECES[form], kind)
+    assert (np.abs(host(h) - want[index]) <= tol[index]).all()
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("n,k,live", [(4096, 96, 1900), (1056, 160, 1300)])
+def test_gated_quantised_rows_in_large_tiles(q8, form, n, k, live):
+    w = [q8.MX4Weights(n, k) for _ in range(2)]
+    for i, b in enumerate(w):
+        q8.q8_mx4_pack_weights(to_dev(rows(36 + i, n, k) * np.float32(2 / k ** 0.5)), b)
+    a = acts_of(q8, rows(38, live, k), form)
+    for out in FORMS:
+        h, both, want = torch.empty(live, n, device="cuda"), q8.Acts(live + 20, n, out), q8.Acts(live + 20, n, out)
+        both.data.fill_(0x41), want.data.fill_(0x41)
+        q8.q8_mx4_gated(*w, a, None, live, H=h, h_acts=both)
+        q8.q8_mx_quantize_acts(h, live, want)
+        assert torch.equal(both.data, want.data)
 
 
 @pytest.mark.parametrize("live", [9, 150])
