@@ -4,7 +4,8 @@ in-tree with hipcc for gfx950.
 Flags: -O3, no fast-math, -ffp-contract=off (every fused multiply-add in the
 kernels is written out explicitly), and packed-fp32 instructions disabled.
 The timeline build adds -DQ8_TIMELINE (per-wave real-time counter records,
-include/q8timeline.h); nothing else differs.
+include/q8timeline.h); nothing else differs.  The sources are compiled side by
+side, each to an object of its own, and linked.
 """
 
 from __future__ import annotations
@@ -12,6 +13,8 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -20,9 +23,10 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(HERE, "libq8narrow.so")
 TIMELINE_LIB_PATH = os.path.join(HERE, "libq8narrow_timeline.so")
 
-SOURCES = ["q8_pack.hip", "q8_matmul.hip", "q8_rope.hip", "q8_measure.hip", "q8_abi.hip",
-           "q8_noalloc.hip", "q8_kv4_rows.hip", "q8_kv4_attend.hip", "q8_kv4_abi.hip",
-           "q8_mx_rows.hip", "q8_mx_matmul.hip", "q8_mx_columns.hip", "q8_mx_prompt.hip", "q8_norm.hip", "q8_ffn_abi.hip"]
+# the longest to compile first
+SOURCES = ["q8_mx_columns.hip", "q8_matmul.hip", "q8_kv4_attend.hip", "q8_mx_matmul.hip", "q8_mx_prompt.hip",
+           "q8_norm.hip", "q8_pack.hip", "q8_rope.hip", "q8_measure.hip", "q8_abi.hip", "q8_noalloc.hip",
+           "q8_kv4_rows.hip", "q8_kv4_abi.hip", "q8_mx_rows.hip", "q8_ffn_abi.hip"]
 HEADERS = ["q8_internal.h", "q8_measure.h", "q8_kv4_internal.h", "q8_kv4_shares.h",
            "q8_ffn_internal.h", "q8_mx_mfma.h", "q8_lds.h"]
 
@@ -50,39 +54,44 @@ def _filtered(text: str) -> str:
         if "packed-fp32-ops" not in line and "is not a recognized feature" not in line)
 
 
-def _start(out: str, extra_flags: list[str], verbose: bool) -> tuple:
-    srcs = [os.path.join(CSRC, s) for s in SOURCES]
-    tmp = out + ".tmp"
-    cmd = [HIPCC, *FLAGS, *extra_flags, "-shared", "-o", tmp, *srcs]
+def _run(cmd: list[str], what: str, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
-    proc = subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
-    return proc, tmp, out
-
-
-def _finish(job: tuple, verbose: bool) -> str:
-    proc, tmp, out = job
-    text, _ = proc.communicate()
-    msgs = _filtered(text)
+    proc = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    msgs = _filtered(proc.stdout)
     if proc.returncode != 0:
-        raise RuntimeError(f"hipcc failed ({proc.returncode}) building {out}:\n{msgs}")
+        raise RuntimeError(f"hipcc failed ({proc.returncode}) building {what}:\n{msgs}")
     if verbose and msgs.strip():
         print(msgs, file=sys.stderr)
-    os.replace(tmp, out)
-    return out
+
+
+def _build(libs: list[tuple[str, list[str]]], verbose: bool) -> list[str]:
+    """Libraries (path, extra flags), all their objects compiled side by side."""
+    with tempfile.TemporaryDirectory() as tmp, ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+        jobs = []
+        for s in SOURCES:
+            for i, (_, extra) in enumerate(libs):
+                obj = os.path.join(tmp, f"{i}_{s}.o")
+                cmd = [HIPCC, *FLAGS, *extra, "-c", os.path.join(CSRC, s), "-o", obj]
+                jobs.append((i, obj, pool.submit(_run, cmd, s, verbose)))
+        for _, _, job in jobs:
+            job.result()
+        for i, (out, extra) in enumerate(libs):
+            objs = [obj for k, obj, _ in jobs if k == i]
+            _run([HIPCC, *FLAGS, *extra, "-shared", "-o", out + ".tmp", *objs], out, verbose)
+            os.replace(out + ".tmp", out)
+    return [out for out, _ in libs]
 
 
 def build(out: str = LIB_PATH, extra_flags: list[str] | None = None,
           verbose: bool = False) -> str:
     """Compile every source into one shared library at ``out``."""
-    return _finish(_start(out, list(extra_flags or []), verbose), verbose)
+    return _build([(out, list(extra_flags or []))], verbose)[0]
 
 
 def build_all(verbose: bool = False) -> list[str]:
-    """The product library and its timeline build, compiled side by side."""
-    jobs = [_start(LIB_PATH, [], verbose),
-            _start(TIMELINE_LIB_PATH, ["-DQ8_TIMELINE"], verbose)]
-    return [_finish(j, verbose) for j in jobs]
+    """The product library and its timeline build."""
+    return _build([(LIB_PATH, []), (TIMELINE_LIB_PATH, ["-DQ8_TIMELINE"])], verbose)
 
 
 if __name__ == "__main__":
