@@ -679,3 +679,17 @@ def test_two_streams_at_once(q8):
     for i in (0, 1):
         assert torch.equal(blocks[i].stream, blocks[i + 2].stream)
         assert torch.equal(blocks[i].next.data, blocks[i + 2].next.data)
+
+
+def test_decode_feed_forward_example():
+    """The example runs and stays finite."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "decode_feed_forward.py")
+    spec = importlib.util.spec_from_file_location("decode_feed_forward", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    for form in FORMS:
+        out = mod.main(["--live", "3", "--steps", "5", "--format", form])
+        assert out["finite"] and out["format"] == form
