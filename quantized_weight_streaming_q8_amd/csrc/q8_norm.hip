@@ -74,10 +74,13 @@ __device__ inline v4f load_unit(const float* p, int K, int u, bool vec) {
     return v;
 }
 
-__device__ inline void store_unit(float* p, int K, int u, bool vec, v4f v) {
+// far: past the caches, which an output of this size leaves before it is read.
+__device__ inline void store_unit(float* p, int K, int u, bool vec, bool far, v4f v) {
     const int k = u * 4;
     if (k >= K) return;
-    if (vec) {
+    if (vec && far) {
+        __builtin_nontemporal_store(v, reinterpret_cast<v4f*>(p + k));
+    } else if (vec) {
         *reinterpret_cast<v4f*>(p + k) = v;
     } else {
 #pragma unroll
@@ -86,8 +89,9 @@ __device__ inline void store_unit(float* p, int K, int u, bool vec, v4f v) {
     }
 }
 
-struct Vec {  // 16-byte accesses
+struct Access {  // 16-byte accesses
     bool x, r, gate, r_out, y, post_w, post_b, pre_w, pre_b;
+    bool far;  // stores past the caches
 };
 
 // A norm's weights and biases of this thread's units.
@@ -146,12 +150,14 @@ __device__ inline double normed(float x, double mean, double inv, const NormView
     return y;
 }
 
-// Early: every input is fetched before the first statistics, where the registers allow it:
-// short rows' time is the latency of what is fetched one after the other (with three
-// units a thread it costs occupancy, 154 us against 93 for 4099 rows of 5120).
-template <int NW, int V, bool Early>
-__global__ void __launch_bounds__(NW * 64)
-norm_step_kernel(NormStep s, Vec vec, int units) {
+// One unit a thread: every input is fetched before the first statistics, since a short row's
+// time is the latency of what is fetched one after the other.  More units leave the registers
+// to occupancy instead (4099 rows of 4096: 80 us with all inputs early, 67 without; of 5120:
+// 154 and 93): 6 waves a SIMD, which the compiler's own 82 registers just missed (109 us; with
+// 64, for 8 waves, it spills: 147).
+template <int NW, int V>
+__global__ void __launch_bounds__(NW * 64, NW == 8 && (V == 2 || V == 3) ? 6 : 1)
+norm_step_kernel(NormStep s, Access vec, int units) {
     __shared__ double part[2 * NW];
     const int64_t row = blockIdx.x;
     Row<NW, V> m{(int)s.K, s.rK, part, 0};
@@ -163,13 +169,14 @@ norm_step_kernel(NormStep s, Vec vec, int units) {
         if (s.gate) m.load(g, s.gate + row * s.gate_stride, vec.gate);
         m.load(post, s.post, row, vec.post_w, vec.post_b);
     };
-    if constexpr (Early) {
+    constexpr bool kEarly = V == 1;
+    if constexpr (kEarly) {
         load_rest();
         m.load(pre, s.pre, row, vec.pre_w, vec.pre_b);
     }
     double mean = 0.0, inv = 1.0;
     if (s.post.kind >= 0) m.statistics(x, s.post, mean, inv);
-    if constexpr (!Early) load_rest();
+    if constexpr (!kEarly) load_rest();
 #pragma unroll
     for (int i = 0; i < V; ++i) {
 #pragma unroll
@@ -180,12 +187,12 @@ norm_step_kernel(NormStep s, Vec vec, int units) {
             if (s.R) b += (double)r[i][j];
             x[i][j] = m.unit(i) * 4 + j < m.K ? (float)b : 0.0f;
         }
-        if (s.R_out) store_unit(s.R_out + row * s.r_out_stride, m.K, m.unit(i), vec.r_out, x[i]);
+        if (s.R_out) store_unit(s.R_out + row * s.r_out_stride, m.K, m.unit(i), vec.r_out, vec.far, x[i]);
     }
     if (s.Y == nullptr && s.acts.codes == nullptr) return;
     mean = 0.0, inv = 1.0;
     if (s.pre.kind >= 0) m.statistics(x, s.pre, mean, inv);
-    if constexpr (!Early) m.load(pre, s.pre, row, vec.pre_w, vec.pre_b);
+    if constexpr (!kEarly) m.load(pre, s.pre, row, vec.pre_w, vec.pre_b);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int u = m.unit(i);
@@ -196,7 +203,7 @@ norm_step_kernel(NormStep s, Vec vec, int units) {
             for (int j = 0; j < 4; ++j)
                 y[j] = u * 4 + j < m.K ? (float)normed(x[i][j], mean, inv, s.pre, pre.w[i][j], pre.b[i][j]) : 0.0f;
         }
-        if (s.Y) store_unit(s.Y + row * s.y_stride, m.K, u, vec.y, y);
+        if (s.Y) store_unit(s.Y + row * s.y_stride, m.K, u, vec.y, vec.far, y);
         if (s.acts.codes == nullptr) continue;
         const int b = u >> 3, p = u & 7;
         const float v[4] = {y[0], y[1], y[2], y[3]};
@@ -215,9 +222,9 @@ norm_step_kernel(NormStep s, Vec vec, int units) {
     }
 }
 
-template <int NW, int V, bool Early>
-hipError_t launch(const NormStep& s, const Vec& vec, int units, hipStream_t st) {
-    norm_step_kernel<NW, V, Early><<<dim3((unsigned)s.n_rows), dim3(NW * 64), 0, st>>>(s, vec, units);
+template <int NW, int V>
+hipError_t launch(const NormStep& s, const Access& vec, int units, hipStream_t st) {
+    norm_step_kernel<NW, V><<<dim3((unsigned)s.n_rows), dim3(NW * 64), 0, st>>>(s, vec, units);
     return hipGetLastError();
 }
 
@@ -228,7 +235,7 @@ bool wide(const void* p, int64_t stride, int64_t K) {
 }  // namespace
 
 hipError_t launch_norm_step(const NormStep& s, hipStream_t st) {
-    Vec v;
+    Access v;
     v.x = wide(s.X, s.x_stride, s.K);
     v.r = wide(s.R, s.r_stride, s.K);
     v.gate = wide(s.gate, s.gate_stride, s.K);
@@ -238,28 +245,31 @@ hipError_t launch_norm_step(const NormStep& s, hipStream_t st) {
     v.post_b = wide(s.post.bias, s.post.bias_stride, s.K);
     v.pre_w = wide(s.pre.weight, s.pre.weight_stride, s.K);
     v.pre_b = wide(s.pre.bias, s.pre.bias_stride, s.K);
+    // From the size of the L2s on stores go past them (4099 rows of 5120: 87.8 us against
+    // 93.3; below, the next kernel finds the rows there).
+    v.far = (int64_t)s.n_rows * s.K * 4 >= 32 << 20;
     // the row in units, with the padding that the quantised form has
     int64_t width = s.K;
     if (s.acts.codes != nullptr) width = s.acts_form == kQ80 ? s.q80_sc * kScValues : (int64_t)s.acts.kc * kMxChunk;
     const int units = (int)((width + 3) / 4);
-    // 8 waves to a row (4099 rows of 5120: 93 us, with 4 waves 106, with 16 129; 16 rows 7.0
-    // and 7.1 with 16), as long as 4 units a thread are enough.
-    if (units <= 64) return launch<1, 1, true>(s, v, units, st);
-    if (units <= 256) return launch<4, 1, true>(s, v, units, st);
+    // 8 waves to a row (4099 rows of 5120 before the stores: 93 us, with 4 waves 106, with 16
+    // 129; 16 rows 7.0 and 7.1 with 16), as long as 4 units a thread are enough.
+    if (units <= 64) return launch<1, 1>(s, v, units, st);
+    if (units <= 256) return launch<4, 1>(s, v, units, st);
     switch ((units + 511) / 512) {
-        case 1: return launch<8, 1, true>(s, v, units, st);
-        case 2: return launch<8, 2, true>(s, v, units, st);
-        case 3: return launch<8, 3, false>(s, v, units, st);
-        case 4: return launch<8, 4, false>(s, v, units, st);
+        case 1: return launch<8, 1>(s, v, units, st);
+        case 2: return launch<8, 2>(s, v, units, st);
+        case 3: return launch<8, 3>(s, v, units, st);
+        case 4: return launch<8, 4>(s, v, units, st);
         default: break;
     }
     switch ((units + 1023) / 1024) {
-        case 3: return launch<16, 3, false>(s, v, units, st);
-        case 4: return launch<16, 4, false>(s, v, units, st);
-        case 5: return launch<16, 5, false>(s, v, units, st);
-        case 6: return launch<16, 6, false>(s, v, units, st);
-        case 7: return launch<16, 7, false>(s, v, units, st);
-        default: return launch<16, 8, false>(s, v, units, st);
+        case 3: return launch<16, 3>(s, v, units, st);
+        case 4: return launch<16, 4>(s, v, units, st);
+        case 5: return launch<16, 5>(s, v, units, st);
+        case 6: return launch<16, 6>(s, v, units, st);
+        case 7: return launch<16, 7>(s, v, units, st);
+        default: return launch<16, 8>(s, v, units, st);
     }
 }
 
