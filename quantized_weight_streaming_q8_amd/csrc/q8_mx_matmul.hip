@@ -11,6 +11,12 @@
 // (a gate's and the up projection's, or two neighbours), the next pair's weights on
 // their way while one is multiplied.  The waves' sums meet in LDS, where they are added
 // in order: the tree depends on K alone.
+//
+// Measured with 16 tokens, MX8: 7168 x 5120 8.2 us, the gated block of 17408 x 5120 23.3
+// (4.1 TB/s), 151936 x 5120 71 (5.9): 7.0 TB/s, a large read's rate, and 6.5 us that are
+// the launch, the first loads' latency and the sums' way.  Weights are read past the caches: of a
+// model's layers none is there when its turn comes (three gated blocks in turn, 289 MB: 23.3
+// us and 20.4 through the caches, which keep a part of so few; eight: 22.3 and 23.7).
 
 #include <algorithm>
 #include <utility>

@@ -12,6 +12,12 @@
 // products of the first pieces come before those of the second, so that none waits
 // for the one before it.  Scale bytes come a super-chunk (4 chunks) ahead, a part of
 // them with each stage.
+//
+// Measured, 7168 x 5120 (MX4 / MX6 / MX8): 4099 tokens 92 / 108 / 172 us = 3.3 / 2.8 / 1.7
+// PFLOP/s of the result, the matrix instructions alone, in the same rounds, 68 us (MX4);
+// the gated block of 17408 features, 2053 tokens, MX8: 406 us.  What is between: 10 to
+// 20% for the stages' way into LDS, as much for the operands' way out of it, 6 us a tile
+// for its results, and the last round of tiles.
 
 #include <utility>
 
