@@ -13,8 +13,8 @@
 //   rows (larger buffers): a slot's row is consecutive bytes, since tokens take
 //     slots in any order and a tile's 16 bytes of each would be a line each: 4099
 //     tokens in a random order fetched 3.5 times as many 128-byte lines from tiles, and
-//     the product took 152 us against 98.  Within a tile any order is the same lines: for
-//     16 tokens 8.0 us against 13.4.
+//     the product took 152 us against, then, 98.  Within a tile any order is the same lines: for
+//     16 tokens 8.0 us against, then, 13.4.
 // Per row and chunk, in the order of rows (times 16 in tiles):
 //   MX4  64 bytes: blocks 0..3, 16 bytes each, the even value of a byte low;
 //   MX6  96: the first 16 of each block's 24 bytes (32 codes of 6 bits, in order),

@@ -12,11 +12,11 @@
 // their way while one is multiplied.  The waves' sums meet in LDS, where they are added
 // in order: the tree depends on K alone.
 //
-// Measured with 16 tokens, MX8: 7168 x 5120 8.2 us, the gated block of 17408 x 5120 23.3
-// (4.1 TB/s), 151936 x 5120 71 (5.9): 7.0 TB/s, a large read's rate, and 6.5 us that are
-// the launch, the first loads' latency and the sums' way.  Weights are read past the caches: of a
-// model's layers none is there when its turn comes (three gated blocks in turn, 289 MB: 23.3
-// us and 20.4 through the caches, which keep a part of so few; eight: 22.3 and 23.7).
+// Measured with 16 tokens, MX8: 7168 x 5120 6.9 us, the gated block of 17408 x 5120 20.9 to
+// 22.0 (4.4 to 4.6 TB/s), 151936 x 5120 68.6 (6.2): 7.0 TB/s, a large read's rate, and 5 to 6
+// us that are the launch, the first loads' latency and the sums' way.  Weights are read
+// past the caches: of a model's layers none is there when its turn comes (eight gated blocks in
+// turn 22.3 us, through the caches 23.7; the 151936 rows 71.0 and 77.6).
 
 #include <algorithm>
 #include <utility>

@@ -310,6 +310,20 @@ def test_product_and_gated_of_wide_rows(q8, form, n, k):
         assert np.array_equal(host(h), v * v)
 
 
+# Long rows, the most tokens, 2^20 rows.  Signs are random, so that a partial sum of 2^17
+# products of at most 12 x 127 units has a deviation of at most 2^8.5 x 1524 = 5.6e5: 2^24 are 30.
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("n,k,live", [(17, 1 << 17, 3), (17, 1 << 17, 40), (16, 32, 1 << 20), (1 << 20, 32, 3),
+                                      (1 << 20, 32, 33)])
+def test_product_at_the_ends_of_its_ranges(q8, form, n, k, live):
+    codes, scales, w, x = integer_case(n + live, form, n, k, 50)
+    index = np.random.default_rng(live).integers(0, 50, live)
+    y = torch.empty(live, n, device="cuda")
+    q8.q8_mx4_matmul(weights_of(q8, codes, scales), acts_of(q8, x, form), i32(index), live, y)
+    want = (x.astype(np.float64) @ w.T).astype(np.float32)
+    assert torch.equal(y, to_dev(want)[torch.from_numpy(index).cuda()])
+
+
 @pytest.mark.parametrize("form", FORMS)
 @pytest.mark.parametrize("slots", [64, 65, 700])
 def test_the_same_rows_in_buffers_of_any_size(q8, form, slots):
