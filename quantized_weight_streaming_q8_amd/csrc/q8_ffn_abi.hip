@@ -174,11 +174,10 @@ q8_status q8_norm_step(const float* X, int64_t x_stride, const q8_norm* post, co
         (Y != nullptr && (!aligned(Y, 4) || !valid_stride(y_stride, K, n_rows))))
         return Q8_ERR_INVALID_ARG;
     // in place: the same rows, one output to a row
-    for (const auto& in : {X, R}) {
-        const int64_t stride = in == X ? x_stride : r_stride;
-        if (in != nullptr && ((in == R_out && stride != r_out_stride) || (in == Y && stride != y_stride)))
-            return Q8_ERR_INVALID_ARG;
-    }
+    const auto moved = [&](const float* in, int64_t stride) {
+        return in != nullptr && ((in == R_out && stride != r_out_stride) || (in == Y && stride != y_stride));
+    };
+    if (moved(X, x_stride) || moved(R, r_stride)) return Q8_ERR_INVALID_ARG;
     if (Y != nullptr && Y == R_out) return Q8_ERR_INVALID_ARG;
     q8::NormStep s = {};
     if (acts != nullptr) {

@@ -176,6 +176,17 @@ def test_norm_refuses(q8):
             [(12, 600)])
 
 
+def test_norm_in_place_refuses_another_stride_where_both_inputs_are_one(q8):
+    """X and R at one address with strides of their own: an output there has the
+    stride of both or is refused, since its rows would overlap the other's."""
+    lib = q8.library()
+    for out, stride in ((8, 9), (11, 12)):
+        for x_stride, r_stride, o_stride in ((512, 600, 512), (512, 600, 600), (600, 512, 512), (600, 512, 600), (512, 512, 600)):
+            a = [P, x_stride, None, None, 0, 1.0, P, r_stride, None, 0, None, None, 0, None, 16, 512, None]
+            a[out], a[stride] = P, o_stride
+            assert lib.q8_norm_step(*a) == INVALID, (out, x_stride, r_stride, o_stride)
+
+
 # --------------------------------------------------------- binding checks
 
 def test_binding_refuses(q8):
