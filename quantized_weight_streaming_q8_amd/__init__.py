@@ -783,7 +783,9 @@ def q8_mx4_unpack_weights(weights: MX4Weights, codes, scales, stream=None) -> No
 
 
 _Tensor, _float32, _int32 = torch.Tensor, torch.float32, torch.int32
-_get_device, _get_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+# None in a torch without a device, where no handle or tensor leads to a call of them.
+_get_device = getattr(torch._C, "_cuda_getDevice", None)
+_get_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _address(x, name: str, dtype, need_bytes: int, dev: int):

@@ -291,3 +291,21 @@ def test_reference_products_and_norms_closed_forms():
     x = np.array([[3.0, 4.0]])
     assert np.allclose(ref.norm(x, "rms", np.array([1.0, 2.0]), None, 0.0, 0.0), [[3 / 12.5 ** .5, 8 / 12.5 ** .5]])
     assert np.allclose(ref.norm(x, "layer", None, np.array([10.0, 20.0]), 0.0, 1.0), [[9, 21]])
+
+
+def test_imports_where_torch_has_no_device():
+    """A torch built without one lacks the names of the current device and stream:
+    sizes and host checks need neither."""
+    import subprocess
+    import sys
+    code = ("import torch\n"
+            "del torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream\n"
+            "import quantized_weight_streaming_q8_amd as q8\n"
+            "assert q8.q8_mx4_weight_bytes(16, 128) == 1280 and q8.q8_act_buffer_bytes(128) > 0\n"
+            "try:\n"
+            "    q8.q8_norm_step(65536, 0, 128, Y=65536, stream=0)\n"
+            "except q8.Q8Error as e:\n"
+            "    assert e.status == q8.Q8_ERR_INVALID_ARG\n"
+            "else:\n"
+            "    raise AssertionError('no rows accepted')\n")
+    subprocess.run([sys.executable, "-c", code], cwd=ROOT, check=True, timeout=300)
