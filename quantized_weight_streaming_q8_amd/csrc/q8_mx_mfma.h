@@ -42,21 +42,39 @@ __device__ inline v4f multiply(v4u w, uint32_t ws, const Tokens& x, const Scales
     return c;
 }
 
-// 1 / (1 + exp(-x)) with the instructions for 2^x and 1/x, each good to a unit in the
-// last place.  A tile of 128 features and 256 tokens has 64 of these a lane: with
-// expf and a division they took 14 us of a tile's 95.  Below 2^-126 it is 0.
-__device__ inline float sigmoid(float x) {
-    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * x));
+constexpr float kLog2E = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
+
+// 1 / (1 + exp(-y)), exp(-y) = 2^t (1 + r): t holds -y log2 e rounded, r what that left off, which alone
+// would be an error of |y| roundings in the result.  2^t and 1/x are the instructions', each good to a unit in
+// the last place: a tile of 128 features and 256 tokens has 64 of these a lane, and with expf and a division they
+// took 14 us of a tile's 95.  Where exp(-y) exceeds 2^126 the result is 0.
+__device__ inline float sigmoid_parts(float t, float r) {
+    return __builtin_amdgcn_rcpf(__builtin_fmaf(__builtin_amdgcn_exp2f(t), 1.0f + r, 1.0f));
+}
+
+// Measured: 3 roundings off to y = -20, 6 at the lower end (log 2 itself is off by its rounding).  y is held
+// to limits beyond which this is 0 and 1, since the remainder of an infinite t is none.
+__device__ inline float sigmoid(float y) {
+    const float t = -kLog2E * y;
+    return sigmoid_parts(t, __builtin_fmaf(-kLn2, t, -y));
+}
+__device__ inline float limit(float x, float most) { return __builtin_amdgcn_fmed3f(x, -most, most); }  // a number for NaN
+
+// The sigmoid of y = 2 sqrt(2 / pi) (x + 0.044715 x^3), formed as x (A + B x^2) with log2 e in A and B.  The
+// polynomial's roundings are some |y| of the result's: measured 29 to x = -6 (y = -25), 107 at the lower end.
+__device__ inline float sigmoid_of_cubic(float x) {
+    constexpr double kA = 1.5957691216057308 * 1.4426950408889634;
+    const float p = __builtin_fmaf((float)(0.044715 * kA), x * x, (float)kA), t = -x * p;
+    return sigmoid_parts(t, kLn2 * __builtin_fmaf(-x, p, -t));
 }
 
 template <int Kind>
 __device__ inline float activate(float x) {
-    if constexpr (Kind == Q8_ACT_SILU) return x * sigmoid(x);
+    if constexpr (Kind == Q8_ACT_SILU) return x * sigmoid(limit(x, 200.0f));
     else if constexpr (Kind == Q8_ACT_GELU) return 0.5f * x * erfcf(-0.70710678118654752440f * x);
-    else if constexpr (Kind == Q8_ACT_GELU_TANH)
-        return x * sigmoid(1.5957691216057307f * (x + 0.044715f * x * x * x));
+    else if constexpr (Kind == Q8_ACT_GELU_TANH) return x * sigmoid_of_cubic(limit(x, 16.0f));
     else if constexpr (Kind == Q8_ACT_RELU) return x > 0.0f ? x : x == x ? 0.0f : x;
-    else if constexpr (Kind == Q8_ACT_SIGMOID) return sigmoid(x);
+    else if constexpr (Kind == Q8_ACT_SIGMOID) return x == x ? sigmoid(limit(x, 200.0f)) : x;
     else return x;
 }
 

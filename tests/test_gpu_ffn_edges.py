@@ -1,0 +1,130 @@
+"""The feed-forward side's operators on the GPU at the values, sizes and forms
+that each choice of a kernel has an end at.  Tolerances as in test_gpu_ffn.py;
+U is half a step of fp32 relative to a value, a rounding."""
+
+import numpy as np
+import pytest
+import torch
+
+import ffn_ref as ref
+from gpu_util import q8 as _q8, to_dev
+
+pytestmark = pytest.mark.gpu
+
+U = ref.U
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _device():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a GPU")
+    assert _q8().q8_device_supported(), "device is not gfx950"
+    yield
+    torch.cuda.synchronize()
+
+
+@pytest.fixture(scope="module")
+def q8():
+    return _q8()
+
+
+# -------------------------------------------------------------- activations
+
+def gate_values(n, seed):
+    """fp32 numbers over the activations' ranges, their ends and borders, with all 24 bits in use."""
+    r = np.random.default_rng(seed)
+    edges = [0.0, 1e-30, 1.0, 9.49, 9.5, 9.51, 12.0, 16.1, 79.9, 80.0, 80.1, 86.6, 87.4, 88.8, 95.0, 103.9, 104.5, 126.0,
+             129.0, 174.0, 259.0, 261.0, 1e4, 1e18, 3e38]
+    x = np.concatenate([edges, -np.array(edges), r.uniform(-4, 4, n // 4), r.uniform(-12, 12, n // 4), r.uniform(-110, 0, n // 4)])
+    x = np.concatenate([x, r.uniform(-110, 110, n)])[:n] if n > len(edges) * 2 else r.permutation(x)[:n]
+    return x.astype(np.float32)
+
+
+def gates(q8, x, shifts):
+    """([weights of the gate, of the up projection], activations, x as they hold it): token t's gate is x[t] / 2^shifts[f]
+    at feature f without an error, its up projection 1.  x[t] comes in four pieces of 7 bits, each in a block of its
+    own, the first of which saturates for x beyond a block's largest value."""
+    acts = np.zeros((len(x), 160), np.float32)
+    rest = x.astype(np.float64)
+    unit = 2.0 ** (np.floor(np.log2(np.where(x == 0, 1, np.abs(rest)))) - 6)
+    for i in range(4):
+        q = np.trunc(rest / unit)
+        acts[:, 32 * i] = q * unit
+        rest, unit = rest - q * unit, unit / 128
+    assert not rest.any()
+    acts[:, 128] = 1.0
+    n = len(shifts)
+    codes, scales = np.zeros((2, n, 80), np.uint8), np.full((2, n, 5), 127, np.uint8)
+    codes[0][:, [0, 16, 32, 48]] = 2  # 1.0 in the even column
+    codes[1][:, 64] = 2
+    scales[0] -= np.asarray(shifts, np.uint8)[:, None]
+    w = [q8.MX4Weights(n, 160) for _ in range(2)]
+    for c, s, to in zip(codes, scales, w):
+        q8.q8_mx4_pack_weights_q(to_dev(c), to_dev(s), to)
+    a = q8.Acts(len(x), 160, "mx8")
+    q8.q8_mx_quantize_acts(to_dev(acts), len(x), a)
+    return w, a, ref.hold(acts, "mx8")[:, :128].sum(-1)
+
+
+def activation_and_bound(g, kind):
+    """The activation of 64-bit numbers and the error of its fp32 form, in roundings.  exp(-y) is 2^t (1 + r): 2^t is
+    good to a unit in the last place, 2; 1 + r is 1; log 2 in r's computation is off by 1.905e-9, which times y log2 e
+    is 0.0462 |y|.  The sum with 1 is 1, its inverse 2, the product with x 1.  The tanh form's argument has errors of 3
+    (x^2, the polynomial, its constants), each of which is |y| of exp(-y).  GELU's argument has 2, of which erfc makes
+    2 v^2 + 1 each, and erfc itself 16 units.  A sigmoid below 2^-126 may be 0."""
+    if kind in ("silu", "sigmoid", "gelu_tanh"):
+        y = 2 * (2 / np.pi) ** 0.5 * (g + 0.044715 * g ** 3) if kind == "gelu_tanh" else g
+        sig = torch.sigmoid(y)
+        v = sig if kind == "sigmoid" else g * sig
+        bound = 7 + (3 * y.abs() * torch.sigmoid(-y) if kind == "gelu_tanh" else 0.0462 * y.abs())
+        bound = torch.where(sig <= 2.0 ** -126 * 1.001, 2.0 ** 25, bound.clamp(max=2.0 ** 23))
+    elif kind == "gelu":
+        v, bound = 0.5 * g * torch.special.erfc(-g * 0.5 ** 0.5), 36 + 2 * (g.clamp(max=0) ** 2 + 1)
+    elif kind == "relu":
+        v, bound = g.clamp(min=0), 0
+    else:
+        v, bound = g, 0
+    v = torch.where(v.isnan(), torch.zeros_like(v), v)
+    return v, bound * U * v.abs() + 2.0 ** -149 * (g.abs() if kind == "gelu" else 1)
+
+
+# One tile, blocks of 64 and large tiles.
+@pytest.mark.parametrize("kind", ["identity", "silu", "sigmoid", "gelu_tanh", "gelu", "relu"])
+@pytest.mark.parametrize("live,n", [(1, 16), (16, 160), (48, 160), (320, 160), (1900, 4096)])
+def test_activations_to_a_few_roundings(q8, kind, live, n):
+    for seed in range(4 if live < 64 else 1):
+        x = gate_values(live, seed)
+        shifts = np.arange(n) % 8
+        w, a, held = gates(q8, x, shifts)
+        h = torch.full((live, n), 7.0, device="cuda")
+        q8.q8_mx4_gated(*w, a, None, live, H=h, activation=kind)
+        g = to_dev(held)[:, None] / to_dev(2.0 ** shifts[:8])
+        want, tol = activation_and_bound(g, kind)
+        err = (h[:, :n // 8 * 8].unflatten(1, (-1, 8)).double() - want[:, None]).abs()
+        part = (err / tol.clamp(min=1e-60)[:, None]).amax(1).flatten()
+        worst = torch.argmax(part).item()
+        print(f"{kind}: {part[worst].item():.3f} of the bound at {g.flatten()[worst].item():.6g}")
+        assert bool((err <= tol[:, None]).all()), (g.flatten()[worst].item(), want.flatten()[worst].item())
+
+
+@pytest.mark.parametrize("live", [3, 40, 300])
+def test_activations_of_numbers_that_are_not_finite(q8, live):
+    """Infinities as sums that leave fp32's range: formulas as they stand, so x sigmoid(y) of -infinity is NaN."""
+    n, inf = 48, np.inf
+    codes, scales = np.zeros((2, n, 80), np.uint8), np.full((2, n, 5), 127, np.uint8)
+    codes[0][:, 0], codes[1][:, 64] = 7, 2  # 6 and 1
+    scales[0] = 140
+    w = [q8.MX4Weights(n, 160) for _ in range(2)]
+    for c, s, to in zip(codes, scales, w):
+        q8.q8_mx4_pack_weights_q(to_dev(c), to_dev(s), to)
+    x = np.zeros((live, 160), np.float32)
+    x[:, 0], x[:, 128] = np.resize([3e37, -3e37, 0.0], live), 1.0
+    a = q8.Acts(live, 160, "mx8")
+    q8.q8_mx_quantize_acts(to_dev(x), live, a)
+    want = {"silu": (inf, np.nan, 0), "sigmoid": (1, 0, 0.5), "gelu_tanh": (inf, np.nan, 0), "gelu": (inf, np.nan, 0),
+            "relu": (inf, 0, 0), "identity": (inf, -inf, 0)}
+    for kind, values in want.items():
+        h = torch.full((live, n), 7.0, device="cuda")
+        q8.q8_mx4_gated(*w, a, None, live, H=h, activation=kind)
+        expect = np.resize(values, live)[:, None].repeat(n, 1)
+        assert np.array_equal(h.cpu().numpy(), expect, equal_nan=True), kind
