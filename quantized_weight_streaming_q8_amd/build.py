@@ -28,7 +28,7 @@ SOURCES = ["q8_mx_columns.hip", "q8_matmul.hip", "q8_kv4_attend.hip", "q8_mx_mat
            "q8_norm.hip", "q8_pack.hip", "q8_rope.hip", "q8_measure.hip", "q8_abi.hip", "q8_noalloc.hip",
            "q8_kv4_rows.hip", "q8_kv4_abi.hip", "q8_mx_rows.hip", "q8_ffn_abi.hip"]
 HEADERS = ["q8_internal.h", "q8_measure.h", "q8_kv4_internal.h", "q8_kv4_shares.h",
-           "q8_ffn_internal.h", "q8_mx_mfma.h", "q8_lds.h"]
+           "q8_ffn_internal.h", "q8_mx_mfma.h", "q8_mx_plan.h", "q8_lds.h"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -226,11 +226,9 @@ struct MxProduct {
     int activation;
 };
 hipError_t launch_mx_product(const MxProduct& p, hipStream_t st);
-hipError_t launch_mx_columns(const MxProduct& p, hipStream_t st);  // q8_mx_columns.hip
-// Estimates of the time of the two for more than 64 tokens, on one scale.
-float mx_columns_cost(const MxProduct& p);
-float mx_wide_cost(const MxProduct& p);
-hipError_t launch_mx_wide(const MxProduct& p, hipStream_t st);     // q8_mx_prompt.hip
+// The tile as in q8_mx_plan.h.
+hipError_t launch_mx_columns(const MxProduct& p, int r, hipStream_t st);  // q8_mx_columns.hip
+hipError_t launch_mx_wide(const MxProduct& p, int rt, hipStream_t st);    // q8_mx_prompt.hip
 
 struct NormView {
     const float* weight;

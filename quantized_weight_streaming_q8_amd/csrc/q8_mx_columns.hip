@@ -321,30 +321,8 @@ hipError_t launch_columns(const MxProduct& p, hipStream_t st) {
     return hipGetLastError();
 }
 
-// Time of a tile's super-chunk of 512 columns in us, 2 r row groups x 64 tokens: the
-// tokens' way to LDS and the row groups'.
-constexpr float column_time(int form, int r) {
-    return form == kMx4 ? 0.50f + 0.17f * r : form == kMx6 ? 0.67f + 0.15f * r : 0.86f + 0.16f * r;
-}
-
-// Row groups of the tiles that need the least time: whole rounds of the 256 CUs.
-float columns_best(const MxProduct& p, int* best) {
-    const int64_t groups = (row_groups(p.w.rows) * (p.wu.codes != nullptr ? 2 : 1) + 1) / 2;
-    const int64_t blocks = (p.n_live + 63) / 64;
-    const auto cost = [&](int r) {
-        return (float)(((groups + r - 1) / r * blocks + 255) / 256) * column_time(p.form, r);
-    };
-    const bool pairs = p.out.codes != nullptr;  // blocks of 32 features
-    *best = pairs ? 2 : 1;
-    for (int r : {2, 4, 5})
-        if ((!pairs || r % 2 == 0) && cost(r) < cost(*best)) *best = r;
-    return cost(*best);
-}
-
 template <int F, int T>
-hipError_t columns_rows(const MxProduct& p, hipStream_t st) {
-    int r;
-    columns_best(p, &r);
+hipError_t columns_rows(const MxProduct& p, int r, hipStream_t st) {
     if (r == 5) return launch_columns<F, T, 5>(p, st);
     if (r == 4) return launch_columns<F, T, 4>(p, st);
     if (r == 2) return launch_columns<F, T, 2>(p, st);
@@ -352,25 +330,20 @@ hipError_t columns_rows(const MxProduct& p, hipStream_t st) {
 }
 
 template <int F>
-hipError_t columns_tokens(const MxProduct& p, hipStream_t st) {
+hipError_t columns_tokens(const MxProduct& p, int r, hipStream_t st) {
     switch (std::min(4, (p.n_live + 15) / 16)) {
-        case 2: return columns_rows<F, 2>(p, st);
-        case 3: return columns_rows<F, 3>(p, st);
-        default: return columns_rows<F, 4>(p, st);
+        case 2: return columns_rows<F, 2>(p, r, st);
+        case 3: return columns_rows<F, 3>(p, r, st);
+        default: return columns_rows<F, 4>(p, r, st);
     }
 }
 
 }  // namespace
 
-float mx_columns_cost(const MxProduct& p) {
-    int r;
-    return columns_best(p, &r);
-}
-
-hipError_t launch_mx_columns(const MxProduct& p, hipStream_t st) {
-    if (p.form == kMx4) return columns_tokens<kMx4>(p, st);
-    if (p.form == kMx6) return columns_tokens<kMx6>(p, st);
-    return columns_tokens<kMx8>(p, st);
+hipError_t launch_mx_columns(const MxProduct& p, int r, hipStream_t st) {
+    if (p.form == kMx4) return columns_tokens<kMx4>(p, r, st);
+    if (p.form == kMx6) return columns_tokens<kMx6>(p, r, st);
+    return columns_tokens<kMx8>(p, r, st);
 }
 
 }  // namespace q8

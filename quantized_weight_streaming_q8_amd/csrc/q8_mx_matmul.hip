@@ -23,6 +23,7 @@
 
 #include "q8_lds.h"
 #include "q8_mx_mfma.h"
+#include "q8_mx_plan.h"
 
 namespace q8 {
 namespace {
@@ -303,11 +304,9 @@ hipError_t narrow_form(const NarrowArgs& n, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_mx_product(const MxProduct& p, hipStream_t st) {
-    // Up to 64 tokens the way of the weights bounds the time.  Above, blocks of 64
-    // fill the chip where few large tiles would not (7168 x 5120, MX8: 128 tokens 20.2 us
-    // against 37.5, 512 44 against 40), and cost more once both fill it.
-    if (p.n_live > 64 && mx_wide_cost(p) < mx_columns_cost(p)) return launch_mx_wide(p, st);
-    if (p.n_live > 16) return launch_mx_columns(p, st);
+    const MxPlan plan = mx_plan(p.form, p.w.rows, p.wu.codes != nullptr, p.out.codes != nullptr, p.n_live);
+    if (plan.way == MxPlan::kWide) return launch_mx_wide(p, plan.tile, st);
+    if (plan.way == MxPlan::kColumns) return launch_mx_columns(p, plan.tile, st);
     NarrowArgs n;
     n.p = p;
     // one super-chunk a wave; from 13 to 16 two, whose tokens still fit the registers of

@@ -363,35 +363,9 @@ hipError_t launch_wide(const MxProduct& p, hipStream_t st) {
     return hipGetLastError();
 }
 
-// Time of a tile's super-chunk of 512 columns in us, 256 rows x 64 RT tokens.
-constexpr float wide_time(int form, int rt) {
-    if (rt == 4) return form == kMx4 ? 2.7f : form == kMx6 ? 3.0f : 5.3f;
-    return form == kMx4 ? 1.8f : form == kMx6 ? 2.0f : 2.8f;
-}
-
-// Tokens of the tiles that need the least time: whole rounds of the 256 CUs (7168 x 5120,
-// MX4: 1024 tokens in 224 small tiles 30 us, in 112 large ones 39; 4099 tokens in 924 and 476
-// tiles 120 and 98 us).
-float wide_best(const MxProduct& p, int* best) {
-    const int64_t rows = (p.w.rows * (p.wu.codes != nullptr ? 2 : 1) + 255) / 256;
-    const auto cost = [&](int rt) {
-        const int64_t tiles = rows * ((p.n_live + 64 * rt - 1) / (64 * rt));
-        return (float)((tiles + 255) / 256) * wide_time(p.form, rt);
-    };
-    *best = cost(4) <= cost(2) ? 4 : 2;
-    return cost(*best);
-}
-
 }  // namespace
 
-float mx_wide_cost(const MxProduct& p) {
-    int rt;
-    return wide_best(p, &rt);
-}
-
-hipError_t launch_mx_wide(const MxProduct& p, hipStream_t st) {
-    int rt;
-    wide_best(p, &rt);
+hipError_t launch_mx_wide(const MxProduct& p, int rt, hipStream_t st) {
     if (p.form == kMx4) return rt == 4 ? launch_wide<kMx4, 4>(p, st) : launch_wide<kMx4, 2>(p, st);
     if (p.form == kMx6) return rt == 4 ? launch_wide<kMx6, 4>(p, st) : launch_wide<kMx6, 2>(p, st);
     return rt == 4 ? launch_wide<kMx8, 4>(p, st) : launch_wide<kMx8, 2>(p, st);

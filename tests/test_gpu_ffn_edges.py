@@ -7,6 +7,8 @@ import pytest
 import torch
 
 import ffn_ref as ref
+import ffn_shapes as shapes
+import test_gpu_ffn as base
 from gpu_util import q8 as _q8, to_dev
 
 pytestmark = pytest.mark.gpu
@@ -128,3 +130,82 @@ def test_activations_of_numbers_that_are_not_finite(q8, live):
         q8.q8_mx4_gated(*w, a, None, live, H=h, activation=kind)
         expect = np.resize(values, live)[:, None].repeat(n, 1)
         assert np.array_equal(h.cpu().numpy(), expect, equal_nan=True), kind
+
+
+# ---------------------------------------------------------- every tile of a product
+
+def whole_case(seed, form, n, k, slots):
+    """Weights and activations whose products are whole multiples of one unit and whose sums stay below 2^24 of them
+    (a product has at most 12 x 127 units): (weights, their values, activations, theirs), values in 64 bits."""
+    assert k * 12 * 127 < 2 ** 24
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    q8 = _q8()
+    codes = torch.randint(0, 256, (n, k // 2), generator=g, device="cuda", dtype=torch.uint8)
+    w = q8.MX4Weights(n, k)
+    w.data.fill_(0xEE)
+    q8.q8_mx4_pack_weights_q(codes, torch.full((n, k // 32), 127, dtype=torch.uint8, device="cuda"), w)
+    one = to_dev(ref.GRIDS["mx4"])
+    one = torch.cat((one, -one))
+    values = torch.stack((one[(codes & 15).int()], one[(codes >> 4).int()]), -1).flatten(-2)
+    grid = to_dev(ref.GRIDS[form])
+    x = grid[torch.randint(0, len(grid), (slots, k), generator=g, device="cuda")]
+    x *= 1.0 - 2.0 * torch.randint(0, 2, (slots, k), generator=g, device="cuda")
+    x[:, ::32] = grid[-1]  # the scale of every block is 1
+    a = q8.Acts(slots, k, form)
+    q8.q8_mx_quantize_acts(x.float(), slots, a)
+    return w, values, a, x
+
+
+def index_of(live, slots, seed):
+    """Slots in any order, two of them outside the buffer: (on the GPU, which are inside, those)."""
+    index = np.random.default_rng(seed).integers(0, slots, live)
+    index[[1, live - 1]] = [-1, slots]
+    good = torch.from_numpy((index >= 0) & (index < slots)).cuda()
+    index = to_dev(index.astype(np.int32))
+    return index, good, index[good].long()
+
+
+@pytest.mark.parametrize("form", ["mx4", "mx6", "mx8"])
+@pytest.mark.parametrize("shape,tile,several", shapes.PRODUCTS)
+def test_products_in_every_tile(q8, form, shape, tile, several):
+    n, k, live = shape
+    slots = min(live, 700)
+    w, values, a, x = whole_case(n + live, form, n, k, slots)
+    index, good, inside = index_of(live, slots, n)
+    y = torch.full((live + 1, n), 7.0, device="cuda")
+    q8.q8_mx4_matmul(w, a, index, live, y)
+    assert bool((y[live] == 7).all()) and bool(y[:live][~good].isnan().all())
+    assert torch.equal(y[:live][good], (x @ values.T).float()[inside]), tile
+
+
+@pytest.mark.parametrize("form", ["mx4", "mx6", "mx8"])
+@pytest.mark.parametrize("shape,tile,several", shapes.GATED)
+def test_gated_blocks_in_every_tile(q8, form, shape, tile, several):
+    n, k, live = shape
+    slots = min(live, 700)
+    wg, vg, a, x = whole_case(n + live, form, n, k, slots)
+    wu, vu, _, _ = whole_case(n + live + 1, form, n, k, 1)
+    index, good, inside = index_of(live, slots, n)
+    h = torch.full((live + 1, n), 7.0, device="cuda")
+    q8.q8_mx4_gated(wg, wu, a, index, live, H=h, activation="identity")
+    assert bool((h[live] == 7).all()) and bool(h[:live][~good].isnan().all())
+    assert torch.equal(h[:live][good], ((x @ vg.T).float() * (x @ vu.T).float())[inside]), tile
+
+
+@pytest.mark.parametrize("form,out", [("mx4", "mx8"), ("mx6", "mx4"), ("mx8", "mx8"), ("mx8", "mx6")])
+@pytest.mark.parametrize("shape,tile,several", shapes.QUANTISED)
+def test_quantised_rows_in_every_tile(q8, form, out, shape, tile, several):
+    n, k, live = shape
+    slots = min(live, 700)
+    wg, vg, a, x = whole_case(n + live, form, n, k, slots)
+    wu, vu, _, _ = whole_case(n + live + 1, form, n, k, 1)
+    index, good, inside = index_of(live, slots, n)
+    h, alone, both, want = torch.empty(live, n, device="cuda"), *(q8.Acts(live + 3, n, out) for _ in range(3))
+    for b in (alone, both, want):
+        b.data.fill_(0x41)
+    q8.q8_mx4_gated(wg, wu, a, index, live, H=h, h_acts=both, activation="identity")
+    q8.q8_mx4_gated(wg, wu, a, index, live, h_acts=alone, activation="identity")
+    q8.q8_mx_quantize_acts(h, live, want)
+    assert torch.equal(both.data, want.data) and torch.equal(alone.data, want.data), tile
+    assert torch.equal(h[good], ((x @ vg.T).float() * (x @ vu.T).float())[inside]), tile
