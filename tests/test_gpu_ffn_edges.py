@@ -209,3 +209,93 @@ def test_quantised_rows_in_every_tile(q8, form, out, shape, tile, several):
     q8.q8_mx_quantize_acts(h, live, want)
     assert torch.equal(both.data, want.data) and torch.equal(alone.data, want.data), tile
     assert torch.equal(h[good], ((x @ vg.T).float() * (x @ vu.T).float())[inside]), tile
+
+
+@pytest.mark.parametrize("n,k,live", [(45, 160, 5), (45, 160, 40), (4093, 96, 1900)])
+def test_gated_rows_at_a_stride(q8, n, k, live):
+    """h_stride beyond the row, at every alignment: the rows and nothing between them."""
+    wg, vg, a, x = whole_case(n, "mx8", n, k, live)
+    wu, vu, _, _ = whole_case(n + 1, "mx8", n, k, 1)
+    want = (x @ vg.T).float() * (x @ vu.T).float()
+    for stride, off in ((n, 0), (n + 16, 1), (n + 19, 0), (n + 3, 2)):
+        h = torch.full((live * stride + 8,), 7.0, device="cuda")
+        q8.q8_mx4_gated(wg, wu, a, None, live, H=h[off:], h_stride=stride, activation="identity")
+        rows = h[off:off + live * stride].view(live, stride)
+        assert torch.equal(rows[:, :n], want), (stride, off)
+        assert bool((rows[:, n:] == 7).all()) and bool((h[:off] == 7).all()) and bool((h[off + live * stride:] == 7).all())
+
+
+# ------------------------------------------------------ rows past the caches, wide rows
+
+@pytest.mark.parametrize("form", ["mx4", "mx6", "mx8"])
+def test_large_quantisation_is_that_of_its_parts(q8, form):
+    """From 32 MB on fp32 rows go past the caches, read and written; aligned or not."""
+    n, k = 1640, 5152
+    big = torch.randn(n * (k + 3) + 4, device="cuda")
+    big *= torch.exp(torch.randn(big.numel(), device="cuda"))
+    for stride, off in ((k, 0), (k + 3, 1)):
+        x = torch.as_strided(big, (n, k), (stride, 1), off).contiguous()
+        a, out = q8.Acts(n, k, form), torch.empty(n * k + 1, device="cuda")
+        q8.q8_mx_quantize_acts(big[off:], n, a, x_stride=stride)
+        for at in (0, 1):  # 16-byte stores or single ones
+            q8.q8_mx_read_acts(a, None, n, out[at:])
+            got = out[at:at + n * k].view(n, k)
+            for first in range(0, n, 410):
+                part, small = q8.Acts(410, k, form), torch.empty(410, k, device="cuda")
+                q8.q8_mx_quantize_acts(x[first:first + 410], 410, part)
+                q8.q8_mx_read_acts(part, None, 410, small)
+                assert torch.equal(got[first:first + 410], small)
+        some = np.array([0, 1, 819, n - 1])
+        assert np.array_equal(got[to_dev(some)].cpu().numpy().astype(np.float64), ref.hold(x[to_dev(some)].cpu().numpy(), form))
+
+
+def test_large_weights_are_packed_as_their_parts(q8):
+    n, k = 2064, 5120
+    x = torch.randn(n, k, device="cuda") * 0.02
+    w = q8.MX4Weights(n, k)
+    q8.q8_mx4_pack_weights(x, w)
+    codes, scales = (torch.empty(n, k // d, dtype=torch.uint8, device="cuda") for d in (2, 32))
+    q8.q8_mx4_unpack_weights(w, codes, scales)
+    for first in range(0, n, 688):
+        part = q8.MX4Weights(688, k)
+        q8.q8_mx4_pack_weights(x[first:first + 688], part)
+        c, s = (torch.empty(688, k // d, dtype=torch.uint8, device="cuda") for d in (2, 32))
+        q8.q8_mx4_unpack_weights(part, c, s)
+        assert torch.equal(c, codes[first:first + 688]) and torch.equal(s, scales[first:first + 688])
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("stride", [5120, 5123])
+def test_large_norm_is_that_of_its_parts(q8, in_place, stride):
+    """From 32 MB on stores go past the caches."""
+    n, k = 1640, 5120
+    x, r = (torch.randn(n, stride, device="cuda") for _ in range(2))
+    g = torch.randn(n, k, device="cuda")
+    post, pre = (q8.Norm(k, kind, torch.randn(k, device="cuda"), torch.randn(k, device="cuda")) for kind in ("rms", "layer"))
+    args = dict(post=post, gate=g, scale=0.5, residual=r.clone(), pre=pre, x_stride=stride, residual_stride=stride,
+                residual_out_stride=stride, y_stride=stride)
+    out, y = (args["residual"], x.clone()) if in_place else (torch.full_like(r, 7.0) for _ in range(2))
+    acts = q8.Acts(n, k, "mx8")
+    q8.q8_norm_step(y if in_place else x, n, k, residual_out=out, Y=y, acts=acts, **args)
+    held = torch.empty(n, k, device="cuda")
+    q8.q8_mx_read_acts(acts, None, n, held)
+    for first in range(0, n, 205):
+        s = slice(first, first + 205)
+        o, t = (torch.full((205, stride), 7.0, device="cuda") for _ in range(2))
+        a, b = q8.Acts(205, k, "mx8"), torch.empty(205, k, device="cuda")
+        q8.q8_norm_step(x[s], 205, k, residual_out=o, Y=t, acts=a, **dict(args, gate=g[s], residual=r[s]))
+        q8.q8_mx_read_acts(a, None, 205, b)
+        assert torch.equal(out[s, :k], o[:, :k]) and torch.equal(y[s, :k], t[:, :k]) and torch.equal(held[s], b)
+    if not in_place:
+        assert bool((out[:, k:] == 7).all()) and bool((y[:, k:] == 7).all())
+
+
+@pytest.mark.parametrize("k", [8196, 8224, 12288, 12290, 16416, 20480, 20483, 24576, 24581, 28672, 28676, 32737])
+def test_norms_of_wide_rows(q8, k):
+    """Every number of units that a thread of 16 waves holds, at its ends; aligned or not."""
+    base.check_norm(q8, 3, k, None, "rms", None, True)
+    base.check_norm(q8, 2, k, "layer", "layer", "rows", True, per_row=True, offset=0.0)
+    base.check_norm(q8, 2, k, "rms", "rms", "shared", True, in_place=True)
+    if k % 32 == 0:
+        base.test_norm_quantises_as_the_quantiser_does(q8, "mx8", 3, k, 5)
+        base.test_norm_fills_q8_0_slots_as_their_quantiser_does(q8, 3, k, 16)
