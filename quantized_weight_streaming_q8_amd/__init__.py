@@ -669,7 +669,8 @@ _U8 = (torch.uint8,)
 
 
 def q8_acts_bytes(n_slots: int, K: int, format: str) -> int:
-    return int(_lib.q8_acts_bytes(n_slots, K, Q8_ACTS_FORMATS[format]))
+    kind = Q8_ACTS_FORMATS[format]
+    return int(_lib.q8_acts_bytes(n_slots, K, kind)) if 0 < n_slots <= Q8_FFN_MAX_ROWS else 0
 
 
 def q8_mx4_weight_bytes(N: int, K: int) -> int:
@@ -782,6 +783,7 @@ def q8_mx4_unpack_weights(weights: MX4Weights, codes, scales, stream=None) -> No
            "q8_mx4_unpack_weights")
 
 
+# A call's count of rows is checked here too: ctypes keeps the low 32 bits of a larger number.
 _Tensor, _float32, _int32 = torch.Tensor, torch.float32, torch.int32
 # None in a torch without a device, where no handle or tensor leads to a call of them.
 _get_device = getattr(torch._C, "_cuda_getDevice", None)
@@ -803,6 +805,8 @@ def _short(h, kind, name: str, dev: int):
 
 def q8_mx_quantize_acts(X, n_rows: int, acts: Acts, x_stride: int | None = None, stream=None) -> None:
     """Rows of X (x_stride apart, default K) into slots 0 .. n_rows - 1."""
+    if not 0 < n_rows <= Q8_FFN_MAX_ROWS:
+        _check(Q8_ERR_INVALID_ARG, "q8_mx_quantize_acts")
     K = acts.K
     if x_stride is None:
         x_stride = K
@@ -817,6 +821,8 @@ def q8_mx_quantize_acts(X, n_rows: int, acts: Acts, x_stride: int | None = None,
 
 def q8_mx_read_acts(acts: Acts, batch_index, n_rows: int, X, stream=None) -> None:
     """The values of slots batch_index[0 .. n_rows - 1] (None: slots 0 ..)."""
+    if not 0 < n_rows <= Q8_FFN_MAX_ROWS:
+        _check(Q8_ERR_INVALID_ARG, "q8_mx_read_acts")
     dev = _get_device() if type(acts) is Acts else _current_device()
     bi = None if batch_index is None else _address(batch_index, "batch_index", _int32, 4 * n_rows, dev)
     x = _address(X, "X", _float32, 4 * n_rows * acts.K, dev)
@@ -831,6 +837,8 @@ def q8_mx4_matmul(weights: MX4Weights, acts: Acts, batch_index, n_live: int, Y, 
                   stream=None) -> None:
     """Y [n_live][N] (rows y_stride apart, default N); token t takes slot
     batch_index[t] (None: slot t)."""
+    if not 0 < n_live <= Q8_FFN_MAX_ROWS:
+        _check(Q8_ERR_INVALID_ARG, "q8_mx4_matmul")
     N = weights.N
     if y_stride is None:
         y_stride = N
@@ -853,6 +861,8 @@ def q8_mx4_gated(gate: MX4Weights, up: MX4Weights, acts: Acts, batch_index, n_li
     kind = Q8_ACTIVATIONS.get(activation)
     if kind is None:
         raise ValueError(f"activation: expected one of {sorted(Q8_ACTIVATIONS)}, got {activation!r}")
+    if not 0 < n_live <= Q8_FFN_MAX_ROWS:
+        _check(Q8_ERR_INVALID_ARG, "q8_mx4_gated")
     N = gate.N
     if h_stride is None:
         h_stride = N
@@ -875,6 +885,8 @@ def q8_norm_step(X, n_rows: int, K: int, post: Norm | None = None, gate=None, sc
     """residual_out = residual + scale * gate * post(X); y = pre(residual_out)
     goes to Y, to acts, or both.  Strides default to K, gate_stride to 0 (one
     gate for all rows) unless the gate is a tensor of two dimensions."""
+    if not 0 < n_rows <= Q8_FFN_MAX_ROWS:
+        _check(Q8_ERR_INVALID_ARG, "q8_norm_step")
     xs = K if x_stride is None else x_stride
     rs = K if residual_stride is None else residual_stride
     os = K if residual_out_stride is None else residual_out_stride

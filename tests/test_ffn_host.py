@@ -309,3 +309,26 @@ def test_imports_where_torch_has_no_device():
             "else:\n"
             "    raise AssertionError('no rows accepted')\n")
     subprocess.run([sys.executable, "-c", code], cwd=ROOT, check=True, timeout=300)
+
+
+def test_counts_beyond_32_bits_are_refused(q8):
+    """ctypes keeps the low 32 bits of a larger number, which would be a count of rows again."""
+    for n in ((1 << 32) + 4, -(1 << 32) + 4, 1 << 31, (1 << 20) + 1, 0):
+        for form in ("mx4", "mx6", "mx8", "q8_0"):
+            assert q8.q8_acts_bytes(n * 4, 128, form) == 0
+        with pytest.raises(ValueError, match="invalid buffer shape"):
+            q8.Acts(n * 4, 128, "mx8")
+        for call in (lambda: q8.q8_norm_step(P, n, 128, Y=P, stream=0), lambda: q8.q8_mx_quantize_acts(P, n, X, stream=0),
+                     lambda: q8.q8_mx_read_acts(X, None, n, P, stream=0), lambda: q8.q8_mx4_matmul(W, X, P, n, P, stream=0),
+                     lambda: q8.q8_mx4_gated(W, W, X, P, n, H=P, stream=0)):
+            with pytest.raises(q8.Q8Error) as e:
+                call()
+            assert e.value.status == INVALID
+
+
+class W:  # the fields a call's size checks read
+    N, K = 64, 128
+
+
+class X:
+    K, n_slots = 128, 16
