@@ -299,3 +299,25 @@ def test_norms_of_wide_rows(q8, k):
     if k % 32 == 0:
         base.test_norm_quantises_as_the_quantiser_does(q8, "mx8", 3, k, 5)
         base.test_norm_fills_q8_0_slots_as_their_quantiser_does(q8, 3, k, 16)
+
+
+# ---------------------------------------------------------------- ends of the scales
+
+@pytest.mark.parametrize("form", ["mx4", "mx6", "mx8"])
+@pytest.mark.parametrize("live", [8, 40, 400])
+def test_products_at_the_ends_of_the_scales(q8, form, live):
+    """Single products of every code at the smallest and largest scale bytes: exact down to fp32's denormals, infinite
+    beyond its largest number."""
+    held = [(c, s) for s in (0, 1, 2, 3, 10, 60, 120, 200, 250, 252, 253, 254) for c in range(16)]
+    codes, scales = np.zeros((len(held), 16), np.uint8), np.zeros((len(held), 1), np.uint8)
+    codes[:, 0], scales[:, 0] = [c for c, _ in held], [s for _, s in held]
+    w = q8.MX4Weights(len(held), 32)
+    q8.q8_mx4_pack_weights_q(to_dev(codes), to_dev(scales), w)
+    x = np.zeros((live, 32), np.float32)
+    x[:, 0] = np.resize([1.5 * 2.0 ** e for e in (-120, -100, -22, -1, 0, 3, 60, 118)], live)
+    a, y = q8.Acts(live, 32, form), torch.empty(live, len(held), device="cuda")
+    q8.q8_mx_quantize_acts(to_dev(x), live, a)
+    q8.q8_mx4_matmul(w, a, None, live, y)
+    with np.errstate(over="ignore"):
+        want = (ref.hold(x, form) @ ref.mx4_values(codes, scales).T).astype(np.float32)
+    assert np.array_equal(y.cpu().numpy(), want) and np.isinf(want).any() and (np.abs(want[want != 0]) < 2.0 ** -126).any()
