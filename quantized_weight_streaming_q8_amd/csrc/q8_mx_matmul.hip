@@ -28,7 +28,6 @@
 namespace q8 {
 namespace {
 
-
 // A super-chunk of one row group: 4 chunks of codes and their scales.
 struct Weights {
     v4u c0, c1, c2, c3;
@@ -72,7 +71,6 @@ template <int F, int P, int Kept>
 __global__ void __launch_bounds__(Kept == 2 ? 512 : kMaxWaves * 64)
 mx_narrow_kernel(NarrowArgs n) {
     extern __shared__ v4f lds[];  // [2][waves][2][64 lanes], [64]
-    constexpr int PI = form_pieces(F);
     const MxProduct& p = n.p;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int groups = (int)((p.w.rows + 15) / 16);

@@ -176,7 +176,6 @@ mx_wide_kernel(WideArgs n) {
     // Chunk c into stage c % kStages, and with it quarter Q = c % 4 of the next
     // super-chunk's scales.  Past the end the last chunk again: the counts stay.
     const auto load_item = [&](auto Q, int m, int c, int stage) {
-        constexpr int q = decltype(Q)::value;
         const uint32_t to = lds0 + stage * S::kBytes;
         const int from = min(c, kc - 1);
         if (m < S::kLoadN) {

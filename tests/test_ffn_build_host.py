@@ -24,3 +24,8 @@ def test_products_of_up_to_16_tokens_keep_their_registers(tmp_path):
     text = open(asm).read()
     scratch = dict(re.findall(r"\.name:\s+(\S*mx_narrow_kernel\S*)\s+\.private_segment_fixed_size: (\d+)", text))
     assert len(scratch) == 18 and set(scratch.values()) == {"0"}, scratch
+
+
+@pytest.mark.parametrize("name", [s for s in build.SOURCES if s.startswith(("q8_mx_", "q8_norm", "q8_ffn_"))])
+def test_sources_have_no_unused_names(name):
+    assert not re.findall(r"warning: unused .*", compile_source(name, "-fsyntax-only", "-Wall", "-Wno-unused-function").stderr)
