@@ -10,9 +10,9 @@
 // for memory half of the time).  The 4 chunks' sums meet in LDS and are added in order.
 //
 // Measured (MX8): 7168 x 5120, 32 tokens 13.5 us, 64 17.4; 151936 x 5120, 61 tokens 112 us
-// (4.0 TB/s; 16 tokens, kept in registers, 68.6 us, 6.2 TB/s): the tokens' way through each
-// workgroup's LDS, 50 KB a super-chunk, takes about 1 us of each step, which larger tiles
-// share but fewer workgroups pay for.
+// (4.0 TB/s; 16 tokens, kept in registers, 68.7 us, 6.2 TB/s).  A super-chunk of 64 tokens, 50 KB through LDS,
+// takes a workgroup 1.0 us with 32 rows, 1.3 with 64, 1.8 with 128, 2.3 with 160 (q8_mx_plan.h): 0.7 whatever the
+// rows are, which larger tiles share but fewer workgroups pay for.
 
 #include <algorithm>
 

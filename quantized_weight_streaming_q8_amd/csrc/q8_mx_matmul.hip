@@ -12,11 +12,13 @@
 // their way while one is multiplied.  The waves' sums meet in LDS, where they are added
 // in order: the tree depends on K alone.
 //
-// Measured with 16 tokens, MX8: 7168 x 5120 6.9 us, the gated block of 17408 x 5120 20.9 to
-// 22.0 (4.4 to 4.6 TB/s), 151936 x 5120 68.6 (6.2): 7.0 TB/s, a large read's rate, and 5 to 6
-// us that are the launch, the first loads' latency and the sums' way.  Weights are read
-// past the caches: of a model's layers none is there when its turn comes (eight gated blocks in
-// turn 22.3 us, through the caches 23.7; the 151936 rows 71.0 and 77.6).
+// Measured with 16 tokens, MX8: 7168 x 5120 6.9 us (25 matrices in turn 7.3), the gated block of 17408 x 5120 20.7 (eight in
+// turn 19.8; 4.7 and 4.9 TB/s), into quantised rows 23.0, since a workgroup then takes pairs two at a time and
+// the longest has 6 of the 4.25 that are its share; 151936 x 5120 68.7 (6.2): 7.0 TB/s, a large read's rate, and
+// 5 to 6 us that are the launch, the first loads' latency and the sums' way.  Weights are read
+// past the caches: of a model's layers none is there when its turn comes (before the last steps eight gated blocks
+// in turn 22.3 us, through the caches 23.7; the 151936 rows 71.0 and 77.6).  A workgroup has a wave for 512 columns
+// and there are 256 of them: rows of 768 leave two waves to a CU, 151936 x 768 takes 21 us (3.4 TB/s).
 
 #include <algorithm>
 #include <utility>

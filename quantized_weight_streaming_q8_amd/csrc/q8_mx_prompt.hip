@@ -4,7 +4,8 @@
 // A workgroup of 8 waves, 2 x 4, makes a tile of 256 rows x 64 RT tokens, each wave
 // 8 x RT of the instruction's 16 x 16 tiles in registers.  Operands go from memory to
 // LDS past the registers, a chunk of 128 columns a stage, in the order in which the
-// instruction takes them (no bank conflicts, no address arithmetic); a stage is
+// instruction takes them (no address arithmetic; bank conflicts are 22% of LDS's cycles with MX4, 28% with
+// MX8, the results' way out among them); a stage is
 // loaded D stages ahead, so that its latency hides behind the products, and its loads
 // go out one by one between them (all at a chunk's start they kept both waves of a SIMD
 // from their products: 41.2 instead of 38.5 us for 1024 tokens, MX4, 7168 x 5120).
@@ -13,9 +14,9 @@
 // for the one before it.  Scale bytes come a super-chunk (4 chunks) ahead, a part of
 // them with each stage.
 //
-// Measured, 7168 x 5120 (MX4 / MX6 / MX8): 4099 tokens 92 / 108 / 172 us = 3.3 / 2.8 / 1.7
+// Measured, 7168 x 5120 (MX4 / MX6 / MX8): 4099 tokens 93 / 110 / 172 us = 3.2 / 2.7 / 1.7
 // PFLOP/s of the result, the matrix instructions alone, in the same rounds, 68 us (MX4);
-// the gated block of 17408 features, 2053 tokens, MX8: 406 us.  What is between: 10 to
+// the gated block of 17408 features, 2053 tokens, MX8: 403 us.  What is between: 10 to
 // 20% for the stages' way into LDS, as much for the operands' way out of it, 6 us a tile
 // for its results, and the last round of tiles.
 

@@ -1,6 +1,8 @@
 // q8_mx_rows.hip -- microscaled blocks: quantisation of rows and weights, import
 // and export of MX4 weights, and the read-back of activation buffers.
-// Each is one pass and bound by memory: 7168 x 5120 to MX4 and back 65 us, 5.1 TB/s.
+// Each is one pass and bound by memory.  7168 x 5120 in an activation buffer: to MX4 and back 65 us, 5.1 TB/s.
+// Packed weights, whose rows lie side by side, so that a row's blocks are 256 bytes apart: quantised 44 us (3.8 TB/s;
+// the same rows into an activation buffer 37), imported 9.3 (4.2), exported 17.7 (2.2).
 
 #include <algorithm>
 
@@ -13,8 +15,8 @@ constexpr int kThreads = 256;
 
 typedef float v4f __attribute__((ext_vector_type(4)));
 
-// fp32 rows from the size of the L2s on go past them, read or written: 7168 x 5120 to MX4
-// and back 65 us, through them 74.
+// fp32 rows from the size of the L2s on go past them, read or written: 7168 x 5120 in an activation buffer to
+// MX4 and back 65 us, through them 74.
 constexpr int64_t kFar = 32 << 20;
 
 // 8 consecutive lanes a block, 4 values each.  total = rows x padded blocks x 8.
@@ -146,7 +148,9 @@ mx_read_kernel(MxView m, const int32_t* __restrict__ batch_index, int64_t total,
     }
 }
 
-// A launch holds fewer than 2^32 threads; a kernel with more to do goes round.
+// A launch holds fewer than 2^32 threads.  The quantiser goes round; the other kernels take an item a thread, of which
+// weights of 2^34 values have 2^29 (a block each) and 2^33 values that are read back 2^31 (4 each): what
+// this grid holds.
 inline unsigned grid_for(int64_t total) {
     return (unsigned)std::min<int64_t>((total + kThreads - 1) / kThreads, 1 << 23);
 }

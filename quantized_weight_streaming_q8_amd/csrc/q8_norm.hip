@@ -8,9 +8,11 @@
 // then falls to the same side as the definition's (to 2^-50), and the
 // double arithmetic hides behind the memory.
 //
-// Measured: 4099 rows of 5120 with a residual, a gate of each row's own and a layer norm 87
-// us, 4.8 TB/s of a copy's 5.0; 16 rows with both norms into MX8 7 us, one of 768 3.1: a
-// launch (1.7), the inputs' latency, and a sum over the workgroup for each norm.
+// Measured in a graph: 4099 rows of 5120 with a residual, a gate of each row's own and a layer norm 87
+// us, 4.8 TB/s of a copy's 5.0, with one norm into MX8 alone 76; one row of 768 3.1: a launch (1.7), the
+// inputs' latency, and a sum over the workgroup; 16 rows of 5120 with both norms into MX8 or q8_0 slots 8.2, into
+// fp32 rows 6.7: the same with three ways to memory one after the other (X, then the rest, then the second norm's
+// weights), two sums, and the maxima of the blocks.
 
 #include "q8_ffn_internal.h"
 
@@ -267,6 +269,8 @@ hipError_t launch_norm_step(const NormStep& s, hipStream_t st) {
         case 4: return launch<8, 4>(s, v, units, st);
         default: break;
     }
+    // 6 to 8 units a thread (rows above 20480 values) spill 8, 39 and 91 registers: 1024 rows of 20480 76 us (4.4
+    // TB/s), of 24576 94 (4.3), of 28672 141 (3.3), of 32768 188 (2.9).
     switch ((units + 1023) / 1024) {
         case 3: return launch<16, 3>(s, v, units, st);
         case 4: return launch<16, 4>(s, v, units, st);
